@@ -17,6 +17,12 @@ Entry points (same names as the C ABI in ``include/w4a4.h``):
 * ``w4a4_gemm(w, a)`` -> fp32 [M][N]
 * ``w4a4_gemm_partials(w, a)`` -> int32 [M][N][K/32]
 * ``w4a4_gemm_id(experts, E, a, ids, top_k, act_per_slot)`` -> fp32 [M][top_k][N]
+* ``mxfp4_rotate_quantize(x, rotate=True)`` -> :class:`MxFp4` (weights and activations)
+* ``mxfp4_gemm(w, a, dtype=torch.float32)`` -> fp32 or bf16 [M][N]
+* ``w4a4_/w4a8_rmsnorm_quantize_act``, ``mxfp4_rmsnorm_quantize``: residual + RMS norm in
+  front of the quantiser
+* ``w4a4_/w4a8_swiglu_quantize_act``, ``mxfp4_swiglu_quantize``: SwiGLU in front of it
+* ``mxfp4_dequantize``, ``w4a4_/w4a8_dequantize_act``: the values that codes stand for
 """
 from __future__ import annotations
 
@@ -35,6 +41,10 @@ __all__ = [
     "w4a4_gemm_id_workspace_bytes", "w4a4_gemm_id_static", "w4a4_check", "STATUS",
     "Act8", "w4a8_rotate_quantize_act", "w4a8_gemm", "w4a8_gemm_partials", "w4a8_gemm_workspace_bytes",
     "w4a4_gemm_small_m",
+    "MxFp4", "mxfp4_rotate_quantize", "mxfp4_import", "mxfp4_dequantize", "mxfp4_gemm",
+    "w4a4_dequantize_act", "w4a8_dequantize_act",
+    "w4a4_rmsnorm_quantize_act", "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize",
+    "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize",
 ]
 
 STATUS = {
@@ -46,6 +56,7 @@ TAG_Q4_0 = 0x51340000
 TAG_ACT4 = 0x41340000
 TAG_ACT8 = 0x41380000
 TAG_ACT16 = 0x41420000
+TAG_MXFP4 = 0x4D340000
 TAG_ROTATED = 0x1
 
 #: every symbol include/w4a4.h declares
@@ -58,6 +69,10 @@ EXPORTS = [
     "w4a8_rotate_quantize_act", "w4a8_gemm", "w4a8_gemm_partials", "w4a8_gemm_workspace_bytes",
     "w4a4_act16_values_bytes", "w4a16_rotate_act", "w4a16_gemm", "w4a16_gemm_workspace_bytes",
     "h32_q4_0_pack_weights_imatrix", "w4a4_debug_set_wait_limit",
+    "w4a4_mxfp4_codes_bytes", "w4a4_mxfp4_scales_bytes", "mxfp4_rotate_quantize", "mxfp4_import", "mxfp4_dequantize",
+    "w4a4_dequantize_act", "w4a8_dequantize_act", "mxfp4_gemm", "w4a4_rmsnorm_quantize_act",
+    "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize", "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act",
+    "mxfp4_swiglu_quantize",
 ]
 
 
@@ -82,6 +97,13 @@ class _Act4Desc(ctypes.Structure):
 class _Act16Desc(ctypes.Structure):
     _fields_ = [("values", ctypes.c_void_p), ("rows", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("tag", ctypes.c_uint32)]
+
+
+class _RmsNorm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("r", ctypes.c_void_p), ("r_out", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("ldr_out", ctypes.c_int64), ("x_dtype", ctypes.c_int), ("r_dtype", ctypes.c_int),
+                ("g_dtype", ctypes.c_int), ("rotate", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 _LIB = None
@@ -130,6 +152,18 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.w4a4_gemm_id_status.argtypes = [vp, vp]
     lib.w4a4_gemm_id_static.argtypes = [ctypes.POINTER(_Q4_0Desc), i32, i64, ctypes.POINTER(_Act4Desc), vp, i64, i32,
                                          i32, vp, vp]
+    for name in ("w4a4_mxfp4_codes_bytes", "w4a4_mxfp4_scales_bytes"):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [i64, i64], u
+    lib.mxfp4_rotate_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp]
+    lib.mxfp4_import.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    for name in ("mxfp4_dequantize", "w4a4_dequantize_act", "w4a8_dequantize_act"):
+        getattr(lib, name).argtypes = [vp, vp, i32, i64, vp]
+    lib.mxfp4_gemm.argtypes = [vp, vp, vp, i32, i64, vp]
+    for name in ("w4a4_rmsnorm_quantize_act", "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize"):
+        getattr(lib, name).argtypes = [vp, vp, vp]
+    for name in ("w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize"):
+        getattr(lib, name).argtypes = [vp, vp, i32, i64, i64, i64, i64, i32, vp, vp]
     lib.w4a4_check.argtypes = [vp]
     lib.w4a4_debug_set_wait_limit.argtypes = [ctypes.c_uint64, ctypes.c_uint64]
     lib.w4a4_debug_set_wait_limit.restype = None
@@ -151,8 +185,8 @@ def _check(status: int) -> None:
 
 
 def _stream(stream=None) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -516,9 +550,8 @@ def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
     lib = load_library()
     if K <= 0 or K % 32:
         raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-    nc, ns = lib.w4a4_act8_codes_bytes(rows, K), lib.w4a4_act8_scales_bytes(rows, K)
-    codes = torch.empty(max(nc, 16), dtype=torch.int8, device=device)[:nc].view(rows, K)
-    sbuf = torch.empty(max(ns, 16), dtype=torch.uint8, device=device)
+    codes = torch.empty(rows, K, dtype=torch.int8, device=device)
+    sbuf = torch.empty(max(lib.w4a4_act8_scales_bytes(rows, K), 16), dtype=torch.uint8, device=device)
     return Act8(codes, sbuf, rows, K, rotated)
 
 
@@ -631,3 +664,207 @@ def w4a16_gemm(w: Q4_0Weights, a: Act16, y: torch.Tensor | None = None, ws: torc
     _check(load_library().w4a16_gemm(ctypes.byref(w.desc()), ctypes.byref(a.desc()), y.data_ptr(), ldy, ws_ptr,
                                      ws_bytes, _stream(stream)))
     return y
+
+
+# ---------------------------------------------------------------- MXFP4 and the fused quantisers
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+@dataclass
+class MxFp4:
+    """MXFP4 weights or activations in the library's layout: e2m1 codes [rows][K/2] (element 2i in the low
+    nibble of byte i) and the scale bytes in tiles of 128 rows x 4 blocks."""
+    codes: torch.Tensor
+    scales_buf: torch.Tensor  # uint8 scale tiles, [ceil(rows/128)][ceil(K/128)][512]
+    rows: int
+    K: int
+    rotated: bool
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """The scale bytes in row-major order, uint8 [rows][K/32] (a copy)."""
+        rt, kt = (self.rows + 127) // 128, (self.K + 127) // 128
+        t = self.scales_buf[: rt * kt * 512].view(rt, kt, 32, 4, 4).permute(0, 3, 2, 1, 4)
+        return t.reshape(rt * 128, kt * 4)[: self.rows, : self.K // 32].contiguous()
+
+    @property
+    def tag(self) -> int:
+        return TAG_MXFP4 | (TAG_ROTATED if self.rotated else 0)
+
+    def desc(self) -> _Act4Desc:
+        return _Act4Desc(self.codes.data_ptr(), self.scales_buf.data_ptr(), self.rows, self.K, self.tag)
+
+
+def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
+    if K <= 0 or K % 32:
+        raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
+    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device)
+    sbuf = torch.empty((rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
+    return MxFp4(codes, sbuf, rows, K, rotated)
+
+
+def _rows(t: torch.Tensor, name: str, shape=None) -> int:
+    """Checks a 2-D CUDA operand (bf16 or fp32, unit stride along K) and returns its row stride."""
+    _cuda(t, name)
+    if t.dtype not in _DTYPE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D bf16 or fp32 tensor with unit stride along its rows")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row's stride is meaningless (may be 0)
+
+
+def _out(out, alloc, rows: int, K: int, device, rotate: bool):
+    if out is None:
+        return alloc(rows, K, device, rotate)
+    if out.rows != rows or out.K != K:
+        raise ValueError(f"out holds [{out.rows}][{out.K}], the result is [{rows}][{K}]")
+    return out
+
+
+def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | None = None, stream=None) -> MxFp4:
+    """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
+    ldx = _rows(x, "x")
+    rows, K = x.shape
+    out = _out(out, alloc_mxfp4, rows, K, x.device, rotate)
+    d = out.desc()
+    _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, int(rotate),
+                                                ctypes.addressof(d), _stream(stream)))
+    out.rotated = bool(rotate)
+    return out
+
+
+def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True, out: MxFp4 | None = None,
+                 stream=None) -> MxFp4:
+    """Take row-major MXFP4 (uint8 codes [rows][K/2] and scale bytes [rows][K/32], CUDA) bit for bit."""
+    _cuda(codes, "codes")
+    _cuda(scales, "scales")
+    if any(t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous() for t in (codes, scales)):
+        raise ValueError("codes and scales must be contiguous 2-D uint8 tensors")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if K <= 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
+        raise W4A4Error(1, "codes [rows][K/2] and scales [rows][K/32] disagree, or K is not a multiple of 32")
+    out = _out(out, alloc_mxfp4, rows, K, codes.device, rotated)
+    d = out.desc()
+    _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, int(rotated),
+                                       ctypes.addressof(d), _stream(stream)))
+    out.rotated = bool(rotated)
+    return out
+
+
+def _dequantize(fn: str, a, y, dtype, stream) -> torch.Tensor:
+    if y is None:
+        y = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device)
+    ldy = _rows(y, "y", (a.rows, a.K))
+    d = a.desc()
+    _check(getattr(load_library(), fn)(ctypes.addressof(d), y.data_ptr(), _DTYPE[y.dtype], ldy, _stream(stream)))
+    return y
+
+
+def mxfp4_dequantize(a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+                     stream=None) -> torch.Tensor:
+    """The values that MXFP4 codes and scales stand for ([rows][K], fp32 or bf16; a rotation is not undone)."""
+    return _dequantize("mxfp4_dequantize", a, y, dtype, stream)
+
+
+def w4a4_dequantize_act(a: Act4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+                        stream=None) -> torch.Tensor:
+    """The values that int4 codes and scales stand for, as mxfp4_dequantize."""
+    return _dequantize("w4a4_dequantize_act", a, y, dtype, stream)
+
+
+def w4a8_dequantize_act(a: Act8, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+                        stream=None) -> torch.Tensor:
+    """The values that int8 codes and scales stand for, as mxfp4_dequantize."""
+    return _dequantize("w4a8_dequantize_act", a, y, dtype, stream)
+
+
+def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+               stream=None) -> torch.Tensor:
+    """Y[m][n] = the product of MXFP4 weights w [N][K] and activations a [M][K], fp32 sums (fp32 or bf16 [M][N])."""
+    if y is None:
+        y = torch.empty(a.rows, w.rows, dtype=dtype, device=w.codes.device)
+    ldy = _rows(y, "y", (a.rows, w.rows))
+    dw, da = w.desc(), a.desc()
+    _check(load_library().mxfp4_gemm(ctypes.addressof(dw), ctypes.addressof(da), y.data_ptr(), _DTYPE[y.dtype], ldy,
+                                     _stream(stream)))
+    return y
+
+
+def _rmsnorm(fn: str, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
+    n = _RmsNorm(x=x.data_ptr(), ldx=_rows(x, "x"), x_dtype=_DTYPE.get(x.dtype, -1), M=x.shape[0], K=x.shape[1],
+                 rotate=int(rotate), eps=eps)
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        n.ldr, n.ldr_out = _rows(residual, "residual", x.shape), _rows(residual_out, "residual_out", x.shape)
+        if residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out must have residual's type")
+        n.r, n.r_out, n.r_dtype = residual.data_ptr(), residual_out.data_ptr(), _DTYPE[residual.dtype]
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if g is not None:
+        _cuda(g, "g")
+        if g.dtype not in _DTYPE or g.dim() != 1 or g.shape[0] != x.shape[1] or not g.is_contiguous():
+            raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
+        n.g, n.g_dtype = g.data_ptr(), _DTYPE[g.dtype]
+    out = _out(out, alloc, x.shape[0], x.shape[1], x.device, rotate)
+    d = out.desc()
+    _check(getattr(load_library(), fn)(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
+    out.rotated = bool(rotate)
+    return out
+
+
+def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
+                              residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                              rotate: bool = True, out: Act4 | None = None, stream=None) -> Act4:
+    """h = x + residual, y = h * rsqrt(mean h^2 + eps) * g, rotated and rounded to int4, in one pass.
+
+    x, residual: [M][K], bf16 or fp32 each.  h is written to residual_out, in place into
+    residual when that is None; without a residual, h = x and nothing is written.
+    """
+    return _rmsnorm("w4a4_rmsnorm_quantize_act", alloc_act4, x, g, residual, residual_out, eps, rotate, out, stream)
+
+
+def w4a8_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
+                              residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                              rotate: bool = True, out: Act8 | None = None, stream=None) -> Act8:
+    """As w4a4_rmsnorm_quantize_act, to int8 codes."""
+    return _rmsnorm("w4a8_rmsnorm_quantize_act", alloc_act8, x, g, residual, residual_out, eps, rotate, out, stream)
+
+
+def mxfp4_rmsnorm_quantize(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
+                           residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                           rotate: bool = True, out: MxFp4 | None = None, stream=None) -> MxFp4:
+    """As w4a4_rmsnorm_quantize_act, to MXFP4."""
+    return _rmsnorm("mxfp4_rmsnorm_quantize", alloc_mxfp4, x, g, residual, residual_out, eps, rotate, out, stream)
+
+
+def _swiglu(fn: str, alloc, gate, up, rotate, out, stream):
+    ldg, ldu = _rows(gate, "gate"), _rows(up, "up", gate.shape)
+    if up.dtype != gate.dtype:
+        raise ValueError("gate and up must have the same type")
+    M, K = gate.shape
+    out = _out(out, alloc, M, K, gate.device, rotate)
+    d = out.desc()
+    _check(getattr(load_library(), fn)(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, int(rotate),
+                                       ctypes.addressof(d), _stream(stream)))
+    out.rotated = bool(rotate)
+    return out
+
+
+def w4a4_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act4 | None = None,
+                             stream=None) -> Act4:
+    """y = silu(gate) * up (both [M][K], bf16 or fp32), rotated and rounded to int4, in one pass."""
+    return _swiglu("w4a4_swiglu_quantize_act", alloc_act4, gate, up, rotate, out, stream)
+
+
+def w4a8_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act8 | None = None,
+                             stream=None) -> Act8:
+    """As w4a4_swiglu_quantize_act, to int8 codes."""
+    return _swiglu("w4a8_swiglu_quantize_act", alloc_act8, gate, up, rotate, out, stream)
+
+
+def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: MxFp4 | None = None,
+                          stream=None) -> MxFp4:
+    """As w4a4_swiglu_quantize_act, to MXFP4."""
+    return _swiglu("mxfp4_swiglu_quantize", alloc_mxfp4, gate, up, rotate, out, stream)

@@ -118,6 +118,99 @@ w4a4_status check_pair(const w4a4_q4_0* w, const A* a, const char* fn) {
   return W4A4_OK;
 }
 
+w4a4_status check_mx(const w4a4_mxfp4* a, const char* fn) {
+  if (!a) return fail(W4A4_ERR_INVALID_ARG, "%s: MXFP4 descriptor is NULL", fn);
+  if ((a->tag & W4A4_TAG_MAGIC_MASK) != W4A4_TAG_MXFP4)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: descriptor tag 0x%08x is not an MXFP4 tag", fn, a->tag);
+  w4a4_status s = check_k_rows(a->rows, a->K, fn);
+  if (s != W4A4_OK) return s;
+  if (a->rows > 0 && (!a->codes || !a->scales)) return fail(W4A4_ERR_INVALID_ARG, "%s: MXFP4 pointers are NULL", fn);
+  if (!aligned16(a->codes) || !aligned16(a->scales))
+    return fail(W4A4_ERR_ALIGNMENT, "%s: MXFP4 codes/scales must be 16-byte aligned", fn);
+  return W4A4_OK;
+}
+
+// A 2D operand of K elements a row: dtype, row stride, pointer and row alignment.
+w4a4_status check_rows(const void* x, int dtype, int64_t M, int64_t K, int64_t ld, const char* what, const char* fn) {
+  if (dtype != W4A4_DTYPE_BF16 && dtype != W4A4_DTYPE_F32)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: %s dtype %d is neither bf16 (0) nor f32 (1)", fn, what, dtype);
+  if (ld < K) return fail(W4A4_ERR_INVALID_ARG, "%s: %s row stride %lld < K=%lld", fn, what, (long long)ld, (long long)K);
+  if (M > 0 && !x) return fail(W4A4_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
+  if (!aligned16(x) || (ld * (dtype == W4A4_DTYPE_BF16 ? 2 : 4)) % 16 != 0)
+    return fail(W4A4_ERR_ALIGNMENT, "%s: %s and its rows must be 16-byte aligned", fn, what);
+  return W4A4_OK;
+}
+
+// The output descriptor of a fused quantiser: pointers, then rows, K and tag.
+w4a4_status open_out(void* codes, void* scales, void* expanded, int64_t M, int64_t K, int rotate, const char* fn) {
+  w4a4_status s = check_k_rows(M, K, fn);
+  if (s != W4A4_OK) return s;
+  if (rotate != 0 && rotate != 1) return fail(W4A4_ERR_INVALID_ARG, "%s: rotate must be 0 or 1", fn);
+  if (M > 0 && (!codes || !scales)) return fail(W4A4_ERR_INVALID_ARG, "%s: output pointers are NULL", fn);
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(expanded))
+    return fail(W4A4_ERR_ALIGNMENT, "%s: output codes/scales/expanded must be 16-byte aligned", fn);
+  return W4A4_OK;
+}
+
+uint8_t* expanded_of(const w4a4_act4* o) { return o->expanded; }
+template <class O>
+uint8_t* expanded_of(const O*) { return nullptr; }
+
+template <class O>
+void stamp(O* out, uint32_t tag, int64_t M, int64_t K, int rotate) {
+  out->rows = M;
+  out->K = K;
+  out->tag = tag | (rotate ? W4A4_TAG_ROTATED : 0u);
+}
+
+// Rows, or silu(rows) * pair, to codes.
+template <class O>
+w4a4_status rows_to_codes(const char* fn, int fmt, uint32_t tag, const void* x, const void* pair, bool paired, int dtype,
+                          int64_t M, int64_t K, int64_t ldx, int64_t ldp, int rotate, O* out, w4a4_stream_t stream) {
+  if (!out) return fail(W4A4_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  w4a4_status s = open_out(out->codes, out->scales, expanded_of(out), M, K, rotate, fn);
+  if (s == W4A4_OK) s = check_rows(x, dtype, M, K, ldx, paired ? "gate" : "x", fn);
+  if (s == W4A4_OK && paired) s = check_rows(pair, dtype, M, K, ldp, "up", fn);
+  if (s != W4A4_OK) return s;
+  stamp(out, tag, M, K, rotate);
+  if (M == 0) return ok();
+  return cuda_status(w4a4::launch_rows_quantize(fmt, x, paired ? pair : nullptr, dtype == W4A4_DTYPE_BF16, M, K, ldx, ldp,
+                                                rotate, reinterpret_cast<uint8_t*>(out->codes), out->scales,
+                                                expanded_of(out), reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+template <class O>
+w4a4_status norm_to_codes(const char* fn, int fmt, uint32_t tag, const w4a4_rmsnorm* in, O* out, w4a4_stream_t stream) {
+  if (!in || !out) return fail(W4A4_ERR_INVALID_ARG, "%s: in or out is NULL", fn);
+  const int64_t M = in->M, K = in->K;
+  w4a4_status s = open_out(out->codes, out->scales, expanded_of(out), M, K, in->rotate, fn);
+  if (s == W4A4_OK) s = check_rows(in->x, in->x_dtype, M, K, in->ldx, "x", fn);
+  if (s == W4A4_OK && in->r) s = check_rows(in->r, in->r_dtype, M, K, in->ldr, "r", fn);
+  if (s == W4A4_OK && in->r) s = check_rows(in->r_out, in->r_dtype, M, K, in->ldr_out, "r_out", fn);
+  if (s == W4A4_OK && in->g) s = check_rows(in->g, in->g_dtype, 1, K, K, "g", fn);
+  if (s != W4A4_OK) return s;
+  if (!(in->eps >= 0.0f && in->eps <= 3.402823466e38f))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  if (K > w4a4::kNormMaxK)
+    return fail(W4A4_ERR_UNSUPPORTED, "%s: K=%lld; a row of at most %lld is normalised", fn, (long long)K,
+                (long long)w4a4::kNormMaxK);
+  stamp(out, tag, M, K, in->rotate);
+  if (M == 0) return ok();
+  const w4a4::NormArgs n{in->x, in->r, in->r_out, in->g, in->x_dtype == W4A4_DTYPE_BF16, in->r_dtype == W4A4_DTYPE_BF16,
+                         in->g_dtype == W4A4_DTYPE_BF16, in->rotate, M, K, in->ldx, in->ldr, in->ldr_out, in->eps};
+  return cuda_status(w4a4::launch_rmsnorm_quantize(fmt, n, reinterpret_cast<uint8_t*>(out->codes), out->scales,
+                                                   expanded_of(out), reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+w4a4_status read_back(const char* fn, int fmt, const void* codes, const void* scales, int64_t M, int64_t K, void* y,
+                      int y_dtype, int64_t ldy, w4a4_stream_t stream) {
+  const w4a4_status s = check_rows(y, y_dtype, M, K, ldy, "y", fn);
+  if (s != W4A4_OK) return s;
+  if (M == 0) return ok();
+  return cuda_status(w4a4::launch_dequantize(fmt, static_cast<const uint8_t*>(codes), scales, M, K, y,
+                                             y_dtype == W4A4_DTYPE_BF16, ldy, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -501,6 +594,104 @@ w4a4_status w4a4_gemm_id_static(const w4a4_q4_0* experts, int E, int64_t N, cons
                                           a->K, ids, M, top_k, act_per_slot, y, r,
                                           reinterpret_cast<cudaStream_t>(stream)),
                      fn);
+}
+
+size_t w4a4_mxfp4_codes_bytes(int64_t rows, int64_t K) { return w4a4_q4_0_codes_bytes(rows, K); }
+size_t w4a4_mxfp4_scales_bytes(int64_t rows, int64_t K) {
+  if (!valid_k(K) || rows < 0) return 0;
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((K + 127) / 128) * 512;
+}
+
+w4a4_status mxfp4_rotate_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int64_t ldx, int rotate,
+                                  w4a4_mxfp4* out, w4a4_stream_t stream) {
+  return rows_to_codes("mxfp4_rotate_quantize", 32, W4A4_TAG_MXFP4, x, nullptr, false, x_dtype, rows, K, ldx, 0, rotate,
+                       out, stream);
+}
+
+w4a4_status mxfp4_import(const void* codes, const void* scales, int64_t rows, int64_t K, int rotated, w4a4_mxfp4* out,
+                         w4a4_stream_t stream) {
+  const char* fn = "mxfp4_import";
+  if (!out) return fail(W4A4_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  const w4a4_status s = open_out(out->codes, out->scales, nullptr, rows, K, rotated, fn);
+  if (s != W4A4_OK) return s;
+  if (rows > 0 && (!codes || !scales)) return fail(W4A4_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!aligned16(codes)) return fail(W4A4_ERR_ALIGNMENT, "%s: codes must be 16-byte aligned", fn);
+  stamp(out, W4A4_TAG_MXFP4, rows, K, rotated);
+  if (rows == 0) return ok();
+  return cuda_status(w4a4::launch_import_mx(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows,
+                                            K, out->codes, out->scales, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+w4a4_status mxfp4_dequantize(const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream) {
+  const char* fn = "mxfp4_dequantize";
+  const w4a4_status s = check_mx(a, fn);
+  if (s != W4A4_OK) return s;
+  return read_back(fn, 32, a->codes, a->scales, a->rows, a->K, y, y_dtype, ldy, stream);
+}
+
+w4a4_status w4a4_dequantize_act(const w4a4_act4* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream) {
+  const char* fn = "w4a4_dequantize_act";
+  const w4a4_status s = check_act4(a, fn);
+  if (s != W4A4_OK) return s;
+  return read_back(fn, 4, a->codes, a->scales, a->rows, a->K, y, y_dtype, ldy, stream);
+}
+
+w4a4_status w4a8_dequantize_act(const w4a4_act8* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream) {
+  const char* fn = "w4a8_dequantize_act";
+  const w4a4_status s = check_act8(a, fn);
+  if (s != W4A4_OK) return s;
+  return read_back(fn, 8, a->codes, a->scales, a->rows, a->K, y, y_dtype, ldy, stream);
+}
+
+w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy,
+                       w4a4_stream_t stream) {
+  const char* fn = "mxfp4_gemm";
+  w4a4_status s = check_mx(w, fn);
+  if (s != W4A4_OK) return s;
+  if ((s = check_mx(a, fn)) != W4A4_OK) return s;
+  if (w->K != a->K)
+    return fail(W4A4_ERR_MISMATCH, "%s: weights have K=%lld, activations K=%lld", fn, (long long)w->K, (long long)a->K);
+  if ((w->tag & W4A4_TAG_ROTATED) != (a->tag & W4A4_TAG_ROTATED))
+    return fail(W4A4_ERR_MISMATCH, "%s: one operand is H32-rotated, the other is not; refusing a product that would be "
+                "silently wrong", fn);
+  const int64_t M = a->rows, N = w->rows;
+  if (y_dtype != W4A4_DTYPE_BF16 && y_dtype != W4A4_DTYPE_F32)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: y dtype %d is neither bf16 (0) nor f32 (1)", fn, y_dtype);
+  if (ldy < N) return fail(W4A4_ERR_INVALID_ARG, "%s: ldy=%lld < N=%lld", fn, (long long)ldy, (long long)N);
+  if (M == 0 || N == 0) return ok();
+  if (!y) return fail(W4A4_ERR_INVALID_ARG, "%s: y is NULL", fn);
+  if ((reinterpret_cast<uintptr_t>(y) & (y_dtype == W4A4_DTYPE_BF16 ? 1u : 3u)) != 0)
+    return fail(W4A4_ERR_ALIGNMENT, "%s: y must be aligned to its element", fn);
+  if (N > w4a4::kMxMaxRows || M > w4a4::kMxMaxRows)
+    return fail(W4A4_ERR_UNSUPPORTED, "%s: at most %lld rows an operand", fn, (long long)w4a4::kMxMaxRows);
+  return cuda_status(w4a4::launch_mx_gemm(w->codes, w->scales, N, a->codes, a->scales, M, a->K, y,
+                                          y_dtype == W4A4_DTYPE_BF16, ldy, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+w4a4_status w4a4_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act4* out, w4a4_stream_t stream) {
+  return norm_to_codes("w4a4_rmsnorm_quantize_act", 4, W4A4_TAG_ACT4, in, out, stream);
+}
+w4a4_status w4a8_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act8* out, w4a4_stream_t stream) {
+  return norm_to_codes("w4a8_rmsnorm_quantize_act", 8, W4A4_TAG_ACT8, in, out, stream);
+}
+w4a4_status mxfp4_rmsnorm_quantize(const w4a4_rmsnorm* in, w4a4_mxfp4* out, w4a4_stream_t stream) {
+  return norm_to_codes("mxfp4_rmsnorm_quantize", 32, W4A4_TAG_MXFP4, in, out, stream);
+}
+
+w4a4_status w4a4_swiglu_quantize_act(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                     int64_t ldu, int rotate, w4a4_act4* out, w4a4_stream_t stream) {
+  return rows_to_codes("w4a4_swiglu_quantize_act", 4, W4A4_TAG_ACT4, gate, up, true, dtype, M, K, ldg, ldu, rotate, out,
+                       stream);
+}
+w4a4_status w4a8_swiglu_quantize_act(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                     int64_t ldu, int rotate, w4a4_act8* out, w4a4_stream_t stream) {
+  return rows_to_codes("w4a8_swiglu_quantize_act", 8, W4A4_TAG_ACT8, gate, up, true, dtype, M, K, ldg, ldu, rotate, out,
+                       stream);
+}
+w4a4_status mxfp4_swiglu_quantize(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                  int64_t ldu, int rotate, w4a4_mxfp4* out, w4a4_stream_t stream) {
+  return rows_to_codes("mxfp4_swiglu_quantize", 32, W4A4_TAG_MXFP4, gate, up, true, dtype, M, K, ldg, ldu, rotate, out,
+                       stream);
 }
 
 w4a4_status w4a4_check(w4a4_stream_t stream) {

@@ -1,0 +1,174 @@
+// A 32-element block held by four neighbouring lanes, eight consecutive elements
+// each (lane q = lane & 3 holds elements 8q .. 8q + 7): the H32 rotation, the
+// block maximum and the three code formats.  Chunk c = 8 elements is the unit the
+// fused quantisers index by; it is 16 bytes of bf16 or 32 of fp32, so a warp's
+// loads and stores of consecutive chunks are contiguous without a transposition.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "w4a4_device.cuh"
+#include "w4a4_kernels.cuh"
+
+namespace w4a4 {
+
+// ---------------------------------------------------------------- loads and stores of a chunk
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void unpack_bf16(const uint4& a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the high half of the fp32 of the same value
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  unpack_bf16(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // round to nearest even
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    memcpy(&w[i], &h, 4);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------- rotation
+// The normalised 32-point Walsh-Hadamard transform, stages h = 1, 2, 4 inside the
+// lane, 8 and 16 across lanes: each pair becomes (a + b, a - b) with the fp32 adds
+// of the one-lane form (a fused multiply by +-1 rounds like the add), then one
+// multiply by fl32(1/sqrt 32).  All 32 lanes must call it.
+__device__ __forceinline__ void quad_rotate(float (&v)[8], int q) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1) {
+    const float s = (q & h) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(v[i], s, __shfl_xor_sync(0xFFFFFFFFu, v[i], h));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], c_h32());
+}
+
+// max |v| over the block's four lanes; NaN if any element is NaN.
+__device__ __forceinline__ float max_nan2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float quad_amax(const float (&v)[8]) {
+  float a = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = max_nan2(a, fabsf(v[i]));
+  a = max_nan2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+  return max_nan2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+}
+
+// ---------------------------------------------------------------- code formats
+enum Fmt : int { kInt4 = 4, kInt8 = 8, kMx = 32 };
+
+// Where a fused quantiser writes its codes.
+struct QuantOut {
+  uint8_t* codes;
+  void* scales;       // fp32 [rows][K/32] (int4, int8) or scale tiles of bytes (MXFP4)
+  uint8_t* expanded;  // int4 only, may be null: the offset codes a + 8 as bytes
+  int64_t ktiles;     // MXFP4: scale tiles along K, ceil(K / 128)
+};
+
+// Byte of the scale of (row, block) in the MXFP4 scale tiles: 512-byte tiles of 128
+// rows x 4 blocks, in the order the tensor core's scale copy reads them (row r of
+// the tile at 16 * (r % 32) + 4 * (r / 32), its four blocks in a row).
+__host__ __device__ __forceinline__ int64_t mx_scale_at(int64_t row, int64_t blk, int64_t ktiles) {
+  return ((row >> 7) * ktiles + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
+}
+
+// Two values to a byte of e2m1 codes (lo in the low nibble): round to nearest, ties
+// to even, saturating at +-6.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n.reg .b8 a, b, c, d;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\ncvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\ncvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      "mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// Quantise this lane's eight values of a block and store them if ok.
+//   kInt4: d = amax / 7, codes round-half-away(v * fl(1/d)) clamped to -8..7, nibbles
+//          in the Q4_0 order (element i low, i + 16 high);
+//   kInt8: d = amax / 127, codes clamped to -127..127, element order;
+//   kMx:   scale 2^E, E = clamp(floor(log2 amax) - 2, -127, 127) stored as E + 127,
+//          codes e2m1(v * 2^-E), element 2i in the low nibble of byte i.
+// A block with an infinity or a NaN gets a NaN scale and zero codes, so it reads
+// back, and multiplies, as NaN.  c is the chunk's flat index row * K / 8 + col.
+template <int FMT>
+__device__ __forceinline__ void quad_quantize(float (&v)[8], int q, bool ok, int64_t c, int64_t row, int64_t blk,
+                                              int64_t nblk_row, const QuantOut& o) {
+  const float a = quad_amax(v);
+  const bool bad = !(a <= 3.402823466e38f);
+  if constexpr (FMT == kMx) {
+    // floor(log2 a) from the exponent field; a subnormal a ends at the clamp
+    const int e = max(static_cast<int>(__float_as_uint(a) >> 23) - 127 - 2, -127);
+    // 2^-E, e in -127 .. 125: its exponent field is 127 - e, in 2 .. 254
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bad ? 0.0f : __fmul_rn(v[i], inv);
+    const uint32_t w = e2m1x8(v);
+    if (ok) {
+      reinterpret_cast<uint32_t*>(o.codes)[c] = w;
+      if (q == 0) {
+        uint8_t* s = static_cast<uint8_t*>(o.scales) + mx_scale_at(row, blk, o.ktiles);
+        *s = bad ? 255 : static_cast<uint8_t>(e + 127);
+        if (blk == nblk_row - 1)  // the tile's unused blocks multiply zero codes: any finite scale
+          for (int64_t p = 1; p < 4 - (blk & 3); ++p) s[p] = 0;
+      }
+    }
+  } else {
+    constexpr float kTop = FMT == kInt4 ? 7.0f : 127.0f;
+    constexpr float kLow = FMT == kInt4 ? -8.0f : -127.0f;
+    const float d = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(a, kTop);
+    const float inv = (d != 0.0f) ? __frcp_rn(d) : 0.0f;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = fminf(fmaxf(round_half_away(__fmul_rn(v[i], inv)), kLow), kTop);
+      w[i >> 2] |= (bad ? 0u : (static_cast<uint32_t>(static_cast<int>(r)) & (FMT == kInt4 ? 0xFu : 0xFFu)))
+                   << (8 * (i & 3));
+    }
+    if (ok && q == 0) static_cast<float*>(o.scales)[c >> 2] = d;
+    if constexpr (FMT == kInt8) {
+      if (ok) reinterpret_cast<uint2*>(o.codes)[c] = make_uint2(w[0], w[1]);
+    } else {
+      // lane q pairs with lane q + 2, which holds the elements 16 further on
+      const uint32_t h0 = __shfl_down_sync(0xFFFFFFFFu, w[0], 2), h1 = __shfl_down_sync(0xFFFFFFFFu, w[1], 2);
+      if (ok) {
+        if (q < 2)
+          *reinterpret_cast<uint2*>(o.codes + (c >> 2) * 16 + q * 8) = make_uint2(w[0] | (h0 << 4), w[1] | (h1 << 4));
+        if (o.expanded)  // a + 8 = nibble ^ 8
+          reinterpret_cast<uint2*>(o.expanded)[c] = make_uint2(w[0] ^ 0x08080808u, w[1] ^ 0x08080808u);
+      }
+    }
+  }
+}
+
+}  // namespace w4a4

@@ -116,4 +116,33 @@ cudaError_t launch_gemm_id(const uint8_t* w_codes, const uint16_t* w_scales, con
                            int64_t N, const uint8_t* a_codes, const float* a_scales, int64_t K, const int32_t* ids,
                            int64_t M, int top_k, int act_per_slot, float* y, const Routing& r, cudaStream_t stream);
 
+// Fused quantisers (fused_quant.cu).  fmt: 4 = int4, 8 = int8, 32 = MXFP4 (codes,
+// scales and, for int4, the optional expanded operand).  x2 != null: rows silu(x) * x2.
+cudaError_t launch_rows_quantize(int fmt, const void* x, const void* x2, int bf16, int64_t M, int64_t K, int64_t ldx,
+                                 int64_t ldx2, int rotate, uint8_t* codes, void* scales, uint8_t* expanded,
+                                 cudaStream_t st);
+// Residual addition and RMS norm in front of the quantiser; r (with r_out) and g may be null.
+struct NormArgs {
+  const void* x;
+  const void* r;
+  void* r_out;
+  const void* g;
+  int x_bf16, r_bf16, g_bf16, rotate;
+  int64_t M, K, ldx, ldr, ldr_out;
+  float eps;
+};
+constexpr int64_t kNormMaxK = 65536;  // 1024 threads of 8 chunks of 8 values
+cudaError_t launch_rmsnorm_quantize(int fmt, const NormArgs& n, uint8_t* codes, void* scales, uint8_t* expanded,
+                                    cudaStream_t st);
+cudaError_t launch_dequantize(int fmt, const uint8_t* codes, const void* scales, int64_t M, int64_t K, void* y,
+                              int y_bf16, int64_t ldy, cudaStream_t st);
+// Row-major MXFP4 (codes [rows][K/2], scale bytes [rows][K/32]) into the library layout.
+cudaError_t launch_import_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, uint8_t* out,
+                             uint8_t* out_scales, cudaStream_t st);
+// The MXFP4 product (mx_gemm.cu).
+constexpr int64_t kMxMaxRows = 65535 * 128;  // rows of an operand: a tile of 128 or more per grid index
+cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
+                           const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy,
+                           cudaStream_t stream);
+
 }  // namespace w4a4

@@ -69,10 +69,12 @@ typedef enum {
 #define W4A4_TAG_ACT4 0x41340000u    /* int4 activations                      */
 #define W4A4_TAG_ACT8 0x41380000u    /* int8 activations (the exact path)     */
 #define W4A4_TAG_ACT16 0x41420000u   /* bf16 activations (rotate-only route)  */
+#define W4A4_TAG_MXFP4 0x4D340000u   /* MXFP4 weights or activations          */
 #define W4A4_TAG_MAGIC_MASK 0xFFFF0000u
 #define W4A4_TAG_ROTATED 0x00000001u /* values were rotated by H32 per block  */
 
-/* Weight input element types for h32_q4_0_pack_weights. */
+/* Element types: weight inputs of h32_q4_0_pack_weights, inputs and outputs of the
+ * MXFP4 operators and of the fused quantisers. */
 #define W4A4_DTYPE_BF16 0
 #define W4A4_DTYPE_F32 1
 
@@ -419,6 +421,120 @@ w4a4_status w4a4_gemm_id_status(const void* ws, w4a4_stream_t stream);
 w4a4_status w4a4_gemm_id_static(const w4a4_q4_0* experts, int E, int64_t N, const w4a4_act4* a,
                                 const int32_t* ids, int64_t M, int top_k, int act_per_slot, float* y,
                                 w4a4_stream_t stream);
+
+/*
+ * MXFP4: microscaled 4-bit floating point, for weights and activations alike.  One
+ * scale per 32 elements along K, a power of two 2^(s - 127) stored as the byte s
+ * (255 = NaN), and 4-bit e2m1 codes (sign, two exponent bits, one mantissa bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6).  The tensor cores multiply it with its scales, so the
+ * product has no per-block fold.  The optional H32 rotation in front of it is the
+ * one of the int4 formats, and the rotation tags guard it in the same way.
+ *   codes : device, [rows][K/2]; byte i of a row holds element 2i in its low nibble
+ *           and element 2i + 1 in its high nibble (w4a4_mxfp4_codes_bytes).
+ *   scales: device, tiles of 512 bytes, [ceil(rows/128)][ceil(K/128)] of them, each
+ *           128 rows x 4 blocks: the scale of block b of row r is byte
+ *           16 (r % 32) + 4 (r / 32 % 4) + b % 4 of tile (r / 128, b / 4), the order
+ *           the tensor core reads (w4a4_mxfp4_scales_bytes).  Blocks past K/32 in a
+ *           row's last tile are zero; rows past the last are never read into a result.
+ */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows;
+  int64_t K;
+  uint32_t tag; /* W4A4_TAG_MXFP4 | (W4A4_TAG_ROTATED if rotated) */
+} w4a4_mxfp4;
+
+size_t w4a4_mxfp4_codes_bytes(int64_t rows, int64_t K);
+size_t w4a4_mxfp4_scales_bytes(int64_t rows, int64_t K);
+
+/*
+ * mxfp4_rotate_quantize -- rotate rows per 32-block along K (rotate = 1) and round
+ * them to MXFP4.  For weights once per model, for activations each call.
+ *   x    : device, [rows][ldx] elements of type x_dtype.
+ *   out  : host struct; out->codes and out->scales point to caller buffers; rows,
+ *          K and tag are written.
+ * Per block: y as for the int4 formats; a = max |y|; E = clamp(floor(log2 a) - 2,
+ * -127, 127) (a = 0: -127); scale byte E + 127; code = the e2m1 value nearest to
+ * y * 2^-E, ties to the even code, values past 6 to 6.  A block with an infinity or
+ * a NaN gets scale byte 255 and zero codes: it reads back, and multiplies, as NaN.
+ */
+w4a4_status mxfp4_rotate_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int64_t ldx, int rotate,
+                                  w4a4_mxfp4* out, w4a4_stream_t stream);
+
+/*
+ * mxfp4_import -- take row-major MXFP4 (codes [rows][K/2] in the nibble order above,
+ * scale bytes [rows][K/32]; device; codes 16-byte aligned) into the layout above, bit
+ * for bit.  rotated: 1 if the values were rotated by H32.
+ */
+w4a4_status mxfp4_import(const void* codes, const void* scales, int64_t rows, int64_t K, int rotated, w4a4_mxfp4* out,
+                         w4a4_stream_t stream);
+
+/*
+ * Reading back -- y[r][k] = the value that code (r, k) and its scale stand for, as
+ * fp32 or bf16 (y_dtype; rounded to nearest even), in the domain of the codes: the
+ * rotation, if there was one, is not undone.  y: device, [rows][ldy], 16-byte
+ * aligned with its rows.
+ */
+w4a4_status mxfp4_dequantize(const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream);
+w4a4_status w4a4_dequantize_act(const w4a4_act4* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream);
+w4a4_status w4a8_dequantize_act(const w4a4_act8* a, void* y, int y_dtype, int64_t ldy, w4a4_stream_t stream);
+
+/*
+ * mxfp4_gemm -- Y[m][n] = sum_b 2^(s_w + s_a - 254) sum_j w_j a_j, the MXFP4 product
+ * with fp32 sums, for one token to many.
+ *   w : rows = N.   a : rows = M.
+ *   y : device, [M][ldy] fp32 or bf16 (y_dtype; bf16 is rounded once, at the end),
+ *       ldy >= N, aligned to its element.
+ * w->K must equal a->K and the rotation tags must agree (W4A4_ERR_MISMATCH).  No
+ * workspace; the order of every sum is fixed, so equal inputs give equal bits.
+ */
+w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy,
+                       w4a4_stream_t stream);
+
+/*
+ * Residual addition + RMS norm + rotation + quantisation, in one pass: what stands
+ * in front of a projection.
+ *   h = x + r (fp32);  r_out = h (rounded to r's type);
+ *   y = h * rsqrt(mean_k h^2 + eps) * g (fp32, the unrounded h), then the rotation and
+ *   the codes as in w4a4_rotate_quantize_act (int4), w4a8_rotate_quantize_act (int8)
+ *   or mxfp4_rotate_quantize.
+ *   x, r : device, [M][ldx], [M][ldr]; r NULL: no residual (r_out is not written).
+ *   r_out: device, [M][ldr_out] of r's type; r itself for an update in place, no
+ *          other overlap with an input.
+ *   g    : device, K gains, or NULL for none.
+ *   eps  : finite, >= 0.
+ * K <= 65536 (W4A4_ERR_UNSUPPORTED above).  A NaN in a row makes the row read back as
+ * NaN; so does a row of zeros with eps = 0 (0 * infinity).  An infinity, or squares
+ * that overflow fp32, make the norm infinite: finite values become 0, the blocks
+ * (int4, int8, MXFP4) that hold an infinity read back as NaN.
+ */
+typedef struct {
+  const void* x;
+  const void* r;
+  void* r_out;
+  const void* g;
+  int64_t M, K, ldx, ldr, ldr_out;
+  int x_dtype, r_dtype, g_dtype; /* W4A4_DTYPE_BF16 or W4A4_DTYPE_F32 */
+  int rotate;
+  float eps;
+} w4a4_rmsnorm;
+w4a4_status w4a4_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act4* out, w4a4_stream_t stream);
+w4a4_status w4a8_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act8* out, w4a4_stream_t stream);
+w4a4_status mxfp4_rmsnorm_quantize(const w4a4_rmsnorm* in, w4a4_mxfp4* out, w4a4_stream_t stream);
+
+/*
+ * SwiGLU + rotation + quantisation: y = gate / (1 + exp(-gate)) * up (fp32), then the
+ * rotation and the codes as above: what stands in front of a down projection.
+ *   gate, up: device, [M][ldg], [M][ldu] of type dtype (the halves of one product's
+ *             output, for instance).
+ */
+w4a4_status w4a4_swiglu_quantize_act(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                     int64_t ldu, int rotate, w4a4_act4* out, w4a4_stream_t stream);
+w4a4_status w4a8_swiglu_quantize_act(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                     int64_t ldu, int rotate, w4a4_act8* out, w4a4_stream_t stream);
+w4a4_status mxfp4_swiglu_quantize(const void* gate, const void* up, int dtype, int64_t M, int64_t K, int64_t ldg,
+                                  int64_t ldu, int rotate, w4a4_mxfp4* out, w4a4_stream_t stream);
 
 /*
  * w4a4_check -- synchronise `stream`, then report whether any GEMM kernel run

@@ -51,6 +51,11 @@ weighted``                     than the plain scale; 2^k weight invariance
 ``w4a16_matmul``               brute-force fp64 loops; Q4_0-exact weights and
                                bf16 activations reduce it to x @ w^T; constant
                                blocks: 32 d_w alpha (q - 8)
+``e2m1_code``                  every midpoint and neighbour by hand; nearest by
+                               brute force
+``quantize_mxfp4`` /           powers of two, zero, subnormal and non-finite
+``mxfp4_values``               blocks by hand; round trip of every code
+``mxfp4_matmul``               brute-force loops in exact fractions
 =============================  ==============================================
 
 Every function above is pinned; none is "parity unpinned".  The informative
@@ -81,6 +86,7 @@ from .quant import (
     pack_weights_imatrix,
     effective_importance,
 )
+from .mxfp4 import E2M1, e2m1_code, quantize_mxfp4, mxfp4_values, mxfp4_matmul
 from .matmul import block_partials, w4a4_matmul, w4a4_matmul_id, w4a8_matmul, w4a16_matmul, exact_matmul
 
 __all__ = [
@@ -92,5 +98,6 @@ __all__ = [
     "round_bf16", "bf16_to_f32", "rotate_activations_bf16",
     "rotate_importance", "weighted_block_scale", "quantize_weights_q4_0_weighted", "pack_weights_imatrix",
     "effective_importance",
+    "E2M1", "e2m1_code", "quantize_mxfp4", "mxfp4_values", "mxfp4_matmul",
     "block_partials", "w4a4_matmul", "w4a4_matmul_id", "w4a8_matmul", "w4a16_matmul", "exact_matmul",
 ]
