@@ -3,15 +3,23 @@
 // of each operand): the tensor core applies the scales itself, so nothing is folded
 // on the CUDA cores.
 //
-// The weights are the MMA's M operand (128 rows a tile) and the tokens its N operand
-// (NT a tile): one token costs no more tensor work than 16, a warp's lanes hold
-// consecutive outputs n, and every store of Y is contiguous.  Stages of 256 elements
-// of K (128 bytes a row, 128-byte swizzle) and their scale tiles come by TMA; the
-// scale tiles go on to TMEM (tcgen05.cp) in front of the MMAs that use them.
+// The weights are the MMA's M operand and the tokens its N operand: one token costs
+// no more tensor work than 16, a warp's lanes hold consecutive outputs n, and every
+// store of Y is contiguous.  Stages of 256 elements of K (128 bytes a row, 128-byte
+// swizzle) and their scale tiles come by TMA; the scale tiles go on to TMEM
+// (tcgen05.cp) in front of the MMAs that use them.
 //
-// A cluster of S CTAs may share one tile, each with a contiguous share of K: the S
-// partial tiles are exchanged through distributed shared memory and summed in rank
-// order, so the result does not depend on timing and no workspace is needed.
+// Two kernels:
+//   small (M <= 128): a CTA multiplies 128 weight rows by all the tokens; a cluster of
+//     S CTAs shares a tile, each with a contiguous share of K, so that few tiles still
+//     stream the weights through every SM.  The S partial tiles meet in distributed
+//     shared memory and are summed in rank order: no workspace, no dependence on
+//     timing.
+//   pair (M > 128): persistent CTA pairs (cta_group::2) multiply 256 weight rows by up
+//     to 256 tokens.  Each CTA stages half of both operands, which is what lets shared
+//     memory (written once, read once per MMA, 128 bytes a cycle) keep up with the
+//     tensor core.  The accumulators leave TMEM for registers at once, and their stores
+//     overlap the next tile's MMAs.
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"
@@ -21,35 +29,25 @@ namespace w4a4 {
 
 namespace {
 
-constexpr int kTW = 128;       // weight rows per tile
-constexpr int kStageK = 256;   // elements of K per stage
-constexpr int kThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
+constexpr int kTW = 128;      // weight rows per CTA
+constexpr int kStageK = 256;  // elements of K per stage
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kWBytes = kTW * 128;
+constexpr int kSfTile = 1024;  // a stage's scales of 128 rows: two 512-byte tiles
 
 struct MxArgs {
-  const uint8_t* w_scales;
-  const uint8_t* a_scales;
   void* y;
   int64_t ldy;
   int64_t M, N;
-  int K, ktiles, stages, y_bf16;
+  int K, stages;
+  int mt;       // token tiles (of kMaxTok, the last one narrower)
+  int box;      // token rows of one load
+  int64_t tiles;
   int* err;
 };
 
-template <int NT>
-struct Cfg {
-  static constexpr int kAtoms = NT > 128 ? 2 : 1;  // 128-row scale tiles a token tile touches
-  static constexpr int kWBytes = kTW * 128, kABytes = NT * 128;
-  static constexpr int kSfW = 1024, kSfA = kAtoms * 1024;
-  static constexpr int kStageBytes = kWBytes + kABytes + kSfW + kSfA;
-  static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : 8;
-  static constexpr int kSfCols = 8 + 8 * kAtoms;  // TMEM columns of one stage's scales
-  static constexpr int kCols = NT + kSfCols * kStages <= 128 ? 128 : NT + kSfCols * kStages <= 256 ? 256 : 512;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes;
-};
-
 struct Bars {
-  uint64_t full[8], empty[8], done;
+  uint64_t full[8], empty[8], acc_full, acc_empty;
   uint32_t tmem;
   volatile int abort;
 };
@@ -75,207 +73,508 @@ __device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
   }
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)),
-               "l"(src), "r"(bytes), "r"(su32(bar))
-               : "memory");
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
-// 512-byte scale tile (32 rows x 16 bytes, no swizzle) to 4 TMEM columns of all four
-// lane quarters.
-__device__ __forceinline__ void sf_copy(uint32_t taddr, const void* smem) {
-  const uint64_t d = static_cast<uint64_t>((su32(smem) >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-                     (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// One lane of the converged warp; the compiler knows that a single thread runs what
+// it guards (a lane test instead costs about 100 cycles per copy or MMA issued).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
-
-// kind::mxf4 instruction descriptor: A and B e2m1 (code 1), K-major, ue8m0 scales,
-// K = 64; sf picks the byte pair of the scale words.
-__device__ __forceinline__ uint32_t mx_idesc(int n, uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(kTW >> 4) << 24) | (sf << 29);
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-      : "memory");
-}
-
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t local, uint32_t rank, float v) {
+__device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+  return a;
 }
 
-__device__ __forceinline__ void put(const MxArgs& p, int64_t m, int64_t n, float v) {
-  if (p.y_bf16)
-    static_cast<__nv_bfloat16*>(p.y)[m * p.ldy + n] = __float2bfloat16_rn(v);
+// ---------------------------------------------------------------- tcgen05, both group sizes
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(dst)), "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(dst)), "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
   else
-    static_cast<float*>(p.y)[m * p.ldy + n] = v;
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+}
+// 512-byte scale tile (32 rows x 16 bytes, no swizzle) to 4 TMEM columns of all four
+// lane quarters; in a pair, each CTA's own tile to its own TMEM.
+template <int CG>
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t smem) {
+  const uint64_t d = static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+                     (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+// kind::mxf4 instruction descriptor: A and B e2m1 (code 1), K-major, ue8m0 scales,
+// K = 64, 128 rows of A per CTA; mx_sf(2) picks the second byte pair of the scale words.
+__device__ __forceinline__ uint32_t mx_idesc(int cg, int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(cg * kTW >> 4) << 24);
+}
+constexpr uint32_t kSfHigh = (2u << 4) | (2u << 29);
+template <int CG>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t acc) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+// Arrival, when every MMA issued so far is done, on a barrier of this CTA, or on the
+// same barrier of both CTAs of the pair.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            su32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
-// grid (S, weight tiles, token tiles), cluster (S, 1, 1).
+// One stage's MMAs: `steps` of K = 64 (four but for the end of K), behind the scale
+// tiles they use.  sfw: TMEM column of the weights' scales, the tokens' follow; a scale
+// operand has to start on a scale tile's first column, so token tiles start at multiples
+// of 128 rows.  kAtoms: token scale tiles per 128 of K.
+template <int CG, int kAtoms>
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t wsm, uint32_t asm_, uint32_t sfsm, uint32_t sfw,
+                                           uint32_t idesc, int steps, uint32_t& acc) {
+  const uint32_t sfa = sfw + 8;
+  const uint64_t base = (static_cast<uint64_t>(1) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+                        (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);  // as kmajor_desc_sw128
+  const uint64_t wd = base | ((wsm >> 4) & 0x3FFFu), ad = base | ((asm_ >> 4) & 0x3FFFu);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (2 * j < steps) {
+      sf_copy<CG>(sfw + 4 * j, sfsm + 512 * j);
+#pragma unroll
+      for (int t = 0; t < kAtoms; ++t)
+        sf_copy<CG>(sfa + 4 * (j * kAtoms + t), sfsm + kSfTile + t * kSfTile + 512 * j);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < steps) {
+      mma_mx<CG>(d, wd + 2 * k, ad + 2 * k, (k & 1) ? idesc | kSfHigh : idesc, sfw + 4 * (k >> 1),
+                 sfa + 4 * (k >> 1) * kAtoms, acc);
+      acc = 1;
+    }
+  }
+}
+
+// TMA load of a tile, its bytes counted on `bar`: this CTA's, or (pair) the leader's.
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- stores of Y
+// Tokens 0 .. lim - 1 of this lane's weight row n from NC accumulators (r[i] = token
+// i); y points at token 0.  bf16: neighbouring lanes trade so that the even lane
+// stores the pair (n, n + 1) of token i and the odd lane that of token i + 1, 4 bytes
+// each; with an odd N, row stride or address, 2 bytes each.
+template <bool BF16, int NC>
+__device__ __forceinline__ void store_cols(const uint32_t (&r)[NC], void* y, int64_t ldy, int64_t n, int64_t N, int lim) {
+  if constexpr (!BF16) {
+    float* p = static_cast<float*>(y) + n;
+    if (n < N)
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (i < lim) p[i * ldy] = __uint_as_float(r[i]);
+  } else {
+    __nv_bfloat16* base = static_cast<__nv_bfloat16*>(y);
+    if (((N | ldy) & 1) == 0 && (reinterpret_cast<uintptr_t>(y) & 3) == 0) {
+      const int odd = static_cast<int>(n & 1);
+      uint32_t* p = reinterpret_cast<uint32_t*>(base + odd * ldy + n - odd);
+      const int64_t step = ldy >> 1;
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) {
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[i] : r[i + 1], 1);
+        const float lo = __uint_as_float(odd ? got : r[i]), hi = __uint_as_float(odd ? r[i + 1] : got);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        uint32_t w;
+        memcpy(&w, &h, 4);
+        if (n < N && i + odd < lim) p[i * step] = w;
+      }
+    } else if (n < N) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (i < lim) base[i * ldy + n] = __float2bfloat16_rn(__uint_as_float(r[i]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- small: M <= 128
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                              const __grid_constant__ CUtensorMap amap, const MxArgs p) {
-  using C = Cfg<NT>;
+struct Small {
+  static constexpr int kStageBytes = kWBytes + NT * 128 + 2 * kSfTile;
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;  // two CTAs an SM
+  static constexpr int kSfCols = 16;
+  static constexpr int kCols = NT + kSfCols * kStages <= 128 ? 128 : 256;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes;
+};
+constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
+
+// grid (S, weight tiles), cluster (S, 1, 1).
+template <int NT, bool BF16>
+__global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                    const __grid_constant__ CUtensorMap amap,
+                                                                    const __grid_constant__ CUtensorMap wsmap,
+                                                                    const __grid_constant__ CUtensorMap asmap,
+                                                                    const MxArgs p) {
+  using C = Small<NT>;
   extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024 - (su32(raw) & 1023)) & 1023);
+  const uint32_t smem = (su32(raw) + 1023u) & ~1023u;
   __shared__ Bars S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTW, m0 = static_cast<int64_t>(blockIdx.z) * NT;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTW;
   const int s0 = static_cast<int>(static_cast<int64_t>(p.stages) * rank / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / split);
+  constexpr uint32_t kTx = C::kStageBytes;
+  auto load = [&](int s, int st) {
+    const uint32_t base = smem + st * C::kStageBytes, bar = su32(&S.full[st]);
+    mbar_expect_tx(&S.full[st], kTx);
+    load_2d<1>(base, &wmap, s * 128, static_cast<int32_t>(n0), bar);
+    load_2d<1>(base + kWBytes + NT * 128, &wsmap, s * 256, static_cast<int32_t>(blockIdx.y), bar);
+    load_2d<1>(base + kWBytes, &amap, s * 128, 0, bar);
+    load_2d<1>(base + kWBytes + NT * 128 + kSfTile, &asmap, s * 256, 0, bar);
+  };
 
-  if (threadIdx.x == 0) {
+  grid_dep_launch();
+  if (warp == 4 && elect_one()) {  // the copies start before the rest of the set-up
+    prefetch_map(&wmap);
+    prefetch_map(&wsmap);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 1);
     }
-    mbar_init(&S.done, 1);
+    mbar_init(&S.acc_full, 1);
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    grid_dep_wait();
+    for (int i = 0; i < C::kStages && s0 + i < s1; ++i) load(s0 + i, i);
   }
   if (warp == 5) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&S.tmem)), "n"(C::kCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tmem_alloc<1>(&S.tmem, C::kCols);
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
 
-  if (warp == 4 && lane == 0) {
-    const int64_t wt = n0 >> 7, at = m0 >> 7, atiles = (p.M + 127) >> 7;
-    int it = 0;
-    for (int s = s0; s < s1; ++s, ++it) {
+  if (warp == 4 && elect_one()) {
+    int it = min(C::kStages, s1 - s0);
+    for (; s0 + it < s1; ++it) {
       const int st = it % C::kStages;
-      if (it >= C::kStages && !wait_bar(S, &S.empty[st], (it / C::kStages - 1) & 1, p.err)) break;
-      uint8_t* base = smem + st * C::kStageBytes;
-      const uint32_t sf = 512u * min(2, p.ktiles - 2 * s);
-      uint32_t bytes = C::kWBytes + C::kABytes + sf;
-      for (int t = 0; t < C::kAtoms; ++t) bytes += at + t < atiles ? sf : 0u;
-      mbar_expect_tx(&S.full[st], bytes);
-      tma_2d(base, &wmap, s * 128, static_cast<int32_t>(n0), &S.full[st]);
-      tma_2d(base + C::kWBytes, &amap, s * 128, static_cast<int32_t>(m0), &S.full[st]);
-      uint8_t* sfp = base + C::kWBytes + C::kABytes;
-      bulk_load(sfp, p.w_scales + (wt * p.ktiles + 2 * s) * 512, sf, &S.full[st]);
-      for (int t = 0; t < C::kAtoms; ++t)
-        if (at + t < atiles)
-          bulk_load(sfp + C::kSfW + t * 1024, p.a_scales + ((at + t) * p.ktiles + 2 * s) * 512, sf, &S.full[st]);
+      if (!wait_bar(S, &S.empty[st], (it / C::kStages - 1) & 1, p.err)) break;
+      load(s0 + it, st);
     }
     if (S.abort)  // copies still in flight must land before the CTA leaves
       for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i) drain_bar(&S.full[i % C::kStages], (i / C::kStages) & 1);
-  } else if (warp == 5 && lane == 0) {
-    // a token tile narrower than a scale tile starts inside it: 32 rows are a column
-    const uint32_t sub = NT < 128 ? static_cast<uint32_t>(m0 & 127) >> 5 : 0u;
-    int it = 0;
+  } else if (warp == 5 && elect_one()) {
+    const uint32_t idesc = mx_idesc(1, NT);
     uint32_t acc = 0;
-    for (int s = s0; s < s1; ++s, ++it) {
+    for (int s = s0, it = 0; s < s1; ++s, ++it) {
       const int st = it % C::kStages;
       if (!wait_bar(S, &S.full[st], (it / C::kStages) & 1, p.err)) break;
       tc_fence_after();
-      uint8_t* base = smem + st * C::kStageBytes;
-      uint8_t* sfp = base + C::kWBytes + C::kABytes;
-      const uint32_t sfw = tmem + NT + st * C::kSfCols, sfa = sfw + 8;
-      const int steps = (min(kStageK, p.K - s * kStageK) + 63) / 64;  // MMAs of K = 64
-      for (int j = 0; 2 * j < steps; ++j) {
-        sf_copy(sfw + 4 * j, sfp + 512 * j);
-        for (int t = 0; t < C::kAtoms; ++t) sf_copy(sfa + 4 * (j * C::kAtoms + t), sfp + C::kSfW + t * 1024 + 512 * j);
-      }
-      for (int k = 0; k < steps; ++k) {
-        mma_mx(tmem, kmajor_desc_sw128(base) + 2 * k, kmajor_desc_sw128(base + C::kWBytes) + 2 * k,
-               mx_idesc(NT, (k & 1) * 2), sfw + 4 * (k >> 1), sfa + 4 * (k >> 1) * C::kAtoms + sub, acc);
-        acc = 1;
-      }
-      mma_commit(&S.empty[st]);
+      const uint32_t base = smem + st * C::kStageBytes;
+      stage_mmas<1, 1>(tmem, base, base + kWBytes, base + kWBytes + NT * 128, tmem + NT + st * C::kSfCols, idesc,
+                       (min(kStageK, p.K - s * kStageK) + 63) / 64, acc);
+      commit<1>(&S.empty[st]);
     }
-    mma_commit(&S.done);
-    if (S.abort) drain_bar(&S.done, 0);
+    commit<1>(&S.acc_full);
+    if (S.abort) drain_bar(&S.acc_full, 0);
   }
 
   __syncwarp();
-  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.done, 0, p.err) && !S.abort);
+  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p.err) && !S.abort);
   tc_fence_after();
   const int64_t n = n0 + 32 * (warp & 3) + lane;
-  const int tok = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  const int tok = static_cast<int>(p.M);
+  constexpr int NC = NT < 32 ? NT : 32;  // columns per pass
+  constexpr int kEsz = BF16 ? 2 : 4;
   if (split == 1) {
-    if (whole) {
-      for (int c = 0; c < tok; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
-        tmem_wait(r);
-        if (n < p.N)
+    if (whole)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < tok) put(p, m0 + c + i, n, __uint_as_float(r[i]));
+      for (int c = 0; c < NT; c += NC) {
+        uint32_t r[NC];
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) tmem_ld16(lanes + c + i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
+        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
-    }
   } else {
-    // tokens r * share .. of the tile are summed and written by rank r
-    const int share = (tok + split - 1) / split;
+    // rank r sums and writes tokens r * share .. ; split and share are powers of two
+    const int share = NT / split, log = 31 - __clz(share);
     cluster_sync();  // every CTA's operand stages are free
-    if (whole) {
-      for (int c = 0; c < tok; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, r);
-        tmem_wait(r);
+    if (whole)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+      for (int c = 0; c < NT; c += NC) {
+        uint32_t r[NC];
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) tmem_ld16(lanes + c + i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
           if (c + i < tok) {
-            const int to = (c + i) / share, slot = (c + i) % share;
-            st_cluster(su32(smem) + 4u * ((rank * share + slot) * kTW + 32 * warp + lane), to, __uint_as_float(r[i]));
+            const int to = (c + i) >> log, slot = (c + i) & (share - 1);
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(
+                             map_rank(smem + 4u * ((rank * share + slot) * kTW + 32 * warp + lane), to)),
+                         "r"(r[i])
+                         : "memory");
           }
       }
-    }
     cluster_sync();
     if (whole && n < p.N) {
-      const float* part = reinterpret_cast<const float*>(smem) + 32 * warp + lane;
+      const float* part = reinterpret_cast<const float*>(raw + (smem - su32(raw))) + 32 * warp + lane;
       for (int i = 0; i < share && rank * share + i < tok; ++i) {
         float v = part[i * kTW];
         for (int r = 1; r < split; ++r) v = __fadd_rn(v, part[(r * share + i) * kTW]);
-        put(p, m0 + rank * share + i, n, v);
+        const int64_t at = static_cast<int64_t>(rank * share + i) * p.ldy + n;
+        if (BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+        else static_cast<float*>(p.y)[at] = v;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kCols));
+  if (warp == 5) tmem_free<1>(tmem, C::kCols);
 }
 
-template <int NT>
-cudaError_t launch_tile(const CUtensorMap& wmap, const CUtensorMap& amap, const MxArgs& a, int split, cudaStream_t st) {
-  using C = Cfg<NT>;
-  static bool configured[64] = {};
+// ---------------------------------------------------------------- pair: M > 128
+constexpr int kMaxTok = 256;
+constexpr int kPairStages = 6;
+constexpr int kPairAtoms = kMaxTok / 128;
+constexpr int kPairSf = kWBytes + (kMaxTok / 2) * 128;
+constexpr int kPairStageBytes = kPairSf + (1 + kPairAtoms) * kSfTile;
+constexpr int kPairSfCols = 8 + 8 * kPairAtoms;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes;
+constexpr int kPairThreads = 320;  // 8 epilogue warps, a copy warp, an MMA warp
+static_assert(kMaxTok + kPairStages * kPairSfCols <= 512, "TMEM columns");
+
+// Tokens of the tile at m0 that the MMA computes: a multiple of 32, whose halves are
+// whole 8-row swizzle atoms.
+__device__ __forceinline__ int tile_tok(int64_t M, int64_t m0) {
+  return static_cast<int>(min(static_cast<int64_t>(kMaxTok), (M - m0 + 31) & ~int64_t(31)));
+}
+
+// Persistent: pair c takes tiles c, c + pairs, ...; tile t is weight rows 256 (t / mt),
+// tokens 256 (t % mt).  CTA `rank` of the pair holds weight rows 128 rank .. of the
+// tile, one half of its tokens as its part of the N operand, and every token's scales.
+template <bool BF16>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                   const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap asmap, const MxArgs p) {
+  extern __shared__ uint8_t raw[];
+  const uint32_t smem = (su32(raw) + 1023u) & ~1023u;
+  __shared__ Bars S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.empty[i], 1);
+    }
+    mbar_init(&S.acc_full, 1);
+    mbar_init(&S.acc_empty, 16);  // the epilogue warps of both CTAs
+    S.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    tmem_alloc<2>(&S.tmem, 512);
+    tc_fence_before();
+  }
+  if (warp == 8 && elect_one()) {
+    prefetch_map(&wmap);
+    prefetch_map(&amap);
+    prefetch_map(&wsmap);
+    prefetch_map(&asmap);
+  }
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  grid_dep_wait();
+
+  if (warp == 8) {
+    if (elect_one()) {
+      const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
+      int it = 0;
+      for (int64_t t = pair; t < p.tiles && !S.abort; t += pairs) {
+        const int32_t w0 = static_cast<int32_t>(t / p.mt) * 256 + static_cast<int32_t>(rank) * kTW;
+        const int32_t m0 = static_cast<int32_t>(t % p.mt) * kMaxTok;
+        const int32_t half = tile_tok(p.M, m0) / 2 * static_cast<int32_t>(rank);
+        for (int s = 0; s < p.stages; ++s, ++it) {
+          const int st = it % kPairStages;
+          if (it >= kPairStages && !wait_bar(S, &S.empty[st], (it / kPairStages - 1) & 1, p.err)) break;
+          const uint32_t base = smem + st * kPairStageBytes, bar = map_rank(su32(&S.full[st]), 0);
+          if (rank == 0) mbar_expect_tx(&S.full[st], tx);
+          load_2d<2>(base, &wmap, s * 128, w0, bar);
+          load_2d<2>(base + kWBytes, &amap, s * 128, m0 + half, bar);
+          load_2d<2>(base + kPairSf, &wsmap, s * 256, w0 >> 7, bar);
+#pragma unroll
+          for (int a = 0; a < kPairAtoms; ++a)
+            load_2d<2>(base + kPairSf + (1 + a) * kSfTile, &asmap, s * 256, (m0 >> 7) + a, bar);
+        }
+      }
+      if (S.abort && rank == 0)  // both CTAs' copies count on the leader's barriers
+        for (int i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
+          drain_bar(&S.full[i % kPairStages], (i / kPairStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (rank == 0 && elect_one()) {
+      int it = 0;
+      int64_t n_tile = 0;
+      for (int64_t t = pair; t < p.tiles && !S.abort; t += pairs, ++n_tile) {
+        const uint32_t idesc = mx_idesc(2, tile_tok(p.M, t % p.mt * kMaxTok));
+        if (n_tile > 0 && !wait_bar(S, &S.acc_empty, static_cast<uint32_t>(n_tile - 1) & 1, p.err)) break;
+        tc_fence_after();
+        uint32_t acc = 0;
+        for (int s = 0; s < p.stages; ++s, ++it) {
+          const int st = it % kPairStages;
+          if (!wait_bar(S, &S.full[st], (it / kPairStages) & 1, p.err)) break;
+          tc_fence_after();
+          const uint32_t base = smem + st * kPairStageBytes;
+          stage_mmas<2, kPairAtoms>(tmem, base, base + kWBytes, base + kPairSf, tmem + kMaxTok + st * kPairSfCols, idesc,
+                                    (min(kStageK, p.K - s * kStageK) + 63) / 64, acc);
+          commit<2>(&S.empty[st]);
+        }
+        commit<2>(&S.acc_full);
+      }
+      if (S.abort) {  // MMAs in flight: the parity of a further commit is not known, so wait out the bound
+        const uint64_t t0 = gtime();
+        while (gtime() - t0 < kWaitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * (warp >> 2);
+    const uint32_t empty = map_rank(su32(&S.acc_empty), 0);
+    int64_t n_tile = 0;
+    for (int64_t t = pair; t < p.tiles; t += pairs, ++n_tile) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, static_cast<uint32_t>(n_tile) & 1, p.err))) break;
+      tc_fence_after();
+      uint32_t r[128];
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) tmem_ld32(lanes + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) tmem_wait32(*reinterpret_cast<uint32_t(*)[32]>(r + c));
+      tc_fence_before();
+      __syncwarp();
+      if (elect_one())
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(empty) : "memory");
+      __syncwarp();
+      const int64_t n = t / p.mt * 256 + rank * kTW + 32 * (warp & 3) + lane;
+      const int64_t m0 = t % p.mt * kMaxTok + 128 * (warp >> 2);
+      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
+                       static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's MMAs and arrivals no longer touch this CTA
+  if (warp == 9) tmem_free<2>(tmem, 512);
+}
+
+// ---------------------------------------------------------------- launches
+template <class Kernel>
+cudaError_t launch(Kernel kernel, bool (&configured)[64], dim3 grid, int threads, int smem, int cluster,
+                   const CUtensorMap (&m)[4], const MxArgs& a, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(mx_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(split, static_cast<unsigned>((a.N + kTW - 1) / kTW), static_cast<unsigned>((a.M + NT - 1) / NT));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<NT>, wmap, amap, a);
+  if (cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], a);
+}
+
+template <int NT>
+cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16, cudaStream_t st) {
+  using C = Small<NT>;
+  static bool configured[2][64] = {};
+  const int64_t tiles = (a.N + kTW - 1) / kTW;
+  // K shared by as many CTAs (a power of two up to 8) as have two stages each and fit
+  // the SMs' two slots
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && a.stages >= split * 4) split *= 2;
+  const dim3 grid(split, static_cast<unsigned>(tiles));
+  return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, C::kSmem, split, m, a, st)
+                : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, C::kSmem, split, m, a, st);
 }
 
 }  // namespace
@@ -284,33 +583,45 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy,
                            cudaStream_t stream) {
   MxArgs a{};
-  a.w_scales = w_scales; a.a_scales = a_scales; a.y = y; a.ldy = ldy; a.M = M; a.N = N;
+  a.y = y; a.ldy = ldy; a.M = M; a.N = N;
   a.K = static_cast<int>(K);
-  a.ktiles = static_cast<int>((K + 127) / 128);
   a.stages = static_cast<int>((K + kStageK - 1) / kStageK);
-  a.y_bf16 = y_bf16;
   a.err = device_error_word();
-  const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  const int64_t tiles = ((N + kTW - 1) / kTW) * ((M + nt - 1) / nt);
-  // K shared by as many CTAs (a power of two up to 8) as still have two stages each
-  // while the tiles leave SMs idle
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= num_sms() && a.stages >= split * 4) split *= 2;
-  CUtensorMap wmap, amap;
-  cudaError_t e = encode_2d_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, static_cast<uint64_t>(K / 2),
-                                static_cast<uint64_t>(N), static_cast<uint64_t>(K / 2), 128, kTW,
-                                CU_TENSOR_MAP_SWIZZLE_128B);
+  if (M <= 128) {
+    a.mt = 1;
+    a.box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  } else {
+    a.mt = static_cast<int>((M + kMaxTok - 1) / kMaxTok);
+    a.tiles = (N + 255) / 256 * a.mt;
+    a.box = a.mt > 1 ? kMaxTok / 2 : static_cast<int>((M + 31) / 32 * 16);
+  }
+  const uint64_t kt = static_cast<uint64_t>((K + 127) / 128) * 128, row = static_cast<uint64_t>(K / 2);
+  CUtensorMap m[4];
+  cudaError_t e = encode_2d_map(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, row, static_cast<uint64_t>(N), row, 128,
+                                kTW, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e == cudaSuccess)
-    e = encode_2d_map(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, static_cast<uint64_t>(K / 2),
-                      static_cast<uint64_t>(M), static_cast<uint64_t>(K / 2), 128, static_cast<uint32_t>(nt),
+    e = encode_2d_map(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, row, static_cast<uint64_t>(M), row, 128, static_cast<uint32_t>(a.box),
                       CU_TENSOR_MAP_SWIZZLE_128B);
+  // scale tiles as rows of 4-byte words: what lies past the last tile reads as zero
+  if (e == cudaSuccess)
+    e = encode_2d_map(&m[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, w_scales, kt, static_cast<uint64_t>((N + 127) / 128), kt * 4,
+                      256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (e == cudaSuccess)
+    e = encode_2d_map(&m[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kt, static_cast<uint64_t>((M + 127) / 128), kt * 4,
+                      256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (e != cudaSuccess) return e;
-  switch (nt) {
-    case 16: return launch_tile<16>(wmap, amap, a, split, stream);
-    case 32: return launch_tile<32>(wmap, amap, a, split, stream);
-    case 64: return launch_tile<64>(wmap, amap, a, split, stream);
-    case 128: return launch_tile<128>(wmap, amap, a, split, stream);
-    default: return launch_tile<256>(wmap, amap, a, split, stream);
+  if (M > 128) {
+    static bool configured[2][64] = {};
+    const int64_t pairs = num_sms() / 2;
+    const dim3 grid(static_cast<unsigned>(2 * (a.tiles < pairs ? a.tiles : pairs)));
+    return y_bf16 ? launch(mx_pair_kernel<true>, configured[1], grid, kPairThreads, kPairSmem, 0, m, a, stream)
+                  : launch(mx_pair_kernel<false>, configured[0], grid, kPairThreads, kPairSmem, 0, m, a, stream);
+  }
+  switch (a.box) {
+    case 16: return launch_small<16>(m, a, y_bf16, stream);
+    case 32: return launch_small<32>(m, a, y_bf16, stream);
+    case 64: return launch_small<64>(m, a, y_bf16, stream);
+    default: return launch_small<128>(m, a, y_bf16, stream);
   }
 }
 
