@@ -42,7 +42,7 @@ __all__ = [
     "Act8", "w4a8_rotate_quantize_act", "w4a8_gemm", "w4a8_gemm_partials", "w4a8_gemm_workspace_bytes",
     "w4a4_gemm_small_m",
     "MxFp4", "mxfp4_rotate_quantize", "mxfp4_import", "mxfp4_dequantize", "mxfp4_gemm",
-    "w4a4_dequantize_act", "w4a8_dequantize_act",
+    "mxfp4_gemm_workspace_bytes", "w4a4_dequantize_act", "w4a8_dequantize_act",
     "w4a4_rmsnorm_quantize_act", "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize",
     "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize",
 ]
@@ -70,7 +70,7 @@ EXPORTS = [
     "w4a4_act16_values_bytes", "w4a16_rotate_act", "w4a16_gemm", "w4a16_gemm_workspace_bytes",
     "h32_q4_0_pack_weights_imatrix", "w4a4_debug_set_wait_limit",
     "w4a4_mxfp4_codes_bytes", "w4a4_mxfp4_scales_bytes", "mxfp4_rotate_quantize", "mxfp4_import", "mxfp4_dequantize",
-    "w4a4_dequantize_act", "w4a8_dequantize_act", "mxfp4_gemm", "w4a4_rmsnorm_quantize_act",
+    "w4a4_dequantize_act", "w4a8_dequantize_act", "mxfp4_gemm", "mxfp4_gemm_workspace_bytes", "w4a4_rmsnorm_quantize_act",
     "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize", "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act",
     "mxfp4_swiglu_quantize",
 ]
@@ -159,7 +159,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.mxfp4_import.argtypes = [vp, vp, i64, i64, i32, vp, vp]
     for name in ("mxfp4_dequantize", "w4a4_dequantize_act", "w4a8_dequantize_act"):
         getattr(lib, name).argtypes = [vp, vp, i32, i64, vp]
-    lib.mxfp4_gemm.argtypes = [vp, vp, vp, i32, i64, vp]
+    lib.mxfp4_gemm.argtypes = [vp, vp, vp, i32, i64, vp, u, vp]
+    lib.mxfp4_gemm_workspace_bytes.argtypes, lib.mxfp4_gemm_workspace_bytes.restype = [i64, i64, i64], u
     for name in ("w4a4_rmsnorm_quantize_act", "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize"):
         getattr(lib, name).argtypes = [vp, vp, vp]
     for name in ("w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize"):
@@ -778,15 +779,28 @@ def w4a8_dequantize_act(a: Act8, y: torch.Tensor | None = None, dtype: torch.dty
     return _dequantize("w4a8_dequantize_act", a, y, dtype, stream)
 
 
+def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().mxfp4_gemm_workspace_bytes(M, N, K))
+
+
 def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
-               stream=None) -> torch.Tensor:
-    """Y[m][n] = the product of MXFP4 weights w [N][K] and activations a [M][K], fp32 sums (fp32 or bf16 [M][N])."""
+               ws: torch.Tensor | None | bool = True, stream=None) -> torch.Tensor:
+    """Y[m][n] = the product of MXFP4 weights w [N][K] and activations a [M][K], fp32 sums (fp32 or bf16 [M][N]).
+
+    ws: True = the cached per-stream workspace (the last wave cut over the SMs where that pays), a tensor = that
+    workspace (zero before its first use), None/False = whole tiles only.
+    """
     if y is None:
         y = torch.empty(a.rows, w.rows, dtype=dtype, device=w.codes.device)
     ldy = _rows(y, "y", (a.rows, w.rows))
+    lib, st = load_library(), _stream(stream)
+    if ws is True:
+        need = lib.mxfp4_gemm_workspace_bytes(a.rows, w.rows, w.K)
+        ws = gemm_workspace(a.rows, w.rows, w.K, y.device, st, need) if need else None
+    ws_ptr, ws_bytes = (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None and ws is not False else (None, 0)
     dw, da = w.desc(), a.desc()
-    _check(load_library().mxfp4_gemm(ctypes.addressof(dw), ctypes.addressof(da), y.data_ptr(), _DTYPE[y.dtype], ldy,
-                                     _stream(stream)))
+    _check(lib.mxfp4_gemm(ctypes.addressof(dw), ctypes.addressof(da), y.data_ptr(), _DTYPE[y.dtype], ldy, ws_ptr,
+                          ws_bytes, st))
     return y
 
 

@@ -643,8 +643,13 @@ w4a4_status w4a8_dequantize_act(const w4a4_act8* a, void* y, int y_dtype, int64_
   return read_back(fn, 8, a->codes, a->scales, a->rows, a->K, y, y_dtype, ldy, stream);
 }
 
-w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy,
-                       w4a4_stream_t stream) {
+size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || !valid_k(K)) return 0;
+  return w4a4::mx_gemm_workspace_bytes(M, N, K);
+}
+
+w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy, void* ws,
+                       size_t ws_bytes, w4a4_stream_t stream) {
   const char* fn = "mxfp4_gemm";
   w4a4_status s = check_mx(w, fn);
   if (s != W4A4_OK) return s;
@@ -664,8 +669,15 @@ w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_
     return fail(W4A4_ERR_ALIGNMENT, "%s: y must be aligned to its element", fn);
   if (N > w4a4::kMxMaxRows || M > w4a4::kMxMaxRows)
     return fail(W4A4_ERR_UNSUPPORTED, "%s: at most %lld rows an operand", fn, (long long)w4a4::kMxMaxRows);
+  if (ws) {
+    const size_t need = w4a4::mx_gemm_workspace_bytes(M, N, a->K);
+    if (ws_bytes < need)
+      return fail(W4A4_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+    if (!aligned16(ws)) return fail(W4A4_ERR_ALIGNMENT, "%s: ws must be 16-byte aligned", fn);
+  }
   return cuda_status(w4a4::launch_mx_gemm(w->codes, w->scales, N, a->codes, a->scales, M, a->K, y,
-                                          y_dtype == W4A4_DTYPE_BF16, ldy, reinterpret_cast<cudaStream_t>(stream)), fn);
+                                          y_dtype == W4A4_DTYPE_BF16, ldy, ws, reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
 }
 
 w4a4_status w4a4_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act4* out, w4a4_stream_t stream) {

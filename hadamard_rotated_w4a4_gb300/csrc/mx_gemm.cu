@@ -19,7 +19,8 @@
 //     to 256 tokens.  Each CTA stages half of both operands, which is what lets shared
 //     memory (written once, read once per MMA, 128 bytes a cycle) keep up with the
 //     tensor core.  The accumulators leave TMEM for registers at once, and their stores
-//     overlap the next tile's MMAs.
+//     (32 bytes a cycle and SM at most) overlap the next tile's MMAs.  With a workspace
+//     the last waves' K work is cut evenly over the pairs (stream-K).
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"
@@ -31,7 +32,9 @@ namespace {
 
 constexpr int kTW = 128;      // weight rows per CTA
 constexpr int kStageK = 256;  // elements of K per stage
-constexpr uint64_t kWaitNs = 1000000000ull;
+// Bound of every wait, about a second.  Counted in SM cycles: reading the global timer in
+// a polling loop delays the wake-up by hundreds of them.
+constexpr int64_t kWaitCycles = int64_t(1) << 31;
 constexpr int kWBytes = kTW * 128;
 constexpr int kSfTile = 1024;  // a stage's scales of 128 rows: two 512-byte tiles
 
@@ -40,9 +43,15 @@ struct MxArgs {
   int64_t ldy;
   int64_t M, N;
   int K, stages;
-  int mt;       // token tiles (of kMaxTok, the last one narrower)
   int box;      // token rows of one load
-  int64_t tiles;
+  // pair kernel
+  int mtok;     // tokens of a tile, 128 or 256 (the last one of a row narrower)
+  int mt;       // token tiles
+  int tiles;
+  int whole;    // tiles 0 .. whole - 1 go to the pairs whole, in turn; the rest by stages
+  int64_t units;     // stages of the rest (0: none)
+  uint32_t* flags;   // [pairs][2 CTAs][8 warps], zero between calls
+  float4* parts;     // [pairs][2][8][32][32]: a warp's 128 accumulators of 32 lanes
   int* err;
 };
 
@@ -55,10 +64,10 @@ struct Bars {
 // Bounded wait; on giving up, every other wait of the CTA gives up too.
 __device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, int* err) {
   if (mbar_try(b, parity)) return true;
-  const uint64_t t0 = gtime();
+  const int64_t t0 = clock64();
   while (!mbar_try(b, parity)) {
     if (S.abort) return false;
-    if (gtime() - t0 > kWaitNs) {
+    if (clock64() - t0 > kWaitCycles) {
       S.abort = 1;
       if (err) atomicOr(err, 32);
       return false;
@@ -68,8 +77,8 @@ __device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, 
 }
 // As above without the shared give-up, for copies and MMAs in flight.
 __device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
-  const uint64_t t0 = gtime();
-  while (!mbar_try(b, parity) && gtime() - t0 < kWaitNs) {
+  const int64_t t0 = clock64();
+  while (!mbar_try(b, parity) && clock64() - t0 < kWaitCycles) {
   }
 }
 
@@ -178,17 +187,17 @@ __device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t wsm, uint32_t as
                         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);  // as kmajor_desc_sw128
   const uint64_t wd = base | ((wsm >> 4) & 0x3FFFu), ad = base | ((asm_ >> 4) & 0x3FFFu);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (2 * j < steps) {
-      sf_copy<CG>(sfw + 4 * j, sfsm + 512 * j);
-#pragma unroll
-      for (int t = 0; t < kAtoms; ++t)
-        sf_copy<CG>(sfa + 4 * (j * kAtoms + t), sfsm + kSfTile + t * kSfTile + 512 * j);
-    }
-  }
-#pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (k < steps) {
+      // the scales of 128 elements in front of their two MMAs, not of a whole stage in
+      // front of four: a copy runs beside the MMA before it (M2048 K20480 N9728: 105.5 -> 100 us)
+      if (!(k & 1)) {
+        const int j = k >> 1;
+        sf_copy<CG>(sfw + 4 * j, sfsm + 512 * j);
+#pragma unroll
+        for (int t = 0; t < kAtoms; ++t)
+          sf_copy<CG>(sfa + 4 * (j * kAtoms + t), sfsm + kSfTile + t * kSfTile + 512 * j);
+      }
       mma_mx<CG>(d, wd + 2 * k, ad + 2 * k, (k & 1) ? idesc | kSfHigh : idesc, sfw + 4 * (k >> 1),
                  sfa + 4 * (k >> 1) * kAtoms, acc);
       acc = 1;
@@ -218,35 +227,37 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, in
 // i); y points at token 0.  bf16: neighbouring lanes trade so that the even lane
 // stores the pair (n, n + 1) of token i and the odd lane that of token i + 1, 4 bytes
 // each; with an odd N, row stride or address, 2 bytes each.
-template <bool BF16, int NC>
-__device__ __forceinline__ void store_cols(const uint32_t (&r)[NC], void* y, int64_t ldy, int64_t n, int64_t N, int lim) {
+template <bool BF16, int NC, bool FULL>
+__device__ __forceinline__ void store_cols_t(const uint32_t (&r)[NC], void* y, int64_t ldy, int64_t n, int64_t N, int lim) {
   if constexpr (!BF16) {
     float* p = static_cast<float*>(y) + n;
     if (n < N)
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (i < lim) p[i * ldy] = __uint_as_float(r[i]);
+      for (int i = 0; i < NC; ++i, p += ldy)
+        if (FULL || i < lim) *p = __uint_as_float(r[i]);
   } else {
     __nv_bfloat16* base = static_cast<__nv_bfloat16*>(y);
     if (((N | ldy) & 1) == 0 && (reinterpret_cast<uintptr_t>(y) & 3) == 0) {
       const int odd = static_cast<int>(n & 1);
-      uint32_t* p = reinterpret_cast<uint32_t*>(base + odd * ldy + n - odd);
-      const int64_t step = ldy >> 1;
+      __nv_bfloat16* p = base + odd * ldy + n - odd;
 #pragma unroll
-      for (int i = 0; i < NC; i += 2) {
+      for (int i = 0; i < NC; i += 2, p += 2 * ldy) {
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[i] : r[i + 1], 1);
         const float lo = __uint_as_float(odd ? got : r[i]), hi = __uint_as_float(odd ? r[i + 1] : got);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        uint32_t w;
-        memcpy(&w, &h, 4);
-        if (n < N && i + odd < lim) p[i * step] = w;
+        if (n < N && (FULL || i + odd < lim)) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(lo, hi);
       }
     } else if (n < N) {
+      __nv_bfloat16* p = base + n;
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (i < lim) base[i * ldy + n] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      for (int i = 0; i < NC; ++i, p += ldy)
+        if (FULL || i < lim) *p = __float2bfloat16_rn(__uint_as_float(r[i]));
     }
   }
+}
+template <bool BF16, int NC>
+__device__ __forceinline__ void store_cols(const uint32_t (&r)[NC], void* y, int64_t ldy, int64_t n, int64_t N, int lim) {
+  if (lim >= NC) store_cols_t<BF16, NC, true>(r, y, ldy, n, N, lim);
+  else store_cols_t<BF16, NC, false>(r, y, ldy, n, N, lim);
 }
 
 // ---------------------------------------------------------------- small: M <= 128
@@ -404,13 +415,44 @@ static_assert(kMaxTok + kPairStages * kPairSfCols <= 512, "TMEM columns");
 
 // Tokens of the tile at m0 that the MMA computes: a multiple of 32, whose halves are
 // whole 8-row swizzle atoms.
-__device__ __forceinline__ int tile_tok(int64_t M, int64_t m0) {
-  return static_cast<int>(min(static_cast<int64_t>(kMaxTok), (M - m0 + 31) & ~int64_t(31)));
+__device__ __forceinline__ int tile_tok(const MxArgs& p, int m0) {
+  return static_cast<int>(min(static_cast<int64_t>(p.mtok), (p.M - m0 + 31) & ~int64_t(31)));
 }
 
-// Persistent: pair c takes tiles c, c + pairs, ...; tile t is weight rows 256 (t / mt),
-// tokens 256 (t % mt).  CTA `rank` of the pair holds weight rows 128 rank .. of the
-// tile, one half of its tokens as its part of the N operand, and every token's scales.
+// The work of a pair, in order: whole tiles `pair`, pair + pairs, ... below p.whole,
+// then the range [lo, hi) of the remaining tiles' stages.  A range is at least a tile
+// long, so a tile is cut between two pairs at most: the one whose range ends in it
+// holds the first stages (head), the one whose range begins in it the last (tail).
+struct Work {
+  int tile, s0, s1;  // the segment: stages [s0, s1) of a tile
+  int step;
+  int64_t lo, hi;
+  __device__ __forceinline__ Work(const MxArgs& p, int pair, int pairs) : tile(pair - pairs), s0(0), s1(0), step(pairs) {
+    // a pair that waits for a tail waits for one that started before it: ranges in
+    // descending order of the pair's number
+    const int64_t at = pairs - 1 - pair;
+    lo = p.units * at / pairs;
+    hi = p.units * (at + 1) / pairs;
+  }
+  __device__ __forceinline__ bool next(const MxArgs& p) {
+    if (tile + step < p.whole) {
+      tile += step;
+      s1 = p.stages;
+      return true;
+    }
+    if (lo >= hi) return false;
+    step = p.whole;  // no whole tile follows
+    tile = p.whole + static_cast<int>(lo / p.stages);
+    s0 = static_cast<int>(lo % p.stages);
+    s1 = static_cast<int>(min(static_cast<int64_t>(p.stages), s0 + (hi - lo)));
+    lo += s1 - s0;
+    return true;
+  }
+};
+
+// Persistent; tile t is weight rows 256 (t / mt), tokens mtok (t % mt).  CTA `rank` of
+// the pair holds weight rows 128 rank .. of the tile, one half of its tokens as its
+// part of the N operand, and every token's scales.
 template <bool BF16>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
@@ -420,7 +462,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ Bars S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   grid_dep_launch();
   if (threadIdx.x == 0) {
@@ -443,6 +485,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     prefetch_map(&wsmap);
     prefetch_map(&asmap);
   }
+  Work work(p, pair, pairs);
+  bool more = work.next(p);
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised
   tc_fence_after();
@@ -453,11 +497,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     if (elect_one()) {
       const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
       int it = 0;
-      for (int64_t t = pair; t < p.tiles && !S.abort; t += pairs) {
-        const int32_t w0 = static_cast<int32_t>(t / p.mt) * 256 + static_cast<int32_t>(rank) * kTW;
-        const int32_t m0 = static_cast<int32_t>(t % p.mt) * kMaxTok;
-        const int32_t half = tile_tok(p.M, m0) / 2 * static_cast<int32_t>(rank);
-        for (int s = 0; s < p.stages; ++s, ++it) {
+      for (; !S.abort && more; more = work.next(p)) {
+        const int32_t w0 = work.tile / p.mt * 256 + static_cast<int32_t>(rank) * kTW;
+        const int32_t m0 = work.tile % p.mt * p.mtok;
+        const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
+        for (int s = work.s0; s < work.s1; ++s, ++it) {
           const int st = it % kPairStages;
           if (it >= kPairStages && !wait_bar(S, &S.empty[st], (it / kPairStages - 1) & 1, p.err)) break;
           const uint32_t base = smem + st * kPairStageBytes, bar = map_rank(su32(&S.full[st]), 0);
@@ -477,14 +521,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
-      int it = 0;
-      int64_t n_tile = 0;
-      for (int64_t t = pair; t < p.tiles && !S.abort; t += pairs, ++n_tile) {
-        const uint32_t idesc = mx_idesc(2, tile_tok(p.M, t % p.mt * kMaxTok));
-        if (n_tile > 0 && !wait_bar(S, &S.acc_empty, static_cast<uint32_t>(n_tile - 1) & 1, p.err)) break;
+      int it = 0, seg = 0;
+      for (; !S.abort && more; more = work.next(p)) {
+        const uint32_t idesc = mx_idesc(2, tile_tok(p, work.tile % p.mt * p.mtok));
+        if (seg > 0 && !wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err)) break;
+        ++seg;
         tc_fence_after();
         uint32_t acc = 0;
-        for (int s = 0; s < p.stages; ++s, ++it) {
+        for (int s = work.s0; s < work.s1; ++s, ++it) {
           const int st = it % kPairStages;
           if (!wait_bar(S, &S.full[st], (it / kPairStages) & 1, p.err)) break;
           tc_fence_after();
@@ -496,8 +540,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         commit<2>(&S.acc_full);
       }
       if (S.abort) {  // MMAs in flight: the parity of a further commit is not known, so wait out the bound
-        const uint64_t t0 = gtime();
-        while (gtime() - t0 < kWaitNs) {
+        const int64_t t0 = clock64();
+        while (clock64() - t0 < kWaitCycles) {
         }
       }
     }
@@ -505,24 +549,70 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   } else {
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * (warp >> 2);
     const uint32_t empty = map_rank(su32(&S.acc_empty), 0);
-    int64_t n_tile = 0;
-    for (int64_t t = pair; t < p.tiles; t += pairs, ++n_tile) {
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, static_cast<uint32_t>(n_tile) & 1, p.err))) break;
-      tc_fence_after();
+    uint32_t seg = 0;
+    bool live = true;  // cleared when a wait gave up; the barrier below still counts this warp
+    for (; more; more = work.next(p)) {
+      live = live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, seg & 1, p.err));
+      ++seg;
       uint32_t r[128];
+      if (live) {
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_ld32(lanes + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+        for (int c = 0; c < 128; c += 32) tmem_ld32(lanes + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_wait32(*reinterpret_cast<uint32_t(*)[32]>(r + c));
-      tc_fence_before();
-      __syncwarp();
-      if (elect_one())
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(empty) : "memory");
-      __syncwarp();
-      const int64_t n = t / p.mt * 256 + rank * kTW + 32 * (warp & 3) + lane;
-      const int64_t m0 = t % p.mt * kMaxTok + 128 * (warp >> 2);
-      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
-                       static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
+        for (int c = 0; c < 128; c += 32) tmem_wait32(*reinterpret_cast<uint32_t(*)[32]>(r + c));
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one())
+          // relaxed: the loads from TMEM are complete, and a release would wait for the
+          // last tile's stores (over 1000 cycles)
+          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(empty) : "memory");
+      }
+      // no warp's stores may queue in front of another warp's arrival: the MMAs wait for it
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (!live) continue;
+      if (work.s0 > 0) {  // tail: deposit for the pair that holds the head, the next one up
+        const int64_t at = (static_cast<int64_t>(pair) * 2 + rank) * 8 + warp;
+        float4* part = p.parts + at * 1024 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          __stcg(part + i * 32, make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                            __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + at), "r"(1u) : "memory");
+        continue;
+      }
+      if (work.s1 < p.stages) {  // head: add the tail, deposited by the pair before this one
+        const int64_t at = (static_cast<int64_t>(pair - 1) * 2 + rank) * 8 + warp;
+        const int64_t t0 = clock64();
+        uint32_t there = 0;
+        while (true) {
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(p.flags + at) : "memory");
+          if (__all_sync(0xFFFFFFFFu, there != 0) || __any_sync(0xFFFFFFFFu, S.abort || clock64() - t0 > kWaitCycles)) break;
+        }
+        if (!__all_sync(0xFFFFFFFFu, there != 0)) {
+          S.abort = 1;
+          if (p.err && lane == 0) atomicOr(p.err, 32);
+          live = false;
+          continue;
+        }
+        const float4* part = p.parts + at * 1024 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float4 v = __ldcg(part + i * 32);
+          r[4 * i] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i]), v.x));
+          r[4 * i + 1] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 1]), v.y));
+          r[4 * i + 2] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 2]), v.z));
+          r[4 * i + 3] = __float_as_uint(__fadd_rn(__uint_as_float(r[4 * i + 3]), v.w));
+        }
+        if (lane == 0) p.flags[at] = 0u;
+      }
+      const int64_t n = work.tile / p.mt * 256 + rank * kTW + 32 * (warp & 3) + lane;
+      const int64_t m0 = work.tile % p.mt * p.mtok + 128 * (warp >> 2);
+      if (128 * (warp >> 2) < p.mtok)
+        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
+                         static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
     }
   }
   tc_fence_before();
@@ -577,23 +667,62 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
                 : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, C::kSmem, split, m, a, st);
 }
 
+// The pair kernel's schedule.
+struct PairPlan {
+  int mtok, mt, tiles, whole, pairs;
+  int64_t units;
+  size_t flag_bytes, ws_bytes;
+};
+PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
+  PairPlan q{};
+  const int64_t pairs = num_sms() / 2, wt = (N + 255) / 256;
+  const int stages = static_cast<int>((K + kStageK - 1) / kStageK);
+  // 128 tokens a tile where that still leaves every tile a pair of its own (M256 K5120
+  // N5120: MEASURED), else 256
+  q.mtok = wt * ((M + 127) / 128) <= pairs ? 128 : 256;
+  q.mt = static_cast<int>((M + q.mtok - 1) / q.mtok);
+  q.tiles = static_cast<int>(wt * q.mt);
+  q.whole = q.tiles;
+  // Whole tiles leave the pairs idle for the unused part of the last wave.  Cutting the
+  // last wave and what is left by stages instead costs a deposit and a pick-up, about
+  // kCutStages of MMAs.
+  constexpr int kCutStages = 8;
+  const int64_t waves = (q.tiles + pairs - 1) / pairs;
+  if (q.tiles > pairs && (waves * pairs - q.tiles) * stages > kCutStages * pairs) {
+    q.whole = static_cast<int>((waves - 2) * pairs);
+    q.units = static_cast<int64_t>(q.tiles - q.whole) * stages;
+    q.flag_bytes = (static_cast<size_t>(pairs) * 16 * sizeof(uint32_t) + 255) & ~size_t(255);
+    q.ws_bytes = q.flag_bytes + static_cast<size_t>(pairs) * 16 * 1024 * sizeof(float4);
+  }
+  q.pairs = static_cast<int>(q.tiles < pairs ? q.tiles : pairs);
+  return q;
+}
+
 }  // namespace
 
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return M <= 128 ? 0 : plan_pair(M, N, K).ws_bytes; }
+
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
-                           const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy,
+                           const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
                            cudaStream_t stream) {
   MxArgs a{};
   a.y = y; a.ldy = ldy; a.M = M; a.N = N;
   a.K = static_cast<int>(K);
   a.stages = static_cast<int>((K + kStageK - 1) / kStageK);
   a.err = device_error_word();
+  PairPlan q{};
   if (M <= 128) {
-    a.mt = 1;
     a.box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   } else {
-    a.mt = static_cast<int>((M + kMaxTok - 1) / kMaxTok);
-    a.tiles = (N + 255) / 256 * a.mt;
-    a.box = a.mt > 1 ? kMaxTok / 2 : static_cast<int>((M + 31) / 32 * 16);
+    q = plan_pair(M, N, K);
+    a.mtok = q.mtok; a.mt = q.mt; a.tiles = q.tiles; a.whole = q.tiles;
+    if (ws && q.units > 0) {
+      a.whole = q.whole;
+      a.units = q.units;
+      a.flags = static_cast<uint32_t*>(ws);
+      a.parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + q.flag_bytes);
+    }
+    a.box = a.mt > 1 ? a.mtok / 2 : static_cast<int>((M + 31) / 32 * 16);
   }
   const uint64_t kt = static_cast<uint64_t>((K + 127) / 128) * 128, row = static_cast<uint64_t>(K / 2);
   CUtensorMap m[4];
@@ -612,8 +741,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
   if (e != cudaSuccess) return e;
   if (M > 128) {
     static bool configured[2][64] = {};
-    const int64_t pairs = num_sms() / 2;
-    const dim3 grid(static_cast<unsigned>(2 * (a.tiles < pairs ? a.tiles : pairs)));
+    const dim3 grid(static_cast<unsigned>(2 * q.pairs));
     return y_bf16 ? launch(mx_pair_kernel<true>, configured[1], grid, kPairThreads, kPairSmem, 0, m, a, stream)
                   : launch(mx_pair_kernel<false>, configured[0], grid, kPairThreads, kPairSmem, 0, m, a, stream);
   }

@@ -139,10 +139,12 @@ cudaError_t launch_dequantize(int fmt, const uint8_t* codes, const void* scales,
 // Row-major MXFP4 (codes [rows][K/2], scale bytes [rows][K/32]) into the library layout.
 cudaError_t launch_import_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, uint8_t* out,
                              uint8_t* out_scales, cudaStream_t st);
-// The MXFP4 product (mx_gemm.cu).
+// The MXFP4 product (mx_gemm.cu); ws: null, or mx_gemm_workspace_bytes(M, N, K) bytes,
+// zero before their first use.
 constexpr int64_t kMxMaxRows = 65535 * 128;  // rows of an operand: a tile of 128 or more per grid index
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
-                           const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy,
+                           const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
                            cudaStream_t stream);
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 }  // namespace w4a4

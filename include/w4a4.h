@@ -486,11 +486,23 @@ w4a4_status w4a8_dequantize_act(const w4a4_act8* a, void* y, int y_dtype, int64_
  *   w : rows = N.   a : rows = M.
  *   y : device, [M][ldy] fp32 or bf16 (y_dtype; bf16 is rounded once, at the end),
  *       ldy >= N, aligned to its element.
- * w->K must equal a->K and the rotation tags must agree (W4A4_ERR_MISMATCH).  No
- * workspace; the order of every sum is fixed, so equal inputs give equal bits.
+ *   ws: optional device workspace (NULL, or mxfp4_gemm_workspace_bytes(M, N, K) bytes or
+ *       more, 16-byte aligned, its first 64 KiB zero before its first use; a smaller
+ *       one is W4A4_ERR_WORKSPACE).  With it, shapes whose tiles would leave SMs idle in
+ *       the last wave cut that wave's K work evenly over the SMs; a tile cut in two is
+ *       summed first part + second part.  Every call leaves the workspace as it needs
+ *       to find it; after W4A4_ERR_TIMEOUT, zero it before reuse.  Calls that share one
+ *       must not overlap on the GPU.
+ * w->K must equal a->K and the rotation tags must agree (W4A4_ERR_MISMATCH).  The order
+ * of every sum is fixed on a given device, with and without a workspace: equal inputs
+ * give equal bits.
  */
-w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy,
-                       w4a4_stream_t stream);
+w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy, void* ws,
+                       size_t ws_bytes, w4a4_stream_t stream);
+
+/* Workspace bytes for mxfp4_gemm at this shape on the current device; 0 when it would
+ * not use one. */
+size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
  * Residual addition + RMS norm + rotation + quantisation, in one pass: what stands

@@ -168,6 +168,25 @@ def test_product(dev, M, K, N, out):
     assert bool((y[0] == 7).all()) and bool((y[-1] == 7).all()) and bool((y[:, N:] == 7).all())
 
 
+# more tiles than CTA pairs (76 on a GB300), the last wave mostly empty: its stages are
+# cut over the pairs; with whole waves in front of it and without, ragged in M, N and K
+@pytest.mark.parametrize("M,K,N", [(200, 2336, 19500), (300, 2592, 29200), (257, 8224, 10100)])
+def test_product_with_the_last_wave_cut(dev, M, K, N):
+    assert w4.mxfp4_gemm_workspace_bytes(M, N, K) > 0
+    gen = torch.Generator("cuda").manual_seed(M)
+    w, x = (torch.randn(r, K, device=dev, generator=gen) for r in (N, M))
+    qw, qa = w4.mxfp4_rotate_quantize(w * 0.02), w4.mxfp4_rotate_quantize(x)
+    W, A = w4.mxfp4_dequantize(qw).double(), w4.mxfp4_dequantize(qa).double()
+    R, tol = A @ W.T, K * 2.0 ** -23 * (A.abs() @ W.abs().T)
+    y = w4.mxfp4_gemm(qw, qa)
+    assert bool(((y.double() - R).abs() <= tol).all())
+    assert bool(((w4.mxfp4_gemm(qw, qa, ws=False).double() - R).abs() <= tol).all())
+    for _ in range(3):  # the workspace is left as it was found, and the sums' order is fixed
+        assert torch.equal(w4.mxfp4_gemm(qw, qa), y)
+    assert torch.equal(w4.mxfp4_gemm(qw, qa, dtype=torch.bfloat16), y.to(torch.bfloat16))
+    w4.w4a4_check()
+
+
 def test_product_does_not_depend_on_what_ran_before(dev):
     qw, qa = operands(dev, 200, 1056, 300)
     y = w4.mxfp4_gemm(qw, qa)
