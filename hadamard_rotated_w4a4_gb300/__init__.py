@@ -671,37 +671,52 @@ def w4a16_gemm(w: Q4_0Weights, a: Act16, y: torch.Tensor | None = None, ws: torc
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-@dataclass
 class MxFp4:
-    """MXFP4 weights or activations in the library's layout: e2m1 codes [rows][K/2] (element 2i in the low
-    nibble of byte i) and the scale bytes in tiles of 128 rows x 4 blocks."""
-    codes: torch.Tensor
-    scales_buf: torch.Tensor  # uint8 scale tiles, [ceil(rows/128)][ceil(K/128)][512]
-    rows: int
-    K: int
-    rotated: bool
+    """MXFP4 weights or activations in the library's layout, in one buffer: e2m1 codes [rows][K/2] (element 2i
+    in the low nibble of byte i), then the scale bytes in tiles of 128 rows x 4 blocks (w4a4_mxfp4)."""
+
+    __slots__ = ("buf", "rows", "K", "_desc", "_at")
+
+    def __init__(self, rows: int, K: int, device, rotated: bool = True):
+        if K <= 0 or K % 32:
+            raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
+        nc = rows * (K // 2)  # a multiple of 16
+        self.buf = torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
+        self.rows, self.K = rows, K
+        ptr = self.buf.data_ptr()
+        self._desc = _Act4Desc(ptr, ptr + nc, rows, K, TAG_MXFP4 | (TAG_ROTATED if rotated else 0))
+        self._at = ctypes.addressof(self._desc)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self.buf[: self.rows * (self.K // 2)].view(self.rows, self.K // 2)
+
+    @property
+    def scales_buf(self) -> torch.Tensor:
+        """The scale tiles, uint8 [ceil(rows/128) * ceil(K/128) * 512]."""
+        return self.buf[self.rows * (self.K // 2):]
 
     @property
     def scales(self) -> torch.Tensor:
         """The scale bytes in row-major order, uint8 [rows][K/32] (a copy)."""
         rt, kt = (self.rows + 127) // 128, (self.K + 127) // 128
-        t = self.scales_buf[: rt * kt * 512].view(rt, kt, 32, 4, 4).permute(0, 3, 2, 1, 4)
+        t = self.scales_buf.view(rt, kt, 32, 4, 4).permute(0, 3, 2, 1, 4)
         return t.reshape(rt * 128, kt * 4)[: self.rows, : self.K // 32].contiguous()
 
     @property
+    def rotated(self) -> bool:
+        return bool(self._desc.tag & TAG_ROTATED)
+
+    @property
     def tag(self) -> int:
-        return TAG_MXFP4 | (TAG_ROTATED if self.rotated else 0)
+        return self._desc.tag
 
     def desc(self) -> _Act4Desc:
-        return _Act4Desc(self.codes.data_ptr(), self.scales_buf.data_ptr(), self.rows, self.K, self.tag)
+        return self._desc
 
 
 def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
-    if K <= 0 or K % 32:
-        raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device)
-    sbuf = torch.empty((rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
-    return MxFp4(codes, sbuf, rows, K, rotated)
+    return MxFp4(rows, K, device, rotated)
 
 
 def _rows(t: torch.Tensor, name: str, shape=None) -> int:
@@ -726,11 +741,9 @@ def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | Non
     """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
     ldx = _rows(x, "x")
     rows, K = x.shape
-    out = _out(out, alloc_mxfp4, rows, K, x.device, rotate)
-    d = out.desc()
-    _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, int(rotate),
-                                                ctypes.addressof(d), _stream(stream)))
-    out.rotated = bool(rotate)
+    out = _out(out, MxFp4, rows, K, x.device, rotate)
+    _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, rotate, out._at,
+                                                _stream(stream)))
     return out
 
 
@@ -744,39 +757,42 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
     rows, K = codes.shape[0], 2 * codes.shape[1]
     if K <= 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
         raise W4A4Error(1, "codes [rows][K/2] and scales [rows][K/32] disagree, or K is not a multiple of 32")
-    out = _out(out, alloc_mxfp4, rows, K, codes.device, rotated)
-    d = out.desc()
-    _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, int(rotated),
-                                       ctypes.addressof(d), _stream(stream)))
-    out.rotated = bool(rotated)
+    out = _out(out, MxFp4, rows, K, codes.device, rotated)
+    _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, rotated, out._at,
+                                       _stream(stream)))
     return out
 
 
-def _dequantize(fn: str, a, y, dtype, stream) -> torch.Tensor:
-    if y is None:
-        y = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device)
-    ldy = _rows(y, "y", (a.rows, a.K))
+def _dequantize(call, a, y, dtype, stream) -> torch.Tensor:
     d = a.desc()
-    _check(getattr(load_library(), fn)(ctypes.addressof(d), y.data_ptr(), _DTYPE[y.dtype], ldy, _stream(stream)))
+    if y is None:
+        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=_device(a)), a.K
+    else:
+        ldy = _rows(y, "y", (a.rows, a.K))
+    _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, _stream(stream)))
     return y
+
+
+def _device(a) -> torch.device:
+    return a.buf.device if isinstance(a, MxFp4) else a.codes.device
 
 
 def mxfp4_dequantize(a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                      stream=None) -> torch.Tensor:
     """The values that MXFP4 codes and scales stand for ([rows][K], fp32 or bf16; a rotation is not undone)."""
-    return _dequantize("mxfp4_dequantize", a, y, dtype, stream)
+    return _dequantize(load_library().mxfp4_dequantize, a, y, dtype, stream)
 
 
 def w4a4_dequantize_act(a: Act4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                         stream=None) -> torch.Tensor:
     """The values that int4 codes and scales stand for, as mxfp4_dequantize."""
-    return _dequantize("w4a4_dequantize_act", a, y, dtype, stream)
+    return _dequantize(load_library().w4a4_dequantize_act, a, y, dtype, stream)
 
 
 def w4a8_dequantize_act(a: Act8, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                         stream=None) -> torch.Tensor:
     """The values that int8 codes and scales stand for, as mxfp4_dequantize."""
-    return _dequantize("w4a8_dequantize_act", a, y, dtype, stream)
+    return _dequantize(load_library().w4a8_dequantize_act, a, y, dtype, stream)
 
 
 def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -791,41 +807,50 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     workspace (zero before its first use), None/False = whole tiles only.
     """
     if y is None:
-        y = torch.empty(a.rows, w.rows, dtype=dtype, device=w.codes.device)
-    ldy = _rows(y, "y", (a.rows, w.rows))
+        y, ldy = torch.empty(a.rows, w.rows, dtype=dtype, device=w.buf.device), w.rows
+    else:
+        ldy = _rows(y, "y", (a.rows, w.rows))
     lib, st = load_library(), _stream(stream)
     if ws is True:
         need = lib.mxfp4_gemm_workspace_bytes(a.rows, w.rows, w.K)
         ws = gemm_workspace(a.rows, w.rows, w.K, y.device, st, need) if need else None
-    ws_ptr, ws_bytes = (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None and ws is not False else (None, 0)
-    dw, da = w.desc(), a.desc()
-    _check(lib.mxfp4_gemm(ctypes.addressof(dw), ctypes.addressof(da), y.data_ptr(), _DTYPE[y.dtype], ldy, ws_ptr,
-                          ws_bytes, st))
+    ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(lib.mxfp4_gemm(w._at, a._at, y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, ws_ptr, ws_bytes, st))
     return y
 
 
-def _rmsnorm(fn: str, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
-    n = _RmsNorm(x=x.data_ptr(), ldx=_rows(x, "x"), x_dtype=_DTYPE.get(x.dtype, -1), M=x.shape[0], K=x.shape[1],
-                 rotate=int(rotate), eps=eps)
+def _finish(call, first, out, rotate, stream):
+    """Runs a fused quantiser into out and keeps its rotation tag."""
+    d = out.desc()
+    _check(call(*first, ctypes.addressof(d), _stream(stream)))
+    if not isinstance(out, MxFp4):  # an MxFp4's descriptor is its own, stamped by the call
+        out.rotated = bool(rotate)
+    return out
+
+
+def _rmsnorm(call, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
+    ldx = _rows(x, "x")
+    M, K = shape = x.shape
+    r = r_out = gp = None
+    ldr = ldr_out = r_dtype = g_dtype = 0
     if residual is not None:
-        if residual_out is None:
-            residual_out = residual
-        n.ldr, n.ldr_out = _rows(residual, "residual", x.shape), _rows(residual_out, "residual_out", x.shape)
-        if residual_out.dtype != residual.dtype:
-            raise ValueError("residual_out must have residual's type")
-        n.r, n.r_out, n.r_dtype = residual.data_ptr(), residual_out.data_ptr(), _DTYPE[residual.dtype]
+        ldr = ldr_out = _rows(residual, "residual", shape)
+        r, r_dtype = residual.data_ptr(), _DTYPE[residual.dtype]
+        r_out = r
+        if residual_out is not None:
+            ldr_out = _rows(residual_out, "residual_out", shape)
+            if residual_out.dtype != residual.dtype:
+                raise ValueError("residual_out must have residual's type")
+            r_out = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if g is not None:
         _cuda(g, "g")
-        if g.dtype not in _DTYPE or g.dim() != 1 or g.shape[0] != x.shape[1] or not g.is_contiguous():
+        if g.dtype not in _DTYPE or g.dim() != 1 or g.shape[0] != K or not g.is_contiguous():
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
-        n.g, n.g_dtype = g.data_ptr(), _DTYPE[g.dtype]
-    out = _out(out, alloc, x.shape[0], x.shape[1], x.device, rotate)
-    d = out.desc()
-    _check(getattr(load_library(), fn)(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
-    out.rotated = bool(rotate)
-    return out
+        gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
+    n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
+    return _finish(call, (ctypes.addressof(n),), _out(out, alloc, M, K, x.device, rotate), rotate, stream)
 
 
 def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
@@ -836,49 +861,45 @@ def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, ep
     x, residual: [M][K], bf16 or fp32 each.  h is written to residual_out, in place into
     residual when that is None; without a residual, h = x and nothing is written.
     """
-    return _rmsnorm("w4a4_rmsnorm_quantize_act", alloc_act4, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().w4a4_rmsnorm_quantize_act, alloc_act4, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
 def w4a8_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
                               residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
                               rotate: bool = True, out: Act8 | None = None, stream=None) -> Act8:
     """As w4a4_rmsnorm_quantize_act, to int8 codes."""
-    return _rmsnorm("w4a8_rmsnorm_quantize_act", alloc_act8, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().w4a8_rmsnorm_quantize_act, alloc_act8, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
                            residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
                            rotate: bool = True, out: MxFp4 | None = None, stream=None) -> MxFp4:
     """As w4a4_rmsnorm_quantize_act, to MXFP4."""
-    return _rmsnorm("mxfp4_rmsnorm_quantize", alloc_mxfp4, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().mxfp4_rmsnorm_quantize, MxFp4, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
-def _swiglu(fn: str, alloc, gate, up, rotate, out, stream):
+def _swiglu(call, alloc, gate, up, rotate, out, stream):
     ldg, ldu = _rows(gate, "gate"), _rows(up, "up", gate.shape)
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    out = _out(out, alloc, M, K, gate.device, rotate)
-    d = out.desc()
-    _check(getattr(load_library(), fn)(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, int(rotate),
-                                       ctypes.addressof(d), _stream(stream)))
-    out.rotated = bool(rotate)
-    return out
+    first = (gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate)
+    return _finish(call, first, _out(out, alloc, M, K, gate.device, rotate), rotate, stream)
 
 
 def w4a4_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act4 | None = None,
                              stream=None) -> Act4:
     """y = silu(gate) * up (both [M][K], bf16 or fp32), rotated and rounded to int4, in one pass."""
-    return _swiglu("w4a4_swiglu_quantize_act", alloc_act4, gate, up, rotate, out, stream)
+    return _swiglu(load_library().w4a4_swiglu_quantize_act, alloc_act4, gate, up, rotate, out, stream)
 
 
 def w4a8_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act8 | None = None,
                              stream=None) -> Act8:
     """As w4a4_swiglu_quantize_act, to int8 codes."""
-    return _swiglu("w4a8_swiglu_quantize_act", alloc_act8, gate, up, rotate, out, stream)
+    return _swiglu(load_library().w4a8_swiglu_quantize_act, alloc_act8, gate, up, rotate, out, stream)
 
 
 def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: MxFp4 | None = None,
                           stream=None) -> MxFp4:
     """As w4a4_swiglu_quantize_act, to MXFP4."""
-    return _swiglu("mxfp4_swiglu_quantize", alloc_mxfp4, gate, up, rotate, out, stream)
+    return _swiglu(load_library().mxfp4_swiglu_quantize, MxFp4, gate, up, rotate, out, stream)
