@@ -114,18 +114,20 @@ __device__ __forceinline__ void quad_rotate(float (&v)[8], int q) {
   for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], make_float2(c_h32(), c_h32()));
 }
 
-// max |v| over the block's four lanes; NaN if any element is NaN.
-__device__ __forceinline__ float max_nan2(float a, float b) {
+// max |v| over this lane's eight values, then over the block's four lanes; NaN if any
+// element is NaN.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float lane_amax(const float (&v)[8]) {
+  return max3_abs(max3_abs(max3_abs(v[0], v[1], v[2]), v[3], v[4]), max3_abs(v[5], v[6], v[7]), 0.0f);
+}
 __device__ __forceinline__ float quad_amax(const float (&v)[8]) {
-  float a = fabsf(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) a = max_nan2(a, fabsf(v[i]));
-  a = max_nan2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-  return max_nan2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+  float a = lane_amax(v);
+  a = max3_abs(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1), 0.0f);
+  return max3_abs(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2), 0.0f);
 }
 
 // ---------------------------------------------------------------- code formats
@@ -216,17 +218,18 @@ __device__ __forceinline__ void quad_quantize(float (&v)[8], int q, bool ok, I c
     // unless some v lies halfway (or is NaN); then the general path rounds.
     constexpr float kMagic = 12582912.0f;
     uint32_t t[8], w[2];
-    float m = 0.0f;
+    float x[8];  // v - nearest
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 s = __fadd2_rn(v2[i], make_float2(kMagic, kMagic));
       const float2 r = __fadd2_rn(s, make_float2(-kMagic, -kMagic));
-      const float2 x = sub2(v2[i], r);
-      m = max_nan2(m, max_nan2(fabsf(x.x), fabsf(x.y)));
+      const float2 dx = sub2(v2[i], r);
+      x[2 * i] = dx.x;
+      x[2 * i + 1] = dx.y;
       t[2 * i] = __float_as_uint(s.x);
       t[2 * i + 1] = __float_as_uint(s.y);
     }
-    if (m < 0.5f && inv <= 3.402823466e38f) {
+    if (lane_amax(x) < 0.5f && inv <= 3.402823466e38f) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         w[h] = prmt(prmt(t[4 * h], t[4 * h + 1], 0x0040u), prmt(t[4 * h + 2], t[4 * h + 3], 0x0040u), 0x5410u);
