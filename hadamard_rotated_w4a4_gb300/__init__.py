@@ -525,35 +525,81 @@ def w4a4_gemm_id_status(ws: torch.Tensor, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- the exact path (int8 activations)
-@dataclass
-class Act8:
-    """int8 activations of the exact path: codes int8 [rows][K] (element order), scales fp32 [rows][K/32]."""
-    codes: torch.Tensor
-    scales_buf: torch.Tensor
-    rows: int
-    K: int
-    rotated: bool
+class _Held:
+    """An operand that keeps its C descriptor: the calls take its address and stamp rows, K and tag into it."""
+
+    __slots__ = ("rows", "K", "_desc", "_at")
+
+    def _hold(self, codes_ptr: int, scales_ptr: int, rows: int, K: int, tag: int, rotated: bool) -> None:
+        self.rows, self.K = rows, K
+        self._desc = _Act4Desc(codes_ptr, scales_ptr, rows, K, tag | TAG_ROTATED if rotated else tag)
+        self._at = ctypes.addressof(self._desc)
+
+    @property
+    def tag(self) -> int:
+        return self._desc.tag
+
+    @property
+    def rotated(self) -> bool:
+        return bool(self._desc.tag & TAG_ROTATED)
+
+    @rotated.setter
+    def rotated(self, value: bool) -> None:
+        self._desc.tag = (self._desc.tag & ~TAG_ROTATED) | (TAG_ROTATED if value else 0)
+
+    def desc(self) -> _Act4Desc:
+        return self._desc
+
+
+class Act8(_Held):
+    """int8 activations of the exact path: codes int8 [rows][K] (element order), scales fp32 [rows][K/32].
+
+    Act8(codes, scales_buf, rows, K, rotated) wraps two buffers; alloc_act8 makes one that holds both.
+    """
+
+    __slots__ = ("_buf", "_codes", "_scales_buf")
+
+    def __init__(self, codes: torch.Tensor, scales_buf: torch.Tensor, rows: int, K: int, rotated: bool):
+        self._buf, self._codes, self._scales_buf = None, codes, scales_buf
+        self._hold(codes.data_ptr(), scales_buf.data_ptr(), rows, K, TAG_ACT8, rotated)
+
+    @classmethod
+    def _alloc(cls, rows: int, K: int, device, rotated: bool) -> "Act8":
+        if K <= 0 or K % 32:
+            raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
+        self = cls.__new__(cls)
+        n = rows * K  # then K/32 fp32 scales a row, and a pad to 16 bytes
+        self._buf = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device)
+        self._codes = self._scales_buf = None
+        ptr = self._buf.data_ptr()
+        self._hold(ptr, ptr + n, rows, K, TAG_ACT8, rotated)
+        return self
+
+    @property
+    def device(self) -> torch.device:
+        return (self._codes if self._buf is None else self._buf).device
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._buf[: self.rows * self.K].view(self.rows, self.K)
+        return self._codes
+
+    @property
+    def scales_buf(self) -> torch.Tensor:
+        """uint8 buffer (padded to 16 bytes) holding the fp32 scales."""
+        if self._scales_buf is None:
+            self._scales_buf = self._buf[self.rows * self.K:].view(torch.uint8)
+        return self._scales_buf
 
     @property
     def scales(self) -> torch.Tensor:
         n = self.rows * (self.K // 32)
         return self.scales_buf[: 4 * n].view(torch.float32).view(self.rows, self.K // 32)
 
-    @property
-    def tag(self) -> int:
-        return TAG_ACT8 | (TAG_ROTATED if self.rotated else 0)
-
-    def desc(self) -> _Act4Desc:
-        return _Act4Desc(self.codes.data_ptr(), self.scales_buf.data_ptr(), self.rows, self.K, self.tag)
-
 
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
-    lib = load_library()
-    if K <= 0 or K % 32:
-        raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-    codes = torch.empty(rows, K, dtype=torch.int8, device=device)
-    sbuf = torch.empty(max(lib.w4a4_act8_scales_bytes(rows, K), 16), dtype=torch.uint8, device=device)
-    return Act8(codes, sbuf, rows, K, rotated)
+    return Act8._alloc(rows, K, device, rotated)
 
 
 def w4a8_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act8 | None = None, stream=None) -> Act8:
@@ -671,21 +717,23 @@ def w4a16_gemm(w: Q4_0Weights, a: Act16, y: torch.Tensor | None = None, ws: torc
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-class MxFp4:
+class MxFp4(_Held):
     """MXFP4 weights or activations in the library's layout, in one buffer: e2m1 codes [rows][K/2] (element 2i
     in the low nibble of byte i), then the scale bytes in tiles of 128 rows x 4 blocks (w4a4_mxfp4)."""
 
-    __slots__ = ("buf", "rows", "K", "_desc", "_at")
+    __slots__ = ("buf",)
 
     def __init__(self, rows: int, K: int, device, rotated: bool = True):
         if K <= 0 or K % 32:
             raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
         nc = rows * (K // 2)  # a multiple of 16
         self.buf = torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
-        self.rows, self.K = rows, K
         ptr = self.buf.data_ptr()
-        self._desc = _Act4Desc(ptr, ptr + nc, rows, K, TAG_MXFP4 | (TAG_ROTATED if rotated else 0))
-        self._at = ctypes.addressof(self._desc)
+        self._hold(ptr, ptr + nc, rows, K, TAG_MXFP4, rotated)
+
+    @property
+    def device(self) -> torch.device:
+        return self.buf.device
 
     @property
     def codes(self) -> torch.Tensor:
@@ -703,17 +751,6 @@ class MxFp4:
         t = self.scales_buf.view(rt, kt, 32, 4, 4).permute(0, 3, 2, 1, 4)
         return t.reshape(rt * 128, kt * 4)[: self.rows, : self.K // 32].contiguous()
 
-    @property
-    def rotated(self) -> bool:
-        return bool(self._desc.tag & TAG_ROTATED)
-
-    @property
-    def tag(self) -> int:
-        return self._desc.tag
-
-    def desc(self) -> _Act4Desc:
-        return self._desc
-
 
 def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
     return MxFp4(rows, K, device, rotated)
@@ -721,12 +758,14 @@ def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
 
 def _rows(t: torch.Tensor, name: str, shape=None) -> int:
     """Checks a 2-D CUDA operand (bf16 or fp32, unit stride along K) and returns its row stride."""
-    _cuda(t, name)
-    if t.dtype not in _DTYPE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    st = t.stride()
+    if not t.is_cuda or t.dtype not in _DTYPE or len(st) != 2 or (st[1] != 1 and t.shape[1] > 1):
+        _cuda(t, name)
         raise ValueError(f"{name} must be a 2-D bf16 or fp32 tensor with unit stride along its rows")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row's stride is meaningless (may be 0)
+    M, K = t.shape
+    return st[0] if M > 1 else K  # a single row's stride is meaningless (may be 0)
 
 
 def _out(out, alloc, rows: int, K: int, device, rotate: bool):
@@ -766,15 +805,11 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
 def _dequantize(call, a, y, dtype, stream) -> torch.Tensor:
     d = a.desc()
     if y is None:
-        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=_device(a)), a.K
+        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device if isinstance(a, Act4) else a.device), a.K
     else:
-        ldy = _rows(y, "y", (a.rows, a.K))
-    _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, _stream(stream)))
+        ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
+    _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(dtype, -1), ldy, _stream(stream)))
     return y
-
-
-def _device(a) -> torch.device:
-    return a.buf.device if isinstance(a, MxFp4) else a.codes.device
 
 
 def mxfp4_dequantize(a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
@@ -819,11 +854,8 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     return y
 
 
-def _finish(call, first, out, rotate, stream):
-    """Runs a fused quantiser into out and keeps its rotation tag."""
-    d = out.desc()
-    _check(call(*first, ctypes.addressof(d), _stream(stream)))
-    if not isinstance(out, MxFp4):  # an MxFp4's descriptor is its own, stamped by the call
+def _tagged(out, rotate):
+    if isinstance(out, Act4):  # the other operands' descriptors are their own, stamped by the call
         out.rotated = bool(rotate)
     return out
 
@@ -850,7 +882,10 @@ def _rmsnorm(call, alloc, x, g, residual, residual_out, eps, rotate, out, stream
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
         gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
     n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
-    return _finish(call, (ctypes.addressof(n),), _out(out, alloc, M, K, x.device, rotate), rotate, stream)
+    out = _out(out, alloc, M, K, x.device, rotate)
+    d = out.desc()
+    _check(call(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
+    return _tagged(out, rotate)
 
 
 def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
@@ -883,8 +918,11 @@ def _swiglu(call, alloc, gate, up, rotate, out, stream):
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    first = (gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate)
-    return _finish(call, first, _out(out, alloc, M, K, gate.device, rotate), rotate, stream)
+    out = _out(out, alloc, M, K, gate.device, rotate)
+    d = out.desc()
+    _check(call(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate, ctypes.addressof(d),
+                _stream(stream)))
+    return _tagged(out, rotate)
 
 
 def w4a4_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act4 | None = None,

@@ -686,7 +686,7 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
   // Whole tiles leave the pairs idle for the unused part of the last wave.  Cutting the
   // last wave and what is left by stages instead costs a deposit and a pick-up, about
   // kCutStages of MMAs.
-  constexpr int kCutStages = 8;
+  constexpr int kCutStages = 28;
   const int64_t waves = (q.tiles + pairs - 1) / pairs;
   if (q.tiles > pairs && (waves * pairs - q.tiles) * stages > kCutStages * pairs) {
     q.whole = static_cast<int>((waves - 2) * pairs);
