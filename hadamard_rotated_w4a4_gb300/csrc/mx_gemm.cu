@@ -46,7 +46,7 @@ struct MxArgs {
   int box;      // token rows of one load
   // pair kernel
   int mtok;     // tokens of a tile, 128 or 256 (the last one of a row narrower)
-  int mt;       // token tiles
+  int mt, wt;   // token tiles, weight tiles
   int tiles;
   int whole;    // tiles 0 .. whole - 1 go to the pairs whole, in turn; the rest by stages
   int64_t units;     // stages of the rest (0: none)
@@ -364,8 +364,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
   } else {
-    // rank r sums and writes tokens r * share .. ; split and share are powers of two
+    // rank r sums and writes tokens r * share ..; share is a power of two, 4 at least.
+    // Partials: [rank][share / 4][128 rows][4 tokens], 16 bytes a lane.
     const int share = NT / split, log = 31 - __clz(share);
+    const uint32_t mine = smem + 16u * (rank * (share / 4) * kTW + 32 * (warp & 3) + lane);
     cluster_sync();  // every CTA's operand stages are free
     if (whole)
 #pragma unroll
@@ -376,24 +378,25 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-          if (c + i < tok) {
-            const int to = (c + i) >> log, slot = (c + i) & (share - 1);
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(
-                             map_rank(smem + 4u * ((rank * share + slot) * kTW + 32 * warp + lane), to)),
-                         "r"(r[i])
+        for (int i = 0; i < NC; i += 4)
+          if (c + i < tok)
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             map_rank(mine + 16u * ((((c + i) & (share - 1)) >> 2) * kTW), (c + i) >> log)),
+                         "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
                          : "memory");
-          }
       }
     cluster_sync();
-    if (whole && n < p.N) {
-      const float* part = reinterpret_cast<const float*>(raw + (smem - su32(raw))) + 32 * warp + lane;
-      for (int i = 0; i < share && rank * share + i < tok; ++i) {
-        float v = part[i * kTW];
-        for (int r = 1; r < split; ++r) v = __fadd_rn(v, part[(r * share + i) * kTW]);
-        const int64_t at = static_cast<int64_t>(rank * share + i) * p.ldy + n;
-        if (BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
-        else static_cast<float*>(p.y)[at] = v;
+    if (whole) {
+      const uint8_t* part = raw + (smem - su32(raw)) + 16 * (32 * warp + lane);
+      for (int i = 0; i < share && rank * share + i < tok; i += 4) {
+        float4 v = *reinterpret_cast<const float4*>(part + 16 * ((i >> 2) * kTW));
+        for (int q = 1; q < split; ++q) {
+          const float4 o = *reinterpret_cast<const float4*>(part + 16 * ((q * (share >> 2) + (i >> 2)) * kTW));
+          v = make_float4(__fadd_rn(v.x, o.x), __fadd_rn(v.y, o.y), __fadd_rn(v.z, o.z), __fadd_rn(v.w, o.w));
+        }
+        const uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+        const int64_t m = static_cast<int64_t>(rank) * share + i;
+        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
       }
     }
   }
@@ -412,6 +415,12 @@ constexpr int kPairSfCols = 8 + 8 * kPairAtoms;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes;
 constexpr int kPairThreads = 320;  // 8 epilogue warps, a copy warp, an MMA warp
 static_assert(kMaxTok + kPairStages * kPairSfCols <= 512, "TMEM columns");
+
+// Weight and token tile of tile t.  Whole tiles: tokens first, so that the pairs at work
+// share few weight tiles.  With every tile's stages cut, weights first: pairs a token
+// tile apart then read the same weights at the same time.
+__device__ __forceinline__ int tile_w(const MxArgs& p, int t) { return p.whole == 0 ? t % p.wt : t / p.mt; }
+__device__ __forceinline__ int tile_m(const MxArgs& p, int t) { return p.whole == 0 ? t / p.wt : t % p.mt; }
 
 // Tokens of the tile at m0 that the MMA computes: a multiple of 32, whose halves are
 // whole 8-row swizzle atoms.
@@ -450,9 +459,8 @@ struct Work {
   }
 };
 
-// Persistent; tile t is weight rows 256 (t / mt), tokens mtok (t % mt).  CTA `rank` of
-// the pair holds weight rows 128 rank .. of the tile, one half of its tokens as its
-// part of the N operand, and every token's scales.
+// Persistent.  CTA `rank` of the pair holds weight rows 128 rank .. of the tile, one
+// half of its tokens as its part of the N operand, and every token's scales.
 template <bool BF16>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
@@ -498,8 +506,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
       int it = 0;
       for (; !S.abort && more; more = work.next(p)) {
-        const int32_t w0 = work.tile / p.mt * 256 + static_cast<int32_t>(rank) * kTW;
-        const int32_t m0 = work.tile % p.mt * p.mtok;
+        const int32_t w0 = tile_w(p, work.tile) * 256 + static_cast<int32_t>(rank) * kTW;
+        const int32_t m0 = tile_m(p, work.tile) * p.mtok;
         const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
         for (int s = work.s0; s < work.s1; ++s, ++it) {
           const int st = it % kPairStages;
@@ -523,7 +531,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     if (rank == 0 && elect_one()) {
       int it = 0, seg = 0;
       for (; !S.abort && more; more = work.next(p)) {
-        const uint32_t idesc = mx_idesc(2, tile_tok(p, work.tile % p.mt * p.mtok));
+        const uint32_t idesc = mx_idesc(2, tile_tok(p, tile_m(p, work.tile) * p.mtok));
         if (seg > 0 && !wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err)) break;
         ++seg;
         tc_fence_after();
@@ -608,8 +616,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (lane == 0) p.flags[at] = 0u;
       }
-      const int64_t n = work.tile / p.mt * 256 + rank * kTW + 32 * (warp & 3) + lane;
-      const int64_t m0 = work.tile % p.mt * p.mtok + 128 * (warp >> 2);
+      const int64_t n = static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3) + lane;
+      const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * p.mtok + 128 * (warp >> 2);
       if (128 * (warp >> 2) < p.mtok)
         store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
                          static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
@@ -658,10 +666,10 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
   using C = Small<NT>;
   static bool configured[2][64] = {};
   const int64_t tiles = (a.N + kTW - 1) / kTW;
-  // K shared by as many CTAs (a power of two up to 8) as have two stages each and fit
-  // the SMs' two slots
+  // K shared by as many CTAs (a power of two up to 8, a quarter of the tokens at most) as
+  // have two stages each and fit the SMs' two slots
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && a.stages >= split * 4) split *= 2;
+  while (split < (NT < 32 ? NT / 4 : 8) && tiles * split * 2 <= 2 * num_sms() && a.stages >= split * 4) split *= 2;
   const dim3 grid(split, static_cast<unsigned>(tiles));
   return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, C::kSmem, split, m, a, st)
                 : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, C::kSmem, split, m, a, st);
@@ -715,7 +723,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
     a.box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   } else {
     q = plan_pair(M, N, K);
-    a.mtok = q.mtok; a.mt = q.mt; a.tiles = q.tiles; a.whole = q.tiles;
+    a.mtok = q.mtok; a.mt = q.mt; a.wt = static_cast<int>((N + 255) / 256); a.tiles = q.tiles; a.whole = q.tiles;
     if (ws && q.units > 0) {
       a.whole = q.whole;
       a.units = q.units;
