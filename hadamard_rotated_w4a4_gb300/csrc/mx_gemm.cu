@@ -435,13 +435,15 @@ __device__ __forceinline__ int tile_tok(const MxArgs& p, int m0) {
 struct Work {
   int tile, s0, s1;  // the segment: stages [s0, s1) of a tile
   int step;
-  int64_t lo, hi;
+  int cut_tile, cut_s0;  // where the range goes on
+  int64_t left;          // its stages still to come
   __device__ __forceinline__ Work(const MxArgs& p, int pair, int pairs) : tile(pair - pairs), s0(0), s1(0), step(pairs) {
     // a pair that waits for a tail waits for one that started before it: ranges in
     // descending order of the pair's number
-    const int64_t at = pairs - 1 - pair;
-    lo = p.units * at / pairs;
-    hi = p.units * (at + 1) / pairs;
+    const int64_t at = pairs - 1 - pair, lo = p.units * at / pairs;
+    left = p.units * (at + 1) / pairs - lo;
+    cut_tile = p.whole + static_cast<int>(lo / p.stages);
+    cut_s0 = static_cast<int>(lo % p.stages);
   }
   __device__ __forceinline__ bool next(const MxArgs& p) {
     if (tile + step < p.whole) {
@@ -449,12 +451,13 @@ struct Work {
       s1 = p.stages;
       return true;
     }
-    if (lo >= hi) return false;
+    if (left <= 0) return false;
     step = p.whole;  // no whole tile follows
-    tile = p.whole + static_cast<int>(lo / p.stages);
-    s0 = static_cast<int>(lo % p.stages);
-    s1 = static_cast<int>(min(static_cast<int64_t>(p.stages), s0 + (hi - lo)));
-    lo += s1 - s0;
+    tile = cut_tile++;
+    s0 = cut_s0;
+    cut_s0 = 0;
+    s1 = static_cast<int>(min(static_cast<int64_t>(p.stages), s0 + left));
+    left -= s1 - s0;
     return true;
   }
 };
