@@ -259,6 +259,10 @@ class Act4:
     def tag(self) -> int:
         return TAG_ACT4 | (TAG_ROTATED if self.rotated else 0)
 
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
     def head(self, rows: int) -> "Act4":
         """The first `rows` rows (views of the same buffers)."""
         return Act4(self.codes[:rows], self.scales_buf, rows, self.K, self.rotated, self.expanded)
@@ -563,18 +567,6 @@ class Act8(_Held):
         self._buf, self._codes, self._scales_buf = None, codes, scales_buf
         self._hold(codes.data_ptr(), scales_buf.data_ptr(), rows, K, TAG_ACT8, rotated)
 
-    @classmethod
-    def _alloc(cls, rows: int, K: int, device, rotated: bool) -> "Act8":
-        if K <= 0 or K % 32:
-            raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-        self = cls.__new__(cls)
-        n = rows * K  # then K/32 fp32 scales a row, and a pad to 16 bytes
-        self._buf = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device)
-        self._codes = self._scales_buf = None
-        ptr = self._buf.data_ptr()
-        self._hold(ptr, ptr + n, rows, K, TAG_ACT8, rotated)
-        return self
-
     @property
     def device(self) -> torch.device:
         return (self._codes if self._buf is None else self._buf).device
@@ -599,7 +591,15 @@ class Act8(_Held):
 
 
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
-    return Act8._alloc(rows, K, device, rotated)
+    if K <= 0 or K % 32:
+        raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
+    a = Act8.__new__(Act8)
+    n = rows * K  # then K/32 fp32 scales a row, and a pad to 16 bytes
+    a._buf = buf = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device)
+    a._codes = a._scales_buf = None
+    ptr = buf.data_ptr()
+    a._hold(ptr, ptr + n, rows, K, TAG_ACT8, rotated)
+    return a
 
 
 def w4a8_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act8 | None = None, stream=None) -> Act8:
@@ -768,9 +768,7 @@ def _rows(t: torch.Tensor, name: str, shape=None) -> int:
     return st[0] if M > 1 else K  # a single row's stride is meaningless (may be 0)
 
 
-def _out(out, alloc, rows: int, K: int, device, rotate: bool):
-    if out is None:
-        return alloc(rows, K, device, rotate)
+def _fits(out, rows: int, K: int):
     if out.rows != rows or out.K != K:
         raise ValueError(f"out holds [{out.rows}][{out.K}], the result is [{rows}][{K}]")
     return out
@@ -780,7 +778,7 @@ def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | Non
     """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
     ldx = _rows(x, "x")
     rows, K = x.shape
-    out = _out(out, MxFp4, rows, K, x.device, rotate)
+    out = MxFp4(rows, K, x.device, rotate) if out is None else _fits(out, rows, K)
     _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, rotate, out._at,
                                                 _stream(stream)))
     return out
@@ -796,18 +794,18 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
     rows, K = codes.shape[0], 2 * codes.shape[1]
     if K <= 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
         raise W4A4Error(1, "codes [rows][K/2] and scales [rows][K/32] disagree, or K is not a multiple of 32")
-    out = _out(out, MxFp4, rows, K, codes.device, rotated)
+    out = MxFp4(rows, K, codes.device, rotated) if out is None else _fits(out, rows, K)
     _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, rotated, out._at,
                                        _stream(stream)))
     return out
 
 
 def _dequantize(call, a, y, dtype, stream) -> torch.Tensor:
-    d = a.desc()
     if y is None:
-        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device if isinstance(a, Act4) else a.device), a.K
+        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=a.device), a.K
     else:
         ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
+    d = a.desc()
     _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(dtype, -1), ldy, _stream(stream)))
     return y
 
@@ -877,12 +875,12 @@ def _rmsnorm(call, alloc, x, g, residual, residual_out, eps, rotate, out, stream
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if g is not None:
-        _cuda(g, "g")
-        if g.dtype not in _DTYPE or g.dim() != 1 or g.shape[0] != K or not g.is_contiguous():
+        if not g.is_cuda or g.dtype not in _DTYPE or g.shape != (K,) or g.stride(0) != 1:
+            _cuda(g, "g")
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
         gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
     n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
-    out = _out(out, alloc, M, K, x.device, rotate)
+    out = alloc(M, K, x.device, rotate) if out is None else _fits(out, M, K)
     d = out.desc()
     _check(call(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
     return _tagged(out, rotate)
@@ -918,7 +916,7 @@ def _swiglu(call, alloc, gate, up, rotate, out, stream):
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    out = _out(out, alloc, M, K, gate.device, rotate)
+    out = alloc(M, K, gate.device, rotate) if out is None else _fits(out, M, K)
     d = out.desc()
     _check(call(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate, ctypes.addressof(d),
                 _stream(stream)))
