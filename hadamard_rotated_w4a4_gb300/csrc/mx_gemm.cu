@@ -44,6 +44,7 @@ struct MxArgs {
   int64_t M, N;
   int K, stages;
   int box;      // token rows of one load
+  int ring;     // small kernel: stages in shared memory
   // pair kernel
   int mtok;     // tokens of a tile, 128 or 256 (the last one of a row narrower)
   int mt, wt;   // token tiles, weight tiles
@@ -56,7 +57,7 @@ struct MxArgs {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], acc_full, acc_empty;
+  uint64_t full[12], empty[12], acc_full, acc_empty;
   uint32_t tmem;
   volatile int abort;
 };
@@ -89,7 +90,10 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
 }
 
 // One lane of the converged warp; the compiler knows that a single thread runs what
-// it guards (a lane test instead costs about 100 cycles per copy or MMA issued).
+// it guards.  The copy and MMA loops are run by their whole warps and elect a lane for
+// the instructions alone, so that addresses, descriptors and columns stay in uniform
+// registers: a lane test around the loop costs about 100 cycles per copy or MMA, an
+// election around it 33 (M1024 K17408 N5120 35.7 us, against 31.6 with the loop uniform).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -181,7 +185,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // of 128 rows.  kAtoms: token scale tiles per 128 of K.
 template <int CG, int kAtoms>
 __device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t wsm, uint32_t asm_, uint32_t sfsm, uint32_t sfw,
-                                           uint32_t idesc, int steps, uint32_t& acc) {
+                                           uint32_t idesc, int steps, uint32_t acc) {
   const uint32_t sfa = sfw + 8;
   const uint64_t base = (static_cast<uint64_t>(1) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
                         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);  // as kmajor_desc_sw128
@@ -199,8 +203,7 @@ __device__ __forceinline__ void stage_mmas(uint32_t d, uint32_t wsm, uint32_t as
           sf_copy<CG>(sfa + 4 * (j * kAtoms + t), sfsm + kSfTile + t * kSfTile + 512 * j);
       }
       mma_mx<CG>(d, wd + 2 * k, ad + 2 * k, (k & 1) ? idesc | kSfHigh : idesc, sfw + 4 * (k >> 1),
-                 sfa + 4 * (k >> 1) * kAtoms, acc);
-      acc = 1;
+                 sfa + 4 * (k >> 1) * kAtoms, k > 0 ? 1u : acc);
     }
   }
 }
@@ -264,14 +267,17 @@ __device__ __forceinline__ void store_cols(const uint32_t (&r)[NC], void* y, int
 template <int NT>
 struct Small {
   static constexpr int kStageBytes = kWBytes + NT * 128 + 2 * kSfTile;
-  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;  // two CTAs an SM
-  static constexpr int kSfCols = 16;
-  static constexpr int kCols = NT + kSfCols * kStages <= 128 ? 128 : 256;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes;
+  // stages in flight with two CTAs an SM, and with one
+  static constexpr int kRing2 = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr int kRing1 = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 6;
+  static constexpr int kSfCols = 16, kCols = 256;  // TMEM columns of a stage's scales, of the CTA
+  // the stages, or the partial tiles that the CTAs of a split exchange
+  static constexpr int smem(int ring) { return 1024 + (ring * kStageBytes > NT * 512 ? ring * kStageBytes : NT * 512); }
+  static_assert(kRing1 <= 12 && NT + kRing1 * kSfCols <= kCols && smem(kRing1) <= 227 * 1024 && smem(kRing2) <= 113 * 1024);
 };
 constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
 
-// grid (S, weight tiles), cluster (S, 1, 1).
+// grid (S, weight tiles, token tiles), cluster (S, 1, 1).
 template <int NT, bool BF16>
 __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                     const __grid_constant__ CUtensorMap amap,
@@ -282,9 +288,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   extern __shared__ uint8_t raw[];
   const uint32_t smem = (su32(raw) + 1023u) & ~1023u;
   __shared__ Bars S;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTW;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTW, m0 = static_cast<int64_t>(blockIdx.z) * NT;
   const int s0 = static_cast<int>(static_cast<int64_t>(p.stages) * rank / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / split);
   constexpr uint32_t kTx = C::kStageBytes;
@@ -293,15 +299,15 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     mbar_expect_tx(&S.full[st], kTx);
     load_2d<1>(base, &wmap, s * 128, static_cast<int32_t>(n0), bar);
     load_2d<1>(base + kWBytes + NT * 128, &wsmap, s * 256, static_cast<int32_t>(blockIdx.y), bar);
-    load_2d<1>(base + kWBytes, &amap, s * 128, 0, bar);
-    load_2d<1>(base + kWBytes + NT * 128 + kSfTile, &asmap, s * 256, 0, bar);
+    load_2d<1>(base + kWBytes, &amap, s * 128, static_cast<int32_t>(m0), bar);
+    load_2d<1>(base + kWBytes + NT * 128 + kSfTile, &asmap, s * 256, static_cast<int32_t>(m0 >> 7), bar);
   };
 
   grid_dep_launch();
   if (warp == 4 && elect_one()) {  // the copies start before the rest of the set-up
     prefetch_map(&wmap);
     prefetch_map(&wsmap);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < p.ring; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 1);
     }
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     grid_dep_wait();
-    for (int i = 0; i < C::kStages && s0 + i < s1; ++i) load(s0 + i, i);
+    for (int i = 0; i < p.ring && s0 + i < s1; ++i) load(s0 + i, i);
   }
   if (warp == 5) {
     tmem_alloc<1>(&S.tmem, C::kCols);
@@ -319,28 +325,32 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = S.tmem;
 
-  if (warp == 4 && elect_one()) {
-    int it = min(C::kStages, s1 - s0);
-    for (; s0 + it < s1; ++it) {
-      const int st = it % C::kStages;
-      if (!wait_bar(S, &S.empty[st], (it / C::kStages - 1) & 1, p.err)) break;
-      load(s0 + it, st);
+  if (warp == 4) {
+    int st = 0, round = 0;  // stage s0 + ring + ... reuses slot st after `round` uses
+    for (int s = s0 + p.ring; s < s1; ++s) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], round & 1, p.err))) break;
+      if (elect_one()) load(s, st);
+      __syncwarp();
+      if (++st == p.ring) st = 0, ++round;
     }
     if (S.abort)  // copies still in flight must land before the CTA leaves
-      for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i) drain_bar(&S.full[i % C::kStages], (i / C::kStages) & 1);
-  } else if (warp == 5 && elect_one()) {
+      for (int i = 0; i < p.ring && i < s1 - s0; ++i) drain_bar(&S.full[i], (i < st ? round + 1 : round) & 1);
+  } else if (warp == 5) {
     const uint32_t idesc = mx_idesc(1, NT);
-    uint32_t acc = 0;
-    for (int s = s0, it = 0; s < s1; ++s, ++it) {
-      const int st = it % C::kStages;
-      if (!wait_bar(S, &S.full[st], (it / C::kStages) & 1, p.err)) break;
+    int st = 0, round = 0;
+    for (int s = s0; s < s1; ++s) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p.err))) break;
       tc_fence_after();
       const uint32_t base = smem + st * C::kStageBytes;
-      stage_mmas<1, 1>(tmem, base, base + kWBytes, base + kWBytes + NT * 128, tmem + NT + st * C::kSfCols, idesc,
-                       (min(kStageK, p.K - s * kStageK) + 63) / 64, acc);
-      commit<1>(&S.empty[st]);
+      if (elect_one()) {
+        stage_mmas<1, 1>(tmem, base, base + kWBytes, base + kWBytes + NT * 128, tmem + NT + st * C::kSfCols, idesc,
+                         (min(kStageK, p.K - s * kStageK) + 63) / 64, s > s0);
+        commit<1>(&S.empty[st]);
+      }
+      __syncwarp();
+      if (++st == p.ring) st = 0, ++round;
     }
-    commit<1>(&S.acc_full);
+    if (elect_one()) commit<1>(&S.acc_full);
     if (S.abort) drain_bar(&S.acc_full, 0);
   }
 
@@ -349,9 +359,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   tc_fence_after();
   const int64_t n = n0 + 32 * (warp & 3) + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-  const int tok = static_cast<int>(p.M);
+  const int tok = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
   constexpr int NC = NT < 32 ? NT : 32;  // columns per pass
   constexpr int kEsz = BF16 ? 2 : 4;
+  uint8_t* const y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * kEsz;
   if (split == 1) {
     if (whole)
 #pragma unroll
@@ -361,7 +372,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         for (int i = 0; i < NC; i += 16) tmem_ld16(lanes + c + i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
 #pragma unroll
         for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
-        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
+        store_cols<BF16>(r, y + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
   } else {
     // rank r sums and writes tokens r * share ..; share is a power of two, 4 at least.
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         }
         const uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
         const int64_t m = static_cast<int64_t>(rank) * share + i;
-        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
+        store_cols<BF16>(r, y + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
       }
     }
   }
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t raw[];
   const uint32_t smem = (su32(raw) + 1023u) & ~1023u;
   __shared__ Bars S;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
@@ -505,17 +516,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   grid_dep_wait();
 
   if (warp == 8) {
-    if (elect_one()) {
-      const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
-      int it = 0;
-      for (; !S.abort && more; more = work.next(p)) {
-        const int32_t w0 = tile_w(p, work.tile) * 256 + static_cast<int32_t>(rank) * kTW;
-        const int32_t m0 = tile_m(p, work.tile) * p.mtok;
-        const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
-        for (int s = work.s0; s < work.s1; ++s, ++it) {
-          const int st = it % kPairStages;
-          if (it >= kPairStages && !wait_bar(S, &S.empty[st], (it / kPairStages - 1) & 1, p.err)) break;
-          const uint32_t base = smem + st * kPairStageBytes, bar = map_rank(su32(&S.full[st]), 0);
+    const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
+    const uint32_t full0 = map_rank(su32(&S.full[0]), 0);  // the leader's barriers count both CTAs' copies
+    int st = 0, round = 0;
+    for (; !S.abort && more; more = work.next(p)) {
+      const int32_t w0 = tile_w(p, work.tile) * 256 + static_cast<int32_t>(rank) * kTW;
+      const int32_t m0 = tile_m(p, work.tile) * p.mtok;
+      const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
+      for (int s = work.s0; s < work.s1; ++s) {
+        if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], (round - 1) & 1, p.err))) break;
+        const uint32_t base = smem + st * kPairStageBytes, bar = full0 + st * 8;
+        if (elect_one()) {
           if (rank == 0) mbar_expect_tx(&S.full[st], tx);
           load_2d<2>(base, &wmap, s * 128, w0, bar);
           load_2d<2>(base + kWBytes, &amap, s * 128, m0 + half, bar);
@@ -524,31 +535,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           for (int a = 0; a < kPairAtoms; ++a)
             load_2d<2>(base + kPairSf + (1 + a) * kSfTile, &asmap, s * 256, (m0 >> 7) + a, bar);
         }
+        __syncwarp();
+        if (++st == kPairStages) st = 0, ++round;
       }
-      if (S.abort && rank == 0)  // both CTAs' copies count on the leader's barriers
-        for (int i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
-          drain_bar(&S.full[i % kPairStages], (i / kPairStages) & 1);
     }
+    if (S.abort && rank == 0)  // copies in flight must land before the CTAs leave
+      for (int i = 0; i < kPairStages; ++i)
+        if (round > 0 || i < st) drain_bar(&S.full[i], (i < st ? round : round - 1) & 1);
     __syncwarp();
   } else if (warp == 9) {
-    if (rank == 0 && elect_one()) {
-      int it = 0, seg = 0;
+    if (rank == 0) {  // the whole warp runs the loop, so that what an MMA takes stays in uniform registers
+      int st = 0, round = 0, seg = 0;
       for (; !S.abort && more; more = work.next(p)) {
         const uint32_t idesc = mx_idesc(2, tile_tok(p, tile_m(p, work.tile) * p.mtok));
-        if (seg > 0 && !wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err)) break;
+        if (seg > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err))) break;
         ++seg;
         tc_fence_after();
-        uint32_t acc = 0;
-        for (int s = work.s0; s < work.s1; ++s, ++it) {
-          const int st = it % kPairStages;
-          if (!wait_bar(S, &S.full[st], (it / kPairStages) & 1, p.err)) break;
+        for (int s = work.s0; s < work.s1; ++s) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p.err))) break;
           tc_fence_after();
           const uint32_t base = smem + st * kPairStageBytes;
-          stage_mmas<2, kPairAtoms>(tmem, base, base + kWBytes, base + kPairSf, tmem + kMaxTok + st * kPairSfCols, idesc,
-                                    (min(kStageK, p.K - s * kStageK) + 63) / 64, acc);
-          commit<2>(&S.empty[st]);
+          if (elect_one()) {
+            stage_mmas<2, kPairAtoms>(tmem, base, base + kWBytes, base + kPairSf, tmem + kMaxTok + st * kPairSfCols, idesc,
+                                      (min(kStageK, p.K - s * kStageK) + 63) / 64, s > work.s0);
+            commit<2>(&S.empty[st]);
+          }
+          __syncwarp();
+          if (++st == kPairStages) st = 0, ++round;
         }
-        commit<2>(&S.acc_full);
+        if (elect_one()) commit<2>(&S.acc_full);
+        __syncwarp();
       }
       if (S.abort) {  // MMAs in flight: the parity of a further commit is not known, so wait out the bound
         const int64_t t0 = clock64();
@@ -641,7 +657,7 @@ cudaError_t launch(Kernel kernel, bool (&configured)[64], dim3 grid, int threads
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
@@ -664,18 +680,26 @@ cudaError_t launch(Kernel kernel, bool (&configured)[64], dim3 grid, int threads
   return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], a);
 }
 
+// CTAs that share a tile's K (a power of two up to 8, a quarter of the tokens at most).
+int small_split(int nt, int64_t tiles, int stages) {
+  int split = 1;
+  while (split < (nt < 32 ? nt / 4 : 8) && tiles * split * 2 <= 2 * num_sms() && stages >= split * 4) split *= 2;
+  return split;
+}
+
 template <int NT>
 cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16, cudaStream_t st) {
   using C = Small<NT>;
   static bool configured[2][64] = {};
-  const int64_t tiles = (a.N + kTW - 1) / kTW;
-  // K shared by as many CTAs (a power of two up to 8, a quarter of the tokens at most) as
-  // have two stages each and fit the SMs' two slots
-  int split = 1;
-  while (split < (NT < 32 ? NT / 4 : 8) && tiles * split * 2 <= 2 * num_sms() && a.stages >= split * 4) split *= 2;
-  const dim3 grid(split, static_cast<unsigned>(tiles));
-  return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, C::kSmem, split, m, a, st)
-                : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, C::kSmem, split, m, a, st);
+  const int64_t wt = (a.N + kTW - 1) / kTW, mt = (a.M + NT - 1) / NT, tiles = wt * mt;
+  const int split = small_split(NT, tiles, a.stages);
+  const dim3 grid(split, static_cast<unsigned>(wt), static_cast<unsigned>(mt));
+  MxArgs b = a;
+  b.ring = tiles * split <= num_sms() ? C::kRing1 : C::kRing2;
+  if (b.ring > (a.stages + split - 1) / split) b.ring = (a.stages + split - 1) / split;
+  const int smem = C::smem(b.ring);
+  return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, smem, split, m, b, st)
+                : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, smem, split, m, b, st);
 }
 
 // The pair kernel's schedule.
