@@ -10,12 +10,12 @@
 // (tcgen05.cp) in front of the MMAs that use them.
 //
 // Two kernels:
-//   small (M <= 128): a CTA multiplies 128 weight rows by all the tokens; a cluster of
-//     S CTAs shares a tile, each with a contiguous share of K, so that few tiles still
+//   small (few tiles): a CTA multiplies 128 weight rows by up to 128 tokens; a cluster of
+//     S CTAs may share a tile, each with a contiguous share of K, so that few tiles still
 //     stream the weights through every SM.  The S partial tiles meet in distributed
 //     shared memory and are summed in rank order: no workspace, no dependence on
 //     timing.
-//   pair (M > 128): persistent CTA pairs (cta_group::2) multiply 256 weight rows by up
+//   pair: persistent CTA pairs (cta_group::2) multiply 256 weight rows by up
 //     to 256 tokens.  Each CTA stages half of both operands, which is what lets shared
 //     memory (written once, read once per MMA, 128 bytes a cycle) keep up with the
 //     tensor core.  The accumulators leave TMEM for registers at once, and their stores
@@ -46,8 +46,7 @@ struct MxArgs {
   int box;      // token rows of one load
   int ring;     // small kernel: stages in shared memory
   // pair kernel
-  int mtok;     // tokens of a tile, 128 or 256 (the last one of a row narrower)
-  int mt, wt;   // token tiles, weight tiles
+  int mt, wt;   // token tiles (the last one narrower), weight tiles
   int tiles;
   int whole;    // tiles 0 .. whole - 1 go to the pairs whole, in turn; the rest by stages
   int64_t units;     // stages of the rest (0: none)
@@ -263,7 +262,7 @@ __device__ __forceinline__ void store_cols(const uint32_t (&r)[NC], void* y, int
   else store_cols_t<BF16, NC, false>(r, y, ldy, n, N, lim);
 }
 
-// ---------------------------------------------------------------- small: M <= 128
+// ---------------------------------------------------------------- small
 template <int NT>
 struct Small {
   static constexpr int kStageBytes = kWBytes + NT * 128 + 2 * kSfTile;
@@ -271,8 +270,13 @@ struct Small {
   static constexpr int kRing2 = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
   static constexpr int kRing1 = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 6;
   static constexpr int kSfCols = 16, kCols = 256;  // TMEM columns of a stage's scales, of the CTA
-  // the stages, or the partial tiles that the CTAs of a split exchange
-  static constexpr int smem(int ring) { return 1024 + (ring * kStageBytes > NT * 512 ? ring * kStageBytes : NT * 512); }
+  // The stages, or the partial tiles that the CTAs of a split exchange; and enough that a
+  // third CTA does not fit an SM, whose TMEM holds two: one that waited for TMEM while
+  // its cluster waits for it could wait for ever.
+  static constexpr int smem(int ring) {
+    const int need = 1024 + (ring * kStageBytes > NT * 512 ? ring * kStageBytes : NT * 512);
+    return need > 77 * 1024 ? need : 77 * 1024;
+  }
   static_assert(kRing1 <= 12 && NT + kRing1 * kSfCols <= kCols && smem(kRing1) <= 227 * 1024 && smem(kRing2) <= 113 * 1024);
 };
 constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
@@ -303,7 +307,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     load_2d<1>(base + kWBytes + NT * 128 + kSfTile, &asmap, s * 256, static_cast<int32_t>(m0 >> 7), bar);
   };
 
-  grid_dep_launch();
   if (warp == 4 && elect_one()) {  // the copies start before the rest of the set-up
     prefetch_map(&wmap);
     prefetch_map(&wsmap);
@@ -322,6 +325,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     tc_fence_before();
   }
   __syncthreads();
+  grid_dep_launch();  // behind the allocation: the next kernel must not take the TMEM this one waits for
   tc_fence_after();
   const uint32_t tmem = S.tmem;
 
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   if (warp == 5) tmem_free<1>(tmem, C::kCols);
 }
 
-// ---------------------------------------------------------------- pair: M > 128
+// ---------------------------------------------------------------- pair
 constexpr int kMaxTok = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairAtoms = kMaxTok / 128;
@@ -436,7 +440,7 @@ __device__ __forceinline__ int tile_m(const MxArgs& p, int t) { return p.whole =
 // Tokens of the tile at m0 that the MMA computes: a multiple of 32, whose halves are
 // whole 8-row swizzle atoms.
 __device__ __forceinline__ int tile_tok(const MxArgs& p, int m0) {
-  return static_cast<int>(min(static_cast<int64_t>(p.mtok), (p.M - m0 + 31) & ~int64_t(31)));
+  return static_cast<int>(min(static_cast<int64_t>(kMaxTok), (p.M - m0 + 31) & ~int64_t(31)));
 }
 
 // The work of a pair, in order: whole tiles `pair`, pair + pairs, ... below p.whole,
@@ -486,7 +490,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&S.full[i], 1);
@@ -511,6 +514,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   bool more = work.next(p);
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised
+  grid_dep_launch();  // behind the allocation: the next kernel must not take the TMEM this one waits for
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   grid_dep_wait();
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     int st = 0, round = 0;
     for (; !S.abort && more; more = work.next(p)) {
       const int32_t w0 = tile_w(p, work.tile) * 256 + static_cast<int32_t>(rank) * kTW;
-      const int32_t m0 = tile_m(p, work.tile) * p.mtok;
+      const int32_t m0 = tile_m(p, work.tile) * kMaxTok;
       const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
       for (int s = work.s0; s < work.s1; ++s) {
         if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], (round - 1) & 1, p.err))) break;
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     if (rank == 0) {  // the whole warp runs the loop, so that what an MMA takes stays in uniform registers
       int st = 0, round = 0, seg = 0;
       for (; !S.abort && more; more = work.next(p)) {
-        const uint32_t idesc = mx_idesc(2, tile_tok(p, tile_m(p, work.tile) * p.mtok));
+        const uint32_t idesc = mx_idesc(2, tile_tok(p, tile_m(p, work.tile) * kMaxTok));
         if (seg > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err))) break;
         ++seg;
         tc_fence_after();
@@ -636,9 +640,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) p.flags[at] = 0u;
       }
       const int64_t n = static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3) + lane;
-      const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * p.mtok + 128 * (warp >> 2);
-      if (128 * (warp >> 2) < p.mtok)
-        store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
+      const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * kMaxTok + 128 * (warp >> 2);
+      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
                          static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
     }
   }
@@ -680,11 +683,20 @@ cudaError_t launch(Kernel kernel, bool (&configured)[64], dim3 grid, int threads
   return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], a);
 }
 
-// CTAs that share a tile's K (a power of two up to 8, a quarter of the tokens at most).
+// CTAs that share a tile's K: the power of two up to 8 (a quarter of the tokens at
+// most, no CTA without a stage, all CTAs resident) with the least of its stages and its
+// exchange.  In units of 10 ns, measured on a GB300: 25 a stage; the exchange of the
+// partial tiles 30, 80, 200, 330 for 16, 32, 64, 128 tokens, half as much again with two
+// CTAs on an SM.  K17408 N256, one tile of 128 tokens: 19.8 us alone, 8.2 over 8 CTAs;
+// K2048 N2560: 4.6 us alone, 7.4 over 2.
 int small_split(int nt, int64_t tiles, int stages) {
-  int split = 1;
-  while (split < (nt < 32 ? nt / 4 : 8) && tiles * split * 2 <= 2 * num_sms() && stages >= split * 4) split *= 2;
-  return split;
+  const int exchange = nt == 16 ? 30 : nt == 32 ? 80 : nt == 64 ? 200 : 330;
+  int best = 1, least = stages * 25;
+  for (int split = 2; split <= 8 && split <= nt / 4 && split <= stages && tiles * split <= 2 * num_sms(); split *= 2) {
+    const int cost = (stages + split - 1) / split * 25 + (tiles * split > num_sms() ? exchange * 3 / 2 : exchange);
+    if (cost < least) best = split, least = cost;
+  }
+  return best;
 }
 
 template <int NT>
@@ -702,9 +714,15 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
                 : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, smem, split, m, b, st);
 }
 
+// The small kernel serves up to 128 tokens, and more while its tiles (128 x 128) have an
+// SM each: no pair of SMs to bring together, and K is split.  M512 K17408 N640: 14.0 us,
+// the pair kernel 22.0; M256 K5120 N5120 8.1 and 9.6; M512 K5120 N5120 (160 tiles on 152
+// SMs) 10.1 and 10.3, at K17408 26.3 and 23.1.
+bool use_small(int64_t M, int64_t N) { return M <= 128 || (M + 127) / 128 * ((N + 127) / 128) <= num_sms(); }
+
 // The pair kernel's schedule.
 struct PairPlan {
-  int mtok, mt, tiles, whole, pairs;
+  int mt, tiles, whole, pairs;
   int64_t units;
   size_t flag_bytes, ws_bytes;
 };
@@ -712,10 +730,7 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
   PairPlan q{};
   const int64_t pairs = num_sms() / 2, wt = (N + 255) / 256;
   const int stages = static_cast<int>((K + kStageK - 1) / kStageK);
-  // 128 tokens a tile where that still leaves every tile a pair of its own (M256 K5120
-  // N5120: MEASURED), else 256
-  q.mtok = wt * ((M + 127) / 128) <= pairs ? 128 : 256;
-  q.mt = static_cast<int>((M + q.mtok - 1) / q.mtok);
+  q.mt = static_cast<int>((M + kMaxTok - 1) / kMaxTok);
   q.tiles = static_cast<int>(wt * q.mt);
   q.whole = q.tiles;
   // Whole tiles leave the pairs idle for the unused part of the last wave.  Cutting the
@@ -735,7 +750,7 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
-size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return M <= 128 ? 0 : plan_pair(M, N, K).ws_bytes; }
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return use_small(M, N) ? 0 : plan_pair(M, N, K).ws_bytes; }
 
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
@@ -746,18 +761,19 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
   a.stages = static_cast<int>((K + kStageK - 1) / kStageK);
   a.err = device_error_word();
   PairPlan q{};
-  if (M <= 128) {
+  const bool small = use_small(M, N);
+  if (small) {
     a.box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   } else {
     q = plan_pair(M, N, K);
-    a.mtok = q.mtok; a.mt = q.mt; a.wt = static_cast<int>((N + 255) / 256); a.tiles = q.tiles; a.whole = q.tiles;
+    a.mt = q.mt; a.wt = static_cast<int>((N + 255) / 256); a.tiles = q.tiles; a.whole = q.tiles;
     if (ws && q.units > 0) {
       a.whole = q.whole;
       a.units = q.units;
       a.flags = static_cast<uint32_t*>(ws);
       a.parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + q.flag_bytes);
     }
-    a.box = a.mt > 1 ? a.mtok / 2 : static_cast<int>((M + 31) / 32 * 16);
+    a.box = a.mt > 1 ? kMaxTok / 2 : static_cast<int>((M + 31) / 32 * 16);
   }
   const uint64_t kt = static_cast<uint64_t>((K + 127) / 128) * 128, row = static_cast<uint64_t>(K / 2);
   CUtensorMap m[4];
@@ -774,7 +790,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
     e = encode_2d_map(&m[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kt, static_cast<uint64_t>((M + 127) / 128), kt * 4,
                       256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (e != cudaSuccess) return e;
-  if (M > 128) {
+  if (!small) {
     static bool configured[2][64] = {};
     const dim3 grid(static_cast<unsigned>(2 * q.pairs));
     return y_bf16 ? launch(mx_pair_kernel<true>, configured[1], grid, kPairThreads, kPairSmem, 0, m, a, stream)
