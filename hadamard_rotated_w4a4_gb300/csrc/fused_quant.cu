@@ -45,14 +45,24 @@ bool fits32(int64_t M, int64_t ld, int64_t ld2 = 0) {
   return M < top / 8 && M * (ld > ld2 ? ld : ld2) < top;
 }
 
-// silu(g) * u = g u / (1 + 2^(-g log2 e)).  The approximate exponential and reciprocal
-// (about 2 units in the last place each, and |g| / 2 more from rounding the exponent)
-// stay far below the step of the 8-bit codes that follow.
-__device__ __forceinline__ float swiglu(float g, float u) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
-  return __fmul_rn(__fmul_rn(g, r), u);
+// v = silu(v) * u, silu(g) = g / (1 + 2^(-g log2 e)).  The approximate exponential and
+// reciprocal (about 2 units in the last place each, and |g| / 2 more from rounding the
+// exponent) stay far below the step of the 8-bit codes that follow.
+__device__ __forceinline__ void swiglu8(float (&v)[8], const float (&u)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 g = make_float2(v[i], v[i + 1]);
+    const float2 t = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    const float2 y = __fmul2_rn(__fmul2_rn(g, r), make_float2(u[i], u[i + 1]));
+    v[i] = y.x;
+    v[i + 1] = y.y;
+  }
 }
 
 // ---------------------------------------------------------------- rows and SwiGLU
@@ -86,8 +96,7 @@ __global__ void __launch_bounds__(kThreads) rows_quantize_kernel(const T* __rest
     if constexpr (kPair) {
       float u[8];
       b[j].get(u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = swiglu(v[i], u[i]);
+      swiglu8(v, u);
     }
     if (rotate) quad_rotate(v, q);
     quad_quantize<FMT, I>(v, q, ok[j], first + j * kThreads, row[j], col[j] >> 2, static_cast<I>(cpr.d >> 2), o);
@@ -152,7 +161,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const TX* __rest
           ra[0].get(u);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = __fadd_rn(v[j][i], u[i]);
+        for (int i = 0; i < 8; i += 2) {
+          const float2 h = __fadd2_rn(make_float2(v[j][i], v[j][i + 1]), make_float2(u[i], u[i + 1]));
+          v[j][i] = h.x;
+          v[j][i + 1] = h.y;
+        }
         store8(r_out + col * 8, v[j], wide);
       }
     }

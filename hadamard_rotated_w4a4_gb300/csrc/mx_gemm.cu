@@ -720,11 +720,16 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
 // SMs) 10.1 and 10.3, at K17408 26.3 and 23.1.
 bool use_small(int64_t M, int64_t N) { return M <= 128 || (M + 127) / 128 * ((N + 127) / 128) <= num_sms(); }
 
+// The first MiB of a workspace holds counters that every product leaves at zero (the
+// int4 products keep theirs there too, and may be given the same workspace): the flags
+// lie in it, the partial tiles behind it.
+constexpr size_t kWsCounters = size_t(1) << 20;
+
 // The pair kernel's schedule.
 struct PairPlan {
   int mt, tiles, whole, pairs;
   int64_t units;
-  size_t flag_bytes, ws_bytes;
+  size_t ws_bytes;
 };
 PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
   PairPlan q{};
@@ -741,8 +746,7 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
   if (q.tiles > pairs && (waves * pairs - q.tiles) * stages > kCutStages * pairs) {
     q.whole = static_cast<int>((waves - 2) * pairs);
     q.units = static_cast<int64_t>(q.tiles - q.whole) * stages;
-    q.flag_bytes = (static_cast<size_t>(pairs) * 16 * sizeof(uint32_t) + 255) & ~size_t(255);
-    q.ws_bytes = q.flag_bytes + static_cast<size_t>(pairs) * 16 * 1024 * sizeof(float4);
+    q.ws_bytes = kWsCounters + static_cast<size_t>(pairs) * 16 * 1024 * sizeof(float4);
   }
   q.pairs = static_cast<int>(q.tiles < pairs ? q.tiles : pairs);
   return q;
@@ -771,7 +775,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
       a.whole = q.whole;
       a.units = q.units;
       a.flags = static_cast<uint32_t*>(ws);
-      a.parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + q.flag_bytes);
+      a.parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + kWsCounters);
     }
     a.box = a.mt > 1 ? kMaxTok / 2 : static_cast<int>((M + 31) / 32 * 16);
   }

@@ -487,8 +487,8 @@ w4a4_status w4a8_dequantize_act(const w4a4_act8* a, void* y, int y_dtype, int64_
  *   y : device, [M][ldy] fp32 or bf16 (y_dtype; bf16 is rounded once, at the end),
  *       ldy >= N, aligned to its element.
  *   ws: optional device workspace (NULL, or mxfp4_gemm_workspace_bytes(M, N, K) bytes or
- *       more, 16-byte aligned, its first 64 KiB zero before its first use; a smaller
- *       one is W4A4_ERR_WORKSPACE).  With it, shapes whose tiles would leave SMs idle in
+ *       more, 16-byte aligned, all zero before its first use; a smaller one is
+ *       W4A4_ERR_WORKSPACE; it may be one that w4a4_gemm uses as well).  With it, shapes whose tiles would leave SMs idle in
  *       the last wave cut that wave's K work evenly over the SMs; a tile cut in two is
  *       summed first part + second part.  Every call leaves the workspace as it needs
  *       to find it; after W4A4_ERR_TIMEOUT, zero it before reuse.  Calls that share one

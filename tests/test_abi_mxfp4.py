@@ -49,12 +49,12 @@ def test_gemm_refusals(lib):
     assert call(dt=2) == "W4A4_ERR_INVALID_ARG"
     assert call(ldy=63) == "W4A4_ERR_INVALID_ARG"
     assert call(w=mx(rows=65536 * 128), ldy=65536 * 128) == "W4A4_ERR_UNSUPPORTED"
-    big, rows = mx(rows=20000, K=8192), mx(rows=1000, K=8192)  # 79 x 4 tiles: the last wave is cut
-    need = lib.mxfp4_gemm_workspace_bytes(1000, 20000, 8192)
+    big, rows = mx(rows=20000, K=16384), mx(rows=1000, K=16384)  # 79 x 4 tiles: the last wave is cut
+    need = lib.mxfp4_gemm_workspace_bytes(1000, 20000, 16384)
     assert need > 0 and need % 16 == 0
     assert call(w=big, a=rows, ldy=20000, ws=FAKE, ws_bytes=need - 16) == "W4A4_ERR_WORKSPACE"
     assert call(w=big, a=rows, ldy=20000, ws=FAKE + 8, ws_bytes=need) == "W4A4_ERR_ALIGNMENT"
-    assert lib.mxfp4_gemm_workspace_bytes(1, 20000, 8192) == 0 and lib.mxfp4_gemm_workspace_bytes(1000, 20000, 33) == 0
+    assert lib.mxfp4_gemm_workspace_bytes(1, 20000, 16384) == 0 and lib.mxfp4_gemm_workspace_bytes(1000, 20000, 33) == 0
     assert status(lib, "mxfp4_gemm", None, mx(), FAKE, 1, 64, None, 0, None) == "W4A4_ERR_INVALID_ARG"
     assert call(a=mx(rows=0), y=None) == "W4A4_OK"
     assert call(w=mx(rows=0), y=None, ldy=0) == "W4A4_OK"

@@ -187,6 +187,24 @@ def test_product_with_the_last_wave_cut(dev, M, K, N):
     w4.w4a4_check()
 
 
+def test_workspace_shared_with_the_int4_product(dev):
+    """One workspace serves both products of a stream, in any order, whatever each leaves in it."""
+    M, K, N = 257, 8224, 10100
+    qw, qa = operands(dev, M, K, N)
+    x, w = f32_tensor(rows(2, 300, 1024), dev), f32_tensor(rows(1, 640, 1024) * np.float32(0.02), dev)
+    wq, aq = w4.h32_q4_0_pack_weights(w), w4.w4a4_rotate_quantize_act(x)
+    need = max(w4.mxfp4_gemm_workspace_bytes(M, N, K), w4.w4a4_gemm_workspace_bytes(300, 640, 1024))
+    assert w4.mxfp4_gemm_workspace_bytes(M, N, K) > 0 and w4.w4a4_gemm_workspace_bytes(300, 640, 1024) > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    want = w4.mxfp4_gemm(qw, qa, ws=ws), w4.w4a4_gemm(wq, aq, ws=torch.zeros(need, dtype=torch.uint8, device=dev))
+    assert not bool(ws[: 1 << 20].any())  # the counters' part is left as it was found
+    for _ in range(3):
+        assert torch.equal(w4.w4a4_gemm(wq, aq, ws=ws), want[1])
+        assert torch.equal(w4.mxfp4_gemm(qw, qa, ws=ws), want[0])
+    assert not bool(ws[: 1 << 20].any())
+    w4.w4a4_check()
+
+
 def test_product_does_not_depend_on_what_ran_before(dev):
     qw, qa = operands(dev, 200, 1056, 300)
     y = w4.mxfp4_gemm(qw, qa)
