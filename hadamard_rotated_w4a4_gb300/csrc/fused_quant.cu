@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kThreads) rows_quantize_kernel(const T* __rest
     row[j] = col[j] = 0;
     if (ok[j]) {
       chunk_at<I>(c, cpr, row[j], col[j]);
-      a[j].load(x + row[j] * ldx + col[j] * 8, wide);
-      if constexpr (kPair) b[j].load(x2 + row[j] * ldx2 + col[j] * 8, wide);
+      a[j].template load<true>(x + row[j] * ldx + col[j] * 8, wide);
+      if constexpr (kPair) b[j].template load<true>(x2 + row[j] * ldx2 + col[j] * 8, wide);
     }
   }
 #pragma unroll

@@ -21,8 +21,15 @@ struct Chunk;
 template <>
 struct Chunk<float> {
   float v[8];
+  // kLast: nothing reads the values again, so L2 may drop them first
+  template <bool kLast = false>
   __device__ __forceinline__ void load(const float* p, bool wide) {
-    if (wide) {
+    if (wide && kLast) {
+      asm volatile("ld.global.L2::evict_first.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                   : "l"(p)
+                   : "memory");
+    } else if (wide) {
       asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                    : "l"(p)
@@ -41,7 +48,11 @@ struct Chunk<float> {
 template <>
 struct Chunk<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) { a = *reinterpret_cast<const uint4*>(p); }
+  template <bool kLast = false>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) {
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+    a = kLast ? __ldcs(q) : *q;
+  }
   __device__ __forceinline__ void get(float (&o)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll

@@ -89,6 +89,8 @@ F32, BF16 = torch.float32, torch.bfloat16
 # K of one block, below and above a warp's row, odd block counts, several chunks a thread
 NORM_SHAPES = [(1, 32), (1, 5120), (3, 64), (70, 96), (33, 224), (5, 256), (9, 288), (200, 736), (700, 8224), (2, 17408),
                (4, 33024), (1, 65536)]
+# many rows
+NORM_SHAPES += [(457, 288), (500, 5120), (3000, 416), (1000, 9216)]
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
@@ -112,9 +114,10 @@ def test_norm(dev, M, K, fmt):
         check_codes(q, norm64(h.cpu().numpy(), g, 1e-6), fmt, rotate)
 
 
+@pytest.mark.parametrize("M", [50, 1500])
 @pytest.mark.parametrize("dr", [F32, BF16])
-def test_norm_in_place_strided_and_expanded(dev, dr):
-    M, K = 50, 416
+def test_norm_in_place_strided_and_expanded(dev, dr, M):
+    K = 416
     x, r = data(1, M, K, F32, dev), data(2, M, K, dr, dev)
     want_r = (x + r.float()).to(dr)
     wide = torch.full((M, K + 32), 7.0, dtype=dr, device=dev)
