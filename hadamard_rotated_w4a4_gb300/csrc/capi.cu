@@ -720,6 +720,7 @@ w4a4_status w4a4_check(w4a4_stream_t stream) {
 
 void w4a4_debug_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
   w4a4::grp_set_wait_limit(wait_ns, producer_delay_ns);
+  w4a4::mx_set_wait_limit(wait_ns, producer_delay_ns);
 }
 
 const char* w4a4_last_error(void) { return g_err; }

@@ -32,8 +32,7 @@ namespace {
 
 constexpr int kTW = 128;      // weight rows per CTA
 constexpr int kStageK = 256;  // elements of K per stage
-// Bound of every wait, about a second.  Counted in SM cycles: reading the global timer in
-// a polling loop delays the wake-up by hundreds of them.
+// Bound of every wait, about a second, in SM cycles (of 2 GHz at most).
 constexpr int64_t kWaitCycles = int64_t(1) << 31;
 constexpr int kWBytes = kTW * 128;
 constexpr int kSfTile = 1024;  // a stage's scales of 128 rows: two 512-byte tiles
@@ -53,6 +52,7 @@ struct MxArgs {
   uint32_t* flags;   // [pairs][2 CTAs][8 warps], zero between calls
   float4* parts;     // [pairs][2][8][32][32]: a warp's 128 accumulators of 32 lanes
   int* err;
+  int64_t wait, delay;  // cycles: the pipeline waits' bound; a test's hold on the first copy
 };
 
 struct Bars {
@@ -62,18 +62,25 @@ struct Bars {
 };
 
 // Bounded wait; on giving up, every other wait of the CTA gives up too.
-__device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, int* err) {
+__device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, const MxArgs& p) {
   if (mbar_try(b, parity)) return true;
   const int64_t t0 = clock64();
   while (!mbar_try(b, parity)) {
     if (S.abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > p.wait) {
       S.abort = 1;
-      if (err) atomicOr(err, 32);
+      if (p.err) atomicOr(p.err, 32);
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ void hold(const MxArgs& p) {
+  if (p.delay > 0) {
+    const int64_t t0 = clock64();
+    while (clock64() - t0 < p.delay) {
+    }
+  }
 }
 // As above without the shared give-up, for copies and MMAs in flight.
 __device__ __forceinline__ void drain_bar(uint64_t* b, uint32_t parity) {
@@ -307,6 +314,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     load_2d<1>(base + kWBytes + NT * 128 + kSfTile, &asmap, s * 256, static_cast<int32_t>(m0 >> 7), bar);
   };
 
+  const int first = min(p.ring, s1 - s0);  // stages that need no free slot
   if (warp == 4 && elect_one()) {  // the copies start before the rest of the set-up
     prefetch_map(&wmap);
     prefetch_map(&wsmap);
@@ -318,7 +326,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     grid_dep_wait();
-    for (int i = 0; i < p.ring && s0 + i < s1; ++i) load(s0 + i, i);
+    if (p.delay == 0)
+      for (int i = 0; i < first; ++i) load(s0 + i, i);
   }
   if (warp == 5) {
     tmem_alloc<1>(&S.tmem, C::kCols);
@@ -330,20 +339,28 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   const uint32_t tmem = S.tmem;
 
   if (warp == 4) {
+    bool filled = true;
+    if (p.delay > 0) {  // a test holds the first copies back, and issues none once a wait gave up
+      hold(p);
+      filled = !__any_sync(0xFFFFFFFFu, S.abort);
+      if (filled && elect_one())
+        for (int i = 0; i < first; ++i) load(s0 + i, i);
+      __syncwarp();
+    }
     int st = 0, round = 0;  // stage s0 + ring + ... reuses slot st after `round` uses
-    for (int s = s0 + p.ring; s < s1; ++s) {
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], round & 1, p.err))) break;
+    for (int s = s0 + p.ring; filled && s < s1; ++s) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], round & 1, p))) break;
       if (elect_one()) load(s, st);
       __syncwarp();
       if (++st == p.ring) st = 0, ++round;
     }
-    if (S.abort)  // copies still in flight must land before the CTA leaves
-      for (int i = 0; i < p.ring && i < s1 - s0; ++i) drain_bar(&S.full[i], (i < st ? round + 1 : round) & 1);
+    if (S.abort && filled)  // copies still in flight must land before the CTA leaves
+      for (int i = 0; i < first; ++i) drain_bar(&S.full[i], (i < st ? round + 1 : round) & 1);
   } else if (warp == 5) {
     const uint32_t idesc = mx_idesc(1, NT);
     int st = 0, round = 0;
     for (int s = s0; s < s1; ++s) {
-      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p.err))) break;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p))) break;
       tc_fence_after();
       const uint32_t base = smem + st * C::kStageBytes;
       if (elect_one()) {
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   }
 
   __syncwarp();
-  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p.err) && !S.abort);
+  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p) && !S.abort);
   tc_fence_after();
   const int64_t n = n0 + 32 * (warp & 3) + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -523,12 +540,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tx = 2u * (kWBytes + static_cast<uint32_t>(p.box) * 128u + (1 + kPairAtoms) * kSfTile);
     const uint32_t full0 = map_rank(su32(&S.full[0]), 0);  // the leader's barriers count both CTAs' copies
     int st = 0, round = 0;
+    hold(p);
     for (; !S.abort && more; more = work.next(p)) {
       const int32_t w0 = tile_w(p, work.tile) * 256 + static_cast<int32_t>(rank) * kTW;
       const int32_t m0 = tile_m(p, work.tile) * kMaxTok;
       const int32_t half = tile_tok(p, m0) / 2 * static_cast<int32_t>(rank);
       for (int s = work.s0; s < work.s1; ++s) {
-        if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], (round - 1) & 1, p.err))) break;
+        if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.empty[st], (round - 1) & 1, p))) break;
         const uint32_t base = smem + st * kPairStageBytes, bar = full0 + st * 8;
         if (elect_one()) {
           if (rank == 0) mbar_expect_tx(&S.full[st], tx);
@@ -552,11 +570,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       int st = 0, round = 0, seg = 0;
       for (; !S.abort && more; more = work.next(p)) {
         const uint32_t idesc = mx_idesc(2, tile_tok(p, tile_m(p, work.tile) * kMaxTok));
-        if (seg > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p.err))) break;
+        if (seg > 0 && !__all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_empty, static_cast<uint32_t>(seg - 1) & 1, p))) break;
         ++seg;
         tc_fence_after();
         for (int s = work.s0; s < work.s1; ++s) {
-          if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p.err))) break;
+          if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.full[st], round & 1, p))) break;
           tc_fence_after();
           const uint32_t base = smem + st * kPairStageBytes;
           if (elect_one()) {
@@ -583,7 +601,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t seg = 0;
     bool live = true;  // cleared when a wait gave up; the barrier below still counts this warp
     for (; more; more = work.next(p)) {
-      live = live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, seg & 1, p.err));
+      live = live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, seg & 1, p));
       ++seg;
       uint32_t r[128];
       if (live) {
@@ -620,7 +638,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t there = 0;
         while (true) {
           asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(p.flags + at) : "memory");
-          if (__all_sync(0xFFFFFFFFu, there != 0) || __any_sync(0xFFFFFFFFu, S.abort || clock64() - t0 > kWaitCycles)) break;
+          if (__all_sync(0xFFFFFFFFu, there != 0) || __any_sync(0xFFFFFFFFu, S.abort || clock64() - t0 > p.wait)) break;
         }
         if (!__all_sync(0xFFFFFFFFu, there != 0)) {
           S.abort = 1;
@@ -756,6 +774,12 @@ PairPlan plan_pair(int64_t M, int64_t N, int64_t K) {
 
 size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return use_small(M, N) ? 0 : plan_pair(M, N, K).ws_bytes; }
 
+static int64_t g_wait = kWaitCycles, g_delay = 0;
+void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
+  g_wait = wait_ns ? static_cast<int64_t>(2 * wait_ns) : kWaitCycles;
+  g_delay = static_cast<int64_t>(2 * producer_delay_ns);
+}
+
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
                            cudaStream_t stream) {
@@ -764,6 +788,8 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
   a.K = static_cast<int>(K);
   a.stages = static_cast<int>((K + kStageK - 1) / kStageK);
   a.err = device_error_word();
+  a.wait = g_wait;
+  a.delay = g_delay;
   PairPlan q{};
   const bool small = use_small(M, N);
   if (small) {

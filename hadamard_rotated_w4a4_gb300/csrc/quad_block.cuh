@@ -220,10 +220,11 @@ __device__ __forceinline__ void quad_quantize(float (&v)[8], int q, bool ok, I c
     constexpr float kTop = FMT == kInt4 ? 7.0f : 127.0f;
     constexpr float kLow = FMT == kInt4 ? -8.0f : -127.0f;
     const float d = bad ? __uint_as_float(0x7FC00000u) : div_by(a, kTop);
-    const float inv = (d != 0.0f) ? __frcp_rn(d) : 0.0f;
+    // a scale below the normal range has no finite reciprocal: codes of 0
+    const float inv = d < 1.17549435e-38f ? 0.0f : __frcp_rn(d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v2[i] = __fmul2_rn(v2[i], make_float2(inv, inv));
-    // Where the scale and its reciprocal are finite, |v| is at most kTop and a few ulp:
+    // Where the scale is finite, |v| is at most kTop and a few ulp:
     // v + 1.5 * 2^23 is 1.5 * 2^23 plus the nearest integer (ties to even), whose low
     // byte is that integer in two's complement.  It is the rounding half away from zero
     // unless some v lies halfway (or is NaN); then the general path rounds.
@@ -240,7 +241,7 @@ __device__ __forceinline__ void quad_quantize(float (&v)[8], int q, bool ok, I c
       t[2 * i] = __float_as_uint(s.x);
       t[2 * i + 1] = __float_as_uint(s.y);
     }
-    if (lane_amax(x) < 0.5f && inv <= 3.402823466e38f) {
+    if (lane_amax(x) < 0.5f) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         w[h] = prmt(prmt(t[4 * h], t[4 * h + 1], 0x0040u), prmt(t[4 * h + 2], t[4 * h + 3], 0x0040u), 0x5410u);

@@ -146,5 +146,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
                            cudaStream_t stream);
 size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+// Test hook, as grp_set_wait_limit, of the MXFP4 product's waits.
+void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
 
 }  // namespace w4a4

@@ -519,7 +519,8 @@ size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * K <= 65536 (W4A4_ERR_UNSUPPORTED above).  A NaN in a row makes the row read back as
  * NaN; so does a row of zeros with eps = 0 (0 * infinity).  An infinity, or squares
  * that overflow fp32, make the norm infinite: finite values become 0, the blocks
- * (int4, int8, MXFP4) that hold an infinity read back as NaN.
+ * (int4, int8, MXFP4) that hold an infinity read back as NaN.  An int4 or int8 block
+ * whose scale would be below 2^-126 reads back as zeros, here and below.
  */
 typedef struct {
   const void* x;
@@ -565,7 +566,7 @@ w4a4_status w4a4_check(w4a4_stream_t stream);
 /*
  * w4a4_debug_set_wait_limit -- a test hook for the bounded waits.  Later launches
  * of the super-tile GEMM kernel (w4a4_gemm with the expanded activation operand,
- * and w4a4_gemm_id) give up on a pipeline wait after wait_ns nanoseconds instead
+ * and w4a4_gemm_id) and of mxfp4_gemm give up on a pipeline wait after wait_ns nanoseconds instead
  * of one second, and their producer holds its first copy back for
  * producer_delay_ns.  With a delay longer than the limit every CTA gives up: the
  * kernel returns by itself, with its output incomplete, and w4a4_check reports

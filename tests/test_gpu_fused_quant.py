@@ -152,6 +152,23 @@ def test_norm_special_rows(dev, fmt):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
+def test_tiny_blocks(dev, fmt):
+    """Blocks down to the smallest fp32 values: finite, zeros stay zeros, and MXFP4 keeps what fits 2^-127 scales."""
+    one = torch.ones(1, 160, device=dev)
+    # silu(1) is a constant c: gate = 1 passes up * c through to the codes
+    up = torch.zeros(1, 160, device=dev)
+    up[0, 0], up[0, 33], up[0, 64], up[0, 97], up[0, 128] = 1e-30, 1e-36, 1e-38, 1e-44, 1.0
+    v = FMT[fmt][2](FMT[fmt][1](one, up, rotate=False)).cpu()[0]
+    at = torch.zeros(160, dtype=torch.bool)
+    at[[0, 33, 64, 97, 128]] = True
+    assert bool(torch.isfinite(v).all()) and not bool(v[~at].any())
+    c = 1 / (1 + np.exp(-1.0))
+    for k, x in ((0, 1e-30), (128, 1.0)):
+        assert abs(float(v[k]) - c * x) <= (0.25 if fmt == "mx" else 1e-6) * c * x
+    assert 0 <= float(v[33]) <= 1.3e-36 and 0 <= float(v[64]) <= 1.3e-38
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
 @pytest.mark.parametrize("M,K", [(1, 32), (1, 17408), (67, 768), (33, 736), (300, 96)])
 def test_swiglu(dev, M, K, fmt):
     rng = np.random.default_rng(K)

@@ -306,3 +306,22 @@ def test_offsets_past_32_bits(dev):
     y = w4.mxfp4_gemm(qw, w4.mxfp4_rotate_quantize(xs), dtype=torch.bfloat16)
     tail = w4.mxfp4_gemm(qw, w4.mxfp4_rotate_quantize(xs[-130:].contiguous()), dtype=torch.bfloat16)
     assert torch.equal(y[-130:], tail) and not bool(y[:-130].any())
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 2048, 640), (100, 512, 200), (600, 1024, 6000), (257, 8224, 10100)])
+def test_wait_runs_out_then_recovers(dev, M, K, N):
+    """A bounded pipeline wait that gives up (the copies held back longer than the bound): the kernel returns by
+    itself, w4a4_check reports it, and the next call is right again.  Split and unsplit small tiles, pairs with whole
+    tiles, pairs with their stages cut."""
+    qw, qa = operands(dev, M, K, N)
+    want = w4.mxfp4_gemm(qw, qa)
+    w4.w4a4_check()
+    try:
+        w4.w4a4_debug_set_wait_limit(50_000, 5_000_000)
+        w4.mxfp4_gemm(qw, qa)
+        with pytest.raises(w4.W4A4Error, match="TIMEOUT"):
+            w4.w4a4_check()
+    finally:
+        w4.w4a4_debug_set_wait_limit(0, 0)
+    assert torch.equal(w4.mxfp4_gemm(qw, qa), want)
+    w4.w4a4_check()
