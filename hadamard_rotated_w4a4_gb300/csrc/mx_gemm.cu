@@ -21,6 +21,13 @@
 //     tensor core.  The accumulators leave TMEM for registers at once, and their stores
 //     (32 bytes a cycle and SM at most) overlap the next tile's MMAs.  With a workspace
 //     the last waves' K work is cut evenly over the pairs (stream-K).
+//
+// Bounds and measurements (GB300, CUDA graphs).  Pair: a stage of a 256 x 256 tile is 512
+// cycles of MMA and 530 of shared memory; 574 are measured, and about 1,800 between two
+// tiles.  M4096 K5120 N17408 bf16 101 us (7.2 PFLOP/s; 111 us sustained, under the power
+// cap), M1024 K17408 N5120 30.4 us (6.0).  Small: bound by the weights' stream where K x N
+// is large (K69632 N5120, one token: 6.1 TB/s), else by set-up and round trips: one token
+// K5120 N5120 4.7 us, 64 tokens 7.1, 256 tokens 8.1.
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"
