@@ -844,8 +844,8 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     else:
         ldy = _rows(y, "y", (a.rows, w.rows))
     lib, st = load_library(), _stream(stream)
-    if ws is True:
-        need = lib.mxfp4_gemm_workspace_bytes(a.rows, w.rows, w.K)
+    if ws is True:  # batches of up to 128 tokens never use one
+        need = lib.mxfp4_gemm_workspace_bytes(a.rows, w.rows, w.K) if a.rows > 128 else 0
         ws = gemm_workspace(a.rows, w.rows, w.K, y.device, st, need) if need else None
     ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
     _check(lib.mxfp4_gemm(w._at, a._at, y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, ws_ptr, ws_bytes, st))

@@ -27,7 +27,7 @@
 // tiles.  M4096 K5120 N17408 bf16 101 us (7.2 PFLOP/s; 111 us sustained, under the power
 // cap), M1024 K17408 N5120 30.4 us (6.0).  Small: bound by the weights' stream where K x N
 // is large (K69632 N5120, one token: 6.1 TB/s), else by set-up and round trips: one token
-// K5120 N5120 4.7 us, 64 tokens 7.1, 256 tokens 8.1.
+// K5120 N5120 4.3 us, 64 tokens 6.7, 256 tokens 8.1.
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"
@@ -51,6 +51,7 @@ struct MxArgs {
   int K, stages;
   int box;      // token rows of one load
   int ring;     // small kernel: stages in shared memory
+  int apart;    // small kernel: where the partial tiles lie, 0 = over the stages
   // pair kernel
   int mt, wt;   // token tiles (the last one narrower), weight tiles
   int tiles;
@@ -120,6 +121,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves, for what needs no data of the others.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
@@ -284,14 +288,18 @@ struct Small {
   static constexpr int kRing2 = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
   static constexpr int kRing1 = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 6;
   static constexpr int kSfCols = 16, kCols = 256;  // TMEM columns of a stage's scales, of the CTA
-  // The stages, or the partial tiles that the CTAs of a split exchange; and enough that a
+  static constexpr int kPartBytes = NT * 512;  // the partial tiles that the CTAs of a split exchange
+  static constexpr int kMost1 = 226 * 1024, kMost2 = 113 * 1024;  // shared memory with one CTA an SM, with two
+  // Partial tiles behind the stages if that fits, else in their place; and enough that a
   // third CTA does not fit an SM, whose TMEM holds two: one that waited for TMEM while
   // its cluster waits for it could wait for ever.
-  static constexpr int smem(int ring) {
-    const int need = 1024 + (ring * kStageBytes > NT * 512 ? ring * kStageBytes : NT * 512);
+  static constexpr bool apart(int ring, int most) { return 1024 + ring * kStageBytes + kPartBytes <= most; }
+  static constexpr int smem(int ring, int most) {
+    const int stages = ring * kStageBytes;
+    const int need = 1024 + (apart(ring, most) ? stages + kPartBytes : stages > kPartBytes ? stages : kPartBytes);
     return need > 77 * 1024 ? need : 77 * 1024;
   }
-  static_assert(kRing1 <= 12 && NT + kRing1 * kSfCols <= kCols && smem(kRing1) <= 227 * 1024 && smem(kRing2) <= 113 * 1024);
+  static_assert(kRing1 <= 12 && NT + kRing1 * kSfCols <= kCols && smem(kRing1, kMost1) <= kMost1 && smem(kRing2, kMost2) <= kMost2);
 };
 constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
 
@@ -342,6 +350,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   }
   __syncthreads();
   grid_dep_launch();  // behind the allocation: the next kernel must not take the TMEM this one waits for
+  if (split > 1) cluster_arrive_relaxed();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
 
@@ -406,8 +415,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
     // rank r sums and writes tokens r * share ..; share is a power of two, 4 at least.
     // Partials: [rank][share / 4][128 rows][4 tokens], 16 bytes a lane.
     const int share = NT / split, log = 31 - __clz(share);
-    const uint32_t mine = smem + 16u * (rank * (share / 4) * kTW + 32 * (warp & 3) + lane);
-    cluster_sync();  // every CTA's operand stages are free
+    const uint32_t mine = smem + p.apart + 16u * (rank * (share / 4) * kTW + 32 * (warp & 3) + lane);
+    cluster_wait();  // every CTA of the cluster runs
+    if (p.apart == 0) {
+      cluster_arrive_relaxed();
+      cluster_wait();  // and has no MMA that reads its stages
+    }
     if (whole)
 #pragma unroll
       for (int c = 0; c < NT; c += NC) {
@@ -426,7 +439,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
       }
     cluster_sync();
     if (whole) {
-      const uint8_t* part = raw + (smem - su32(raw)) + 16 * (32 * warp + lane);
+      const uint8_t* part = raw + (smem - su32(raw)) + p.apart + 16 * (32 * warp + lane);
       for (int i = 0; i < share && rank * share + i < tok; i += 4) {
         float4 v = *reinterpret_cast<const float4*>(part + 16 * ((i >> 2) * kTW));
         for (int q = 1; q < split; ++q) {
@@ -732,9 +745,12 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
   const int split = small_split(NT, tiles, a.stages);
   const dim3 grid(split, static_cast<unsigned>(wt), static_cast<unsigned>(mt));
   MxArgs b = a;
-  b.ring = tiles * split <= num_sms() ? C::kRing1 : C::kRing2;
+  const bool alone = tiles * split <= num_sms();
+  const int most = alone ? C::kMost1 : C::kMost2;
+  b.ring = alone ? C::kRing1 : C::kRing2;
   if (b.ring > (a.stages + split - 1) / split) b.ring = (a.stages + split - 1) / split;
-  const int smem = C::smem(b.ring);
+  b.apart = split > 1 && C::apart(b.ring, most) ? b.ring * C::kStageBytes : 0;
+  const int smem = C::smem(b.ring, most);
   return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, smem, split, m, b, st)
                 : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, smem, split, m, b, st);
 }

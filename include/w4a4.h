@@ -501,7 +501,7 @@ w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_
                        size_t ws_bytes, w4a4_stream_t stream);
 
 /* Workspace bytes for mxfp4_gemm at this shape on the current device; 0 when it would
- * not use one. */
+ * not use one (always for M <= 128). */
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*

@@ -49,6 +49,36 @@ def test_block_matches_the_chain(M, H, F):
     assert np.linalg.norm(got - want) <= 0.02 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_chain_without_waits_between(M):
+    """Kernels may start before the one in front of them ends and share their buffers with it: a hundred blocks
+    in a row, every buffer reused, give the bits of the same blocks with a wait behind each call."""
+    import hadamard_rotated_w4a4_gb300 as w4
+
+    dev = device()
+    H, F = 512, 768
+    gen = torch.Generator("cuda").manual_seed(M)
+    rnd = lambda *s: torch.randn(*s, device=dev, generator=gen)  # noqa: E731
+    wg, wd = w4.mxfp4_rotate_quantize(rnd(2 * F, H) * 0.04), w4.mxfp4_rotate_quantize(rnd(H, F) * 0.04)
+    x0, r0 = rnd(M, H).bfloat16(), rnd(M, H).bfloat16()
+
+    def blocks(wait):
+        x, r = x0.clone(), r0.clone()
+        a, b = w4.MxFp4(M, H, dev), w4.MxFp4(M, F, dev)
+        gu = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dev)
+        for _ in range(100):
+            for call in (lambda: w4.mxfp4_rmsnorm_quantize(x, residual=r, out=a), lambda: w4.mxfp4_gemm(wg, a, y=gu),
+                         lambda: w4.mxfp4_swiglu_quantize(gu[:, :F], gu[:, F:], out=b),
+                         lambda: w4.mxfp4_gemm(wd, b, y=x)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        return x, r
+
+    want, got = blocks(True), blocks(False)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bool(torch.isfinite(got[1]).all())
+
+
 def test_example_runs():
     out = subprocess.run([sys.executable, PATH, "--tokens", "64", "--hidden", "512", "--ffn", "1024"], cwd=ROOT,
                          capture_output=True, text=True, timeout=300)
