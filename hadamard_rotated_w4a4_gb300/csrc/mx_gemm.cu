@@ -290,14 +290,16 @@ struct Small {
   static constexpr int kSfCols = 16, kCols = 256;  // TMEM columns of a stage's scales, of the CTA
   static constexpr int kPartBytes = NT * 512;  // the partial tiles that the CTAs of a split exchange
   static constexpr int kMost1 = 226 * 1024, kMost2 = 113 * 1024;  // shared memory with one CTA an SM, with two
-  // Partial tiles behind the stages if that fits, else in their place; and enough that a
-  // third CTA does not fit an SM, whose TMEM holds two: one that waited for TMEM while
-  // its cluster waits for it could wait for ever.
+  // Partial tiles behind the stages if that fits, else in their place; and enough that
+  // neither a third CTA nor one of the int4 and int8 products (over 148 KB, all of
+  // the TMEM) fits beside it on an SM, whose TMEM holds two: one that waited for TMEM
+  // while its cluster waits for it could wait for ever.
+  static constexpr int kLeast = 80 * 1024;
   static constexpr bool apart(int ring, int most) { return 1024 + ring * kStageBytes + kPartBytes <= most; }
   static constexpr int smem(int ring, int most) {
     const int stages = ring * kStageBytes;
     const int need = 1024 + (apart(ring, most) ? stages + kPartBytes : stages > kPartBytes ? stages : kPartBytes);
-    return need > 77 * 1024 ? need : 77 * 1024;
+    return need > kLeast ? need : kLeast;
   }
   static_assert(kRing1 <= 12 && NT + kRing1 * kSfCols <= kCols && smem(kRing1, kMost1) <= kMost1 && smem(kRing2, kMost2) <= kMost2);
 };
