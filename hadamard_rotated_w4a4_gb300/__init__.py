@@ -529,76 +529,83 @@ def w4a4_gemm_id_status(ws: torch.Tensor, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- the exact path (int8 activations)
-class _Held:
-    """An operand that keeps its C descriptor: the calls take its address and stamp rows, K and tag into it."""
-
-    __slots__ = ("rows", "K", "_desc", "_at")
-
-    def _hold(self, codes_ptr: int, scales_ptr: int, rows: int, K: int, tag: int, rotated: bool) -> None:
-        self.rows, self.K = rows, K
-        self._desc = _Act4Desc(codes_ptr, scales_ptr, rows, K, tag | TAG_ROTATED if rotated else tag)
-        self._at = ctypes.addressof(self._desc)
-
-    @property
-    def tag(self) -> int:
-        return self._desc.tag
-
-    @property
-    def rotated(self) -> bool:
-        return bool(self._desc.tag & TAG_ROTATED)
-
-    @rotated.setter
-    def rotated(self, value: bool) -> None:
-        self._desc.tag = (self._desc.tag & ~TAG_ROTATED) | (TAG_ROTATED if value else 0)
-
-    def desc(self) -> _Act4Desc:
-        return self._desc
-
-
-class Act8(_Held):
+@dataclass(init=False)
+class Act8:
     """int8 activations of the exact path: codes int8 [rows][K] (element order), scales fp32 [rows][K/32].
 
-    Act8(codes, scales_buf, rows, K, rotated) wraps two buffers; alloc_act8 makes one that holds both.
+    Act8(codes, scales_buf, rows, K, rotated) wraps two buffers; alloc_act8 makes one that holds both, and the two
+    fields' views of it are made when they are first asked for.
     """
-
-    __slots__ = ("_buf", "_codes", "_scales_buf")
+    codes: torch.Tensor
+    scales_buf: torch.Tensor  # uint8 buffer (padded to 16 bytes) holding the fp32 scales
+    rows: int
+    K: int
+    rotated: bool
 
     def __init__(self, codes: torch.Tensor, scales_buf: torch.Tensor, rows: int, K: int, rotated: bool):
-        self._buf, self._codes, self._scales_buf = None, codes, scales_buf
-        self._hold(codes.data_ptr(), scales_buf.data_ptr(), rows, K, TAG_ACT8, rotated)
+        self._whole, self._codes, self._scales_buf = None, codes, scales_buf
+        self.rows, self.K, self.rotated = rows, K, rotated
 
-    @property
-    def device(self) -> torch.device:
-        return (self._codes if self._buf is None else self._buf).device
+    def _split(self) -> None:
+        if self._whole is not None:
+            rows, K = self._shape
+            self._codes = self._whole[: rows * K].view(rows, K)
+            self._scales_buf = self._whole[rows * K:].view(torch.uint8)
+            self._whole = None
 
     @property
     def codes(self) -> torch.Tensor:
-        if self._codes is None:
-            self._codes = self._buf[: self.rows * self.K].view(self.rows, self.K)
+        self._split()
         return self._codes
+
+    @codes.setter
+    def codes(self, value: torch.Tensor) -> None:
+        self._split()
+        self._codes = value
 
     @property
     def scales_buf(self) -> torch.Tensor:
-        """uint8 buffer (padded to 16 bytes) holding the fp32 scales."""
-        if self._scales_buf is None:
-            self._scales_buf = self._buf[self.rows * self.K:].view(torch.uint8)
+        self._split()
         return self._scales_buf
+
+    @scales_buf.setter
+    def scales_buf(self, value: torch.Tensor) -> None:
+        self._split()
+        self._scales_buf = value
+
+    @property
+    def device(self) -> torch.device:
+        return (self._codes if self._whole is None else self._whole).device
 
     @property
     def scales(self) -> torch.Tensor:
         n = self.rows * (self.K // 32)
         return self.scales_buf[: 4 * n].view(torch.float32).view(self.rows, self.K // 32)
 
+    @property
+    def tag(self) -> int:
+        return TAG_ACT8 | (TAG_ROTATED if self.rotated else 0)
+
+    def desc(self) -> _Act4Desc:
+        n, w = self.rows * self.K, self._whole
+        if w is not None:
+            room = self._shape[0] * self._shape[1]
+            codes = w.data_ptr()
+            scales = codes + room
+        else:
+            room = min(self._codes.numel(), 8 * self._scales_buf.numel() * self._scales_buf.element_size())
+            codes, scales = self._codes.data_ptr(), self._scales_buf.data_ptr()
+        if n > room:
+            raise ValueError(f"rows={self.rows}, K={self.K}: the buffers hold less")
+        return _Act4Desc(codes, scales, self.rows, self.K, self.tag)
+
 
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
     if K <= 0 or K % 32:
         raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-    a = Act8.__new__(Act8)
+    a = Act8(None, None, rows, K, rotated)
     n = rows * K  # then K/32 fp32 scales a row, and a pad to 16 bytes
-    a._buf = buf = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device)
-    a._codes = a._scales_buf = None
-    ptr = buf.data_ptr()
-    a._hold(ptr, ptr + n, rows, K, TAG_ACT8, rotated)
+    a._whole, a._shape = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device), (rows, K)
     return a
 
 
@@ -717,19 +724,58 @@ def w4a16_gemm(w: Q4_0Weights, a: Act16, y: torch.Tensor | None = None, ws: torc
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-class MxFp4(_Held):
+class MxFp4:
     """MXFP4 weights or activations in the library's layout, in one buffer: e2m1 codes [rows][K/2] (element 2i
-    in the low nibble of byte i), then the scale bytes in tiles of 128 rows x 4 blocks (w4a4_mxfp4)."""
+    in the low nibble of byte i), then the scale bytes in tiles of 128 rows x 4 blocks (w4a4_mxfp4).
 
-    __slots__ = ("buf",)
+    Where the scales lie follows from rows and K, so buf, rows and K are fixed; the C descriptor is kept, and the
+    calls that write the operand stamp their rotation into it.
+    """
+
+    __slots__ = ("_buf", "_rows", "_K", "_desc", "_at")
 
     def __init__(self, rows: int, K: int, device, rotated: bool = True):
         if K <= 0 or K % 32:
             raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
         nc = rows * (K // 2)  # a multiple of 16
-        self.buf = torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
-        ptr = self.buf.data_ptr()
-        self._hold(ptr, ptr + nc, rows, K, TAG_MXFP4, rotated)
+        self._bind(torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device),
+                   rows, K, rotated)
+
+    def _bind(self, buf: torch.Tensor, rows: int, K: int, rotated: bool) -> None:
+        self._buf, self._rows, self._K = buf, rows, K
+        ptr = buf.data_ptr()
+        self._desc = _Act4Desc(ptr, ptr + rows * (K // 2), rows, K, TAG_MXFP4 | TAG_ROTATED if rotated else TAG_MXFP4)
+        self._at = ctypes.addressof(self._desc)
+
+    def __reduce__(self):  # copy, deepcopy and pickle: a descriptor of the copy's own buffer
+        return _mxfp4_of, (self._buf, self._rows, self._K, self.rotated)
+
+    @property
+    def buf(self) -> torch.Tensor:
+        return self._buf
+
+    @property
+    def rows(self) -> int:
+        return self._rows
+
+    @property
+    def K(self) -> int:
+        return self._K
+
+    @property
+    def tag(self) -> int:
+        return self._desc.tag
+
+    @property
+    def rotated(self) -> bool:
+        return bool(self._desc.tag & TAG_ROTATED)
+
+    @rotated.setter
+    def rotated(self, value: bool) -> None:
+        self._desc.tag = (self._desc.tag & ~TAG_ROTATED) | (TAG_ROTATED if value else 0)
+
+    def desc(self) -> _Act4Desc:
+        return _Act4Desc.from_buffer_copy(self._desc)
 
     @property
     def device(self) -> torch.device:
@@ -750,6 +796,12 @@ class MxFp4(_Held):
         rt, kt = (self.rows + 127) // 128, (self.K + 127) // 128
         t = self.scales_buf.view(rt, kt, 32, 4, 4).permute(0, 3, 2, 1, 4)
         return t.reshape(rt * 128, kt * 4)[: self.rows, : self.K // 32].contiguous()
+
+
+def _mxfp4_of(buf: torch.Tensor, rows: int, K: int, rotated: bool) -> MxFp4:
+    q = MxFp4.__new__(MxFp4)
+    q._bind(buf, rows, K, rotated)
+    return q
 
 
 def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
@@ -853,8 +905,7 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
 
 
 def _tagged(out, rotate):
-    if isinstance(out, Act4):  # the other operands' descriptors are their own, stamped by the call
-        out.rotated = bool(rotate)
+    out.rotated = bool(rotate)  # the call stamped a descriptor built from the fields
     return out
 
 
