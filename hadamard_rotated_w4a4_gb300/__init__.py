@@ -196,6 +196,17 @@ def _cuda(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
 
 
+def _fits(out, kind, rows: int, K: int, like: torch.Tensor, exact: bool = True):
+    """A caller's `out`: an operand of that kind on the input's device, for that result (exact) or with room for it."""
+    if not isinstance(out, kind):
+        raise ValueError(f"out must be {kind.__name__}, not {type(out).__name__}")
+    if out.K != K or out.rows < rows or (exact and out.rows != rows):
+        raise ValueError(f"out holds [{out.rows}][{out.K}], the result is [{rows}][{K}]")
+    if out.device != like.device:
+        raise ValueError(f"out is on {out.device}, the input on {like.device}")
+    return out
+
+
 @dataclass
 class Q4_0Weights:
     """Q4_0 weights in the library's layout: codes uint8 [rows][K/2], scales fp16 [rows][K/32],
@@ -219,6 +230,10 @@ class Q4_0Weights:
     def scales(self) -> torch.Tensor:
         n = self.rows * (self.K // 32)
         return self.scales_buf[: 2 * n].view(torch.float16).view(self.rows, self.K // 32)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
 
     @property
     def tag(self) -> int:
@@ -319,7 +334,7 @@ def h32_q4_0_pack_weights(w: torch.Tensor, rotate: bool = True, out: Q4_0Weights
     if dtype is None:
         raise ValueError("w must be bf16 or fp32")
     N, K = w.shape
-    out = out or alloc_q4_0(N, K, w.device, rotate, expanded)
+    out = alloc_q4_0(N, K, w.device, rotate, expanded) if out is None else _fits(out, Q4_0Weights, N, K, w, False)
     d = out.desc()
     ldw = w.stride(0) if N > 1 else K  # a single row's stride is meaningless (may be 0)
     _check(load_library().h32_q4_0_pack_weights(w.data_ptr(), dtype, N, K, ldw, int(rotate),
@@ -343,7 +358,7 @@ def h32_q4_0_pack_weights_imatrix(w: torch.Tensor, imatrix: torch.Tensor | None,
         _cuda(imatrix, "imatrix")
         if imatrix.dtype != torch.float32 or imatrix.numel() != K or not imatrix.is_contiguous():
             raise ValueError("imatrix must be a contiguous fp32 tensor of K values")
-    out = out or alloc_q4_0(N, K, w.device, rotate, expanded)
+    out = alloc_q4_0(N, K, w.device, rotate, expanded) if out is None else _fits(out, Q4_0Weights, N, K, w, False)
     d = out.desc()
     ldw = w.stride(0) if N > 1 else K
     _check(load_library().h32_q4_0_pack_weights_imatrix(
@@ -362,7 +377,8 @@ def q4_0_import(blocks: torch.Tensor, K: int, rotated: bool = True, out: Q4_0Wei
     if K <= 0 or K % 32 or blocks.numel() % (18 * (K // 32)):
         raise W4A4Error(1, "blocks size is not a multiple of a row of K/32 blocks")
     N = blocks.numel() // (18 * (K // 32))
-    out = out or alloc_q4_0(N, K, blocks.device, rotated, expanded)
+    out = (alloc_q4_0(N, K, blocks.device, rotated, expanded) if out is None
+           else _fits(out, Q4_0Weights, N, K, blocks, False))
     d = out.desc()
     _check(load_library().q4_0_import(blocks.data_ptr(), N, K, int(rotated), ctypes.byref(d), _stream(stream)))
     out.rotated = bool(rotated)
@@ -376,7 +392,7 @@ def w4a4_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act4 | N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = out or alloc_act4(M, K, x.device, rotate)
+    out = alloc_act4(M, K, x.device, rotate) if out is None else _fits(out, Act4, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a4_rotate_quantize_act(x.data_ptr(), M, K, ldx, int(rotate),
@@ -587,7 +603,7 @@ class Act8:
         return TAG_ACT8 | (TAG_ROTATED if self.rotated else 0)
 
     def desc(self) -> _Act4Desc:
-        n, w = self.rows * self.K, self._whole
+        rows, K, w = self.rows, self.K, self._whole
         if w is not None:
             room = self._shape[0] * self._shape[1]
             codes = w.data_ptr()
@@ -595,9 +611,9 @@ class Act8:
         else:
             room = min(self._codes.numel(), 8 * self._scales_buf.numel() * self._scales_buf.element_size())
             codes, scales = self._codes.data_ptr(), self._scales_buf.data_ptr()
-        if n > room:
-            raise ValueError(f"rows={self.rows}, K={self.K}: the buffers hold less")
-        return _Act4Desc(codes, scales, self.rows, self.K, self.tag)
+        if rows * K > room:
+            raise ValueError(f"rows={rows}, K={K}: the buffers hold less")
+        return _Act4Desc(codes, scales, rows, K, TAG_ACT8 | TAG_ROTATED if self.rotated else TAG_ACT8)
 
 
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
@@ -615,7 +631,7 @@ def w4a8_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act8 | N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = out or alloc_act8(M, K, x.device, rotate)
+    out = alloc_act8(M, K, x.device, rotate) if out is None else _fits(out, Act8, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a8_rotate_quantize_act(x.data_ptr(), M, K, ldx, int(rotate), ctypes.byref(d),
@@ -667,6 +683,10 @@ class Act16:
     rotated: bool
 
     @property
+    def device(self) -> torch.device:
+        return self.values.device
+
+    @property
     def tag(self) -> int:
         return TAG_ACT16 | (TAG_ROTATED if self.rotated else 0)
 
@@ -689,7 +709,7 @@ def w4a16_rotate_act(x: torch.Tensor, rotate: bool = True, out: Act16 | None = N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = out or alloc_act16(M, K, x.device, rotate)
+    out = alloc_act16(M, K, x.device, rotate) if out is None else _fits(out, Act16, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a16_rotate_act(x.data_ptr(), M, K, ldx, int(rotate), ctypes.byref(d), _stream(stream)))
@@ -732,7 +752,7 @@ class MxFp4:
     calls that write the operand stamp their rotation into it.
     """
 
-    __slots__ = ("_buf", "_rows", "_K", "_desc", "_at")
+    __slots__ = ("_buf", "_rows", "_K", "_gpu", "_desc", "_at")
 
     def __init__(self, rows: int, K: int, device, rotated: bool = True):
         if K <= 0 or K % 32:
@@ -742,7 +762,7 @@ class MxFp4:
                    rows, K, rotated)
 
     def _bind(self, buf: torch.Tensor, rows: int, K: int, rotated: bool) -> None:
-        self._buf, self._rows, self._K = buf, rows, K
+        self._buf, self._rows, self._K, self._gpu = buf, rows, K, buf.is_cuda
         ptr = buf.data_ptr()
         self._desc = _Act4Desc(ptr, ptr + rows * (K // 2), rows, K, TAG_MXFP4 | TAG_ROTATED if rotated else TAG_MXFP4)
         self._at = ctypes.addressof(self._desc)
@@ -779,7 +799,7 @@ class MxFp4:
 
     @property
     def device(self) -> torch.device:
-        return self.buf.device
+        return self._buf.device
 
     @property
     def codes(self) -> torch.Tensor:
@@ -820,17 +840,11 @@ def _rows(t: torch.Tensor, name: str, shape=None) -> int:
     return st[0] if M > 1 else K  # a single row's stride is meaningless (may be 0)
 
 
-def _fits(out, rows: int, K: int):
-    if out.rows != rows or out.K != K:
-        raise ValueError(f"out holds [{out.rows}][{out.K}], the result is [{rows}][{K}]")
-    return out
-
-
 def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | None = None, stream=None) -> MxFp4:
     """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
     ldx = _rows(x, "x")
     rows, K = x.shape
-    out = MxFp4(rows, K, x.device, rotate) if out is None else _fits(out, rows, K)
+    out = MxFp4(rows, K, x.device, rotate) if out is None else _fits(out, MxFp4, rows, K, x)
     _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, rotate, out._at,
                                                 _stream(stream)))
     return out
@@ -846,18 +860,25 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
     rows, K = codes.shape[0], 2 * codes.shape[1]
     if K <= 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
         raise W4A4Error(1, "codes [rows][K/2] and scales [rows][K/32] disagree, or K is not a multiple of 32")
-    out = MxFp4(rows, K, codes.device, rotated) if out is None else _fits(out, rows, K)
+    out = MxFp4(rows, K, codes.device, rotated) if out is None else _fits(out, MxFp4, rows, K, codes)
     _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, rotated, out._at,
                                        _stream(stream)))
     return out
 
 
-def _dequantize(call, a, y, dtype, stream) -> torch.Tensor:
+def _held(q):
+    """The descriptor that a call reads or stamps: an MxFp4's own, another operand's built from its fields."""
+    return q._desc if isinstance(q, MxFp4) else q.desc()
+
+
+def _dequantize(call, kind, a, y, dtype, stream) -> torch.Tensor:
+    if not isinstance(a, kind) or not (a._gpu if kind is MxFp4 else a.device.type == "cuda"):
+        raise ValueError(f"a must be an {kind.__name__} on the GPU")
     if y is None:
         y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=a.device), a.K
     else:
         ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
-    d = a.desc()
+    d = _held(a)
     _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(dtype, -1), ldy, _stream(stream)))
     return y
 
@@ -865,19 +886,19 @@ def _dequantize(call, a, y, dtype, stream) -> torch.Tensor:
 def mxfp4_dequantize(a: MxFp4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                      stream=None) -> torch.Tensor:
     """The values that MXFP4 codes and scales stand for ([rows][K], fp32 or bf16; a rotation is not undone)."""
-    return _dequantize(load_library().mxfp4_dequantize, a, y, dtype, stream)
+    return _dequantize(load_library().mxfp4_dequantize, MxFp4, a, y, dtype, stream)
 
 
 def w4a4_dequantize_act(a: Act4, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                         stream=None) -> torch.Tensor:
     """The values that int4 codes and scales stand for, as mxfp4_dequantize."""
-    return _dequantize(load_library().w4a4_dequantize_act, a, y, dtype, stream)
+    return _dequantize(load_library().w4a4_dequantize_act, Act4, a, y, dtype, stream)
 
 
 def w4a8_dequantize_act(a: Act8, y: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
                         stream=None) -> torch.Tensor:
     """The values that int8 codes and scales stand for, as mxfp4_dequantize."""
-    return _dequantize(load_library().w4a8_dequantize_act, a, y, dtype, stream)
+    return _dequantize(load_library().w4a8_dequantize_act, Act8, a, y, dtype, stream)
 
 
 def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -891,8 +912,10 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     ws: True = the cached per-stream workspace (the last wave cut over the SMs where that pays), a tensor = that
     workspace (zero before its first use), None/False = whole tiles only.
     """
+    if not (isinstance(w, MxFp4) and isinstance(a, MxFp4) and w._gpu and a._gpu):
+        raise ValueError("w and a must be MxFp4 operands on the GPU")
     if y is None:
-        y, ldy = torch.empty(a.rows, w.rows, dtype=dtype, device=w.buf.device), w.rows
+        y, ldy = torch.empty(a.rows, w.rows, dtype=dtype, device=w.device), w.rows
     else:
         ldy = _rows(y, "y", (a.rows, w.rows))
     lib, st = load_library(), _stream(stream)
@@ -905,11 +928,12 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
 
 
 def _tagged(out, rotate):
-    out.rotated = bool(rotate)  # the call stamped a descriptor built from the fields
+    if not isinstance(out, MxFp4):  # the call stamped a descriptor built from the fields
+        out.rotated = bool(rotate)
     return out
 
 
-def _rmsnorm(call, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
+def _rmsnorm(call, kind, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
     ldx = _rows(x, "x")
     M, K = shape = x.shape
     r = r_out = gp = None
@@ -931,8 +955,8 @@ def _rmsnorm(call, alloc, x, g, residual, residual_out, eps, rotate, out, stream
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
         gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
     n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
-    out = alloc(M, K, x.device, rotate) if out is None else _fits(out, M, K)
-    d = out.desc()
+    out = alloc(M, K, x.device, rotate) if out is None else _fits(out, kind, M, K, x)
+    d = _held(out)
     _check(call(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
     return _tagged(out, rotate)
 
@@ -945,30 +969,30 @@ def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, ep
     x, residual: [M][K], bf16 or fp32 each.  h is written to residual_out, in place into
     residual when that is None; without a residual, h = x and nothing is written.
     """
-    return _rmsnorm(load_library().w4a4_rmsnorm_quantize_act, alloc_act4, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().w4a4_rmsnorm_quantize_act, Act4, alloc_act4, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
 def w4a8_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
                               residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
                               rotate: bool = True, out: Act8 | None = None, stream=None) -> Act8:
     """As w4a4_rmsnorm_quantize_act, to int8 codes."""
-    return _rmsnorm(load_library().w4a8_rmsnorm_quantize_act, alloc_act8, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().w4a8_rmsnorm_quantize_act, Act8, alloc_act8, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
 def mxfp4_rmsnorm_quantize(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
                            residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
                            rotate: bool = True, out: MxFp4 | None = None, stream=None) -> MxFp4:
     """As w4a4_rmsnorm_quantize_act, to MXFP4."""
-    return _rmsnorm(load_library().mxfp4_rmsnorm_quantize, MxFp4, x, g, residual, residual_out, eps, rotate, out, stream)
+    return _rmsnorm(load_library().mxfp4_rmsnorm_quantize, MxFp4, MxFp4, x, g, residual, residual_out, eps, rotate, out, stream)
 
 
-def _swiglu(call, alloc, gate, up, rotate, out, stream):
+def _swiglu(call, kind, alloc, gate, up, rotate, out, stream):
     ldg, ldu = _rows(gate, "gate"), _rows(up, "up", gate.shape)
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    out = alloc(M, K, gate.device, rotate) if out is None else _fits(out, M, K)
-    d = out.desc()
+    out = alloc(M, K, gate.device, rotate) if out is None else _fits(out, kind, M, K, gate)
+    d = _held(out)
     _check(call(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate, ctypes.addressof(d),
                 _stream(stream)))
     return _tagged(out, rotate)
@@ -977,16 +1001,16 @@ def _swiglu(call, alloc, gate, up, rotate, out, stream):
 def w4a4_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act4 | None = None,
                              stream=None) -> Act4:
     """y = silu(gate) * up (both [M][K], bf16 or fp32), rotated and rounded to int4, in one pass."""
-    return _swiglu(load_library().w4a4_swiglu_quantize_act, alloc_act4, gate, up, rotate, out, stream)
+    return _swiglu(load_library().w4a4_swiglu_quantize_act, Act4, alloc_act4, gate, up, rotate, out, stream)
 
 
 def w4a8_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act8 | None = None,
                              stream=None) -> Act8:
     """As w4a4_swiglu_quantize_act, to int8 codes."""
-    return _swiglu(load_library().w4a8_swiglu_quantize_act, alloc_act8, gate, up, rotate, out, stream)
+    return _swiglu(load_library().w4a8_swiglu_quantize_act, Act8, alloc_act8, gate, up, rotate, out, stream)
 
 
 def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: MxFp4 | None = None,
                           stream=None) -> MxFp4:
     """As w4a4_swiglu_quantize_act, to MXFP4."""
-    return _swiglu(load_library().mxfp4_swiglu_quantize, MxFp4, gate, up, rotate, out, stream)
+    return _swiglu(load_library().mxfp4_swiglu_quantize, MxFp4, MxFp4, gate, up, rotate, out, stream)
