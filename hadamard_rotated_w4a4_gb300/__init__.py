@@ -191,6 +191,34 @@ def _stream(stream=None) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_at(handle: int):
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _buffers(made):
+    if isinstance(made, torch.Tensor):
+        return (made,)
+    return [t for t in vars(made).values() if isinstance(t, torch.Tensor)] if hasattr(made, "__dict__") else (made.buf,)
+
+
+def _made(stream, make, *args, **kwargs):
+    """make(...), the memory that a call allocates, on the stream that it launches on.
+
+    On a stream other than the current one, memory of the current stream's pool could still be in use by what
+    that stream has queued.  The result's next reader is taken to be the current stream: freed memory waits for it.
+    """
+    if stream is None:
+        return make(*args, **kwargs)
+    handle, here = _stream(stream), torch.cuda.current_stream()
+    if handle == here.cuda_stream:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(_stream_at(handle)):
+        made = make(*args, **kwargs)
+    for t in _buffers(made):
+        t.record_stream(here)
+    return made
+
+
 def _cuda(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
@@ -334,7 +362,8 @@ def h32_q4_0_pack_weights(w: torch.Tensor, rotate: bool = True, out: Q4_0Weights
     if dtype is None:
         raise ValueError("w must be bf16 or fp32")
     N, K = w.shape
-    out = alloc_q4_0(N, K, w.device, rotate, expanded) if out is None else _fits(out, Q4_0Weights, N, K, w, False)
+    out = (_made(stream, alloc_q4_0, N, K, w.device, rotate, expanded) if out is None
+           else _fits(out, Q4_0Weights, N, K, w, False))
     d = out.desc()
     ldw = w.stride(0) if N > 1 else K  # a single row's stride is meaningless (may be 0)
     _check(load_library().h32_q4_0_pack_weights(w.data_ptr(), dtype, N, K, ldw, int(rotate),
@@ -358,7 +387,8 @@ def h32_q4_0_pack_weights_imatrix(w: torch.Tensor, imatrix: torch.Tensor | None,
         _cuda(imatrix, "imatrix")
         if imatrix.dtype != torch.float32 or imatrix.numel() != K or not imatrix.is_contiguous():
             raise ValueError("imatrix must be a contiguous fp32 tensor of K values")
-    out = alloc_q4_0(N, K, w.device, rotate, expanded) if out is None else _fits(out, Q4_0Weights, N, K, w, False)
+    out = (_made(stream, alloc_q4_0, N, K, w.device, rotate, expanded) if out is None
+           else _fits(out, Q4_0Weights, N, K, w, False))
     d = out.desc()
     ldw = w.stride(0) if N > 1 else K
     _check(load_library().h32_q4_0_pack_weights_imatrix(
@@ -377,7 +407,7 @@ def q4_0_import(blocks: torch.Tensor, K: int, rotated: bool = True, out: Q4_0Wei
     if K <= 0 or K % 32 or blocks.numel() % (18 * (K // 32)):
         raise W4A4Error(1, "blocks size is not a multiple of a row of K/32 blocks")
     N = blocks.numel() // (18 * (K // 32))
-    out = (alloc_q4_0(N, K, blocks.device, rotated, expanded) if out is None
+    out = (_made(stream, alloc_q4_0, N, K, blocks.device, rotated, expanded) if out is None
            else _fits(out, Q4_0Weights, N, K, blocks, False))
     d = out.desc()
     _check(load_library().q4_0_import(blocks.data_ptr(), N, K, int(rotated), ctypes.byref(d), _stream(stream)))
@@ -392,7 +422,7 @@ def w4a4_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act4 | N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = alloc_act4(M, K, x.device, rotate) if out is None else _fits(out, Act4, M, K, x, False)
+    out = _made(stream, alloc_act4, M, K, x.device, rotate) if out is None else _fits(out, Act4, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a4_rotate_quantize_act(x.data_ptr(), M, K, ldx, int(rotate),
@@ -411,7 +441,8 @@ _GEMM_WS: dict = {}
 def gemm_workspace(M: int, N: int, K: int, device, stream=None, need: int | None = None) -> torch.Tensor | None:
     """A zero-initialised GEMM workspace kept per (device, stream), grown on demand.
 
-    One per stream, because calls sharing a workspace must not overlap on the GPU.
+    One per stream, because calls sharing a workspace must not overlap on the GPU; allocated and zeroed on it, so
+    that its first product finds it zero whatever the current stream is at.
     ``need`` overrides the size query (the exact path has its own).
     """
     if need is None:
@@ -421,7 +452,7 @@ def gemm_workspace(M: int, N: int, K: int, device, stream=None, need: int | None
     key = (torch.device(device).index, _stream(stream))
     ws = _GEMM_WS.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = _made(stream, torch.zeros, need, dtype=torch.uint8, device=device)
         _GEMM_WS[key] = ws
     return ws
 
@@ -434,7 +465,7 @@ def w4a4_gemm(w: Q4_0Weights, a: Act4, y: torch.Tensor | None = None, ws: torch.
     = that workspace (zero before its first use), None/False = whole-tile schedule.
     """
     if y is None:
-        y = torch.empty(a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
+        y = _made(stream, torch.empty, a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
     _cuda(y, "y")
     if y.dtype != torch.float32 or y.dim() != 2 or y.stride(1) != 1:
         raise ValueError("y must be a 2-D fp32 tensor with unit stride along N")
@@ -453,7 +484,7 @@ def w4a4_gemm_small_m(w: Q4_0Weights, a: Act4, y: torch.Tensor | None = None, st
     """w4a4_gemm for 1 to 8 activation rows (a verification batch): the weight-streaming kernel,
     bit for bit the tensor-core kernel's whole-tile result."""
     if y is None:
-        y = torch.empty(a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
+        y = _made(stream, torch.empty, a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
     _cuda(y, "y")
     if y.dtype != torch.float32 or y.dim() != 2 or y.stride(1) != 1:
         raise ValueError("y must be a 2-D fp32 tensor with unit stride along N")
@@ -466,7 +497,7 @@ def w4a4_gemm_small_m(w: Q4_0Weights, a: Act4, y: torch.Tensor | None = None, st
 def w4a4_gemm_partials(w: Q4_0Weights, a: Act4, P: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Exact per-block integer partials P[m][n][b] (int32), from the tensor-core main loop."""
     if P is None:
-        P = torch.empty(a.rows, w.rows, w.K // 32, dtype=torch.int32, device=w.codes.device)
+        P = _made(stream, torch.empty, a.rows, w.rows, w.K // 32, dtype=torch.int32, device=w.codes.device)
     _cuda(P, "P")
     _check(load_library().w4a4_gemm_partials(ctypes.byref(w.desc()), ctypes.byref(a.desc()), P.data_ptr(),
                                              _stream(stream)))
@@ -486,10 +517,10 @@ def w4a4_gemm_id(experts: Q4_0Weights, E: int, a: Act4, ids: torch.Tensor, top_k
     M = ids.shape[0]
     N = experts.rows // E
     if y is None:
-        y = torch.empty(M, top_k, N, dtype=torch.float32, device=ids.device)
+        y = _made(stream, torch.empty, M, top_k, N, dtype=torch.float32, device=ids.device)
     need = w4a4_gemm_id_workspace_bytes(M, top_k, E, a.K)
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=ids.device)
+        ws = _made(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=ids.device)
     _check(load_library().w4a4_gemm_id(ctypes.byref(experts.desc()), E, N, ctypes.byref(a.desc()), ids.data_ptr(),
                                        M, top_k, int(act_per_slot), y.data_ptr(), ws.data_ptr(),
                                        ws.numel() * ws.element_size(), _stream(stream)))
@@ -631,7 +662,7 @@ def w4a8_rotate_quantize_act(x: torch.Tensor, rotate: bool = True, out: Act8 | N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = alloc_act8(M, K, x.device, rotate) if out is None else _fits(out, Act8, M, K, x, False)
+    out = _made(stream, alloc_act8, M, K, x.device, rotate) if out is None else _fits(out, Act8, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a8_rotate_quantize_act(x.data_ptr(), M, K, ldx, int(rotate), ctypes.byref(d),
@@ -648,7 +679,7 @@ def w4a8_gemm(w: Q4_0Weights, a: Act8, y: torch.Tensor | None = None, ws: torch.
               stream=None) -> torch.Tensor:
     """The exact path: Y[m][n] = sum_b d_w d_a P with int8 activations (fp32 [M][N]); ws as for w4a4_gemm."""
     if y is None:
-        y = torch.empty(a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
+        y = _made(stream, torch.empty, a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
     _cuda(y, "y")
     if y.dtype != torch.float32 or y.dim() != 2 or y.stride(1) != 1:
         raise ValueError("y must be a 2-D fp32 tensor with unit stride along N")
@@ -666,7 +697,7 @@ def w4a8_gemm(w: Q4_0Weights, a: Act8, y: torch.Tensor | None = None, ws: torch.
 def w4a8_gemm_partials(w: Q4_0Weights, a: Act8, P: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Exact per-block integer partials of the exact path, P[m][n][b] (int32)."""
     if P is None:
-        P = torch.empty(a.rows, w.rows, w.K // 32, dtype=torch.int32, device=w.codes.device)
+        P = _made(stream, torch.empty, a.rows, w.rows, w.K // 32, dtype=torch.int32, device=w.codes.device)
     _cuda(P, "P")
     _check(load_library().w4a8_gemm_partials(ctypes.byref(w.desc()), ctypes.byref(a.desc()), P.data_ptr(),
                                              _stream(stream)))
@@ -709,7 +740,7 @@ def w4a16_rotate_act(x: torch.Tensor, rotate: bool = True, out: Act16 | None = N
     if x.dtype != torch.float32 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D fp32 tensor with unit stride along K")
     M, K = x.shape
-    out = alloc_act16(M, K, x.device, rotate) if out is None else _fits(out, Act16, M, K, x, False)
+    out = _made(stream, alloc_act16, M, K, x.device, rotate) if out is None else _fits(out, Act16, M, K, x, False)
     d = out.desc()
     ldx = x.stride(0) if M > 1 else K
     _check(load_library().w4a16_rotate_act(x.data_ptr(), M, K, ldx, int(rotate), ctypes.byref(d), _stream(stream)))
@@ -725,7 +756,7 @@ def w4a16_gemm(w: Q4_0Weights, a: Act16, y: torch.Tensor | None = None, ws: torc
                stream=None) -> torch.Tensor:
     """The rotate-only route: Y[m][n] = sum_b d_w sum_j y (q_w - 8) with bf16 activations (fp32 [M][N])."""
     if y is None:
-        y = torch.empty(a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
+        y = _made(stream, torch.empty, a.rows, w.rows, dtype=torch.float32, device=w.codes.device)
     _cuda(y, "y")
     if y.dtype != torch.float32 or y.dim() != 2 or y.stride(1) != 1:
         raise ValueError("y must be a 2-D fp32 tensor with unit stride along N")
@@ -844,7 +875,7 @@ def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | Non
     """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
     ldx = _rows(x, "x")
     rows, K = x.shape
-    out = MxFp4(rows, K, x.device, rotate) if out is None else _fits(out, MxFp4, rows, K, x)
+    out = _made(stream, MxFp4, rows, K, x.device, rotate) if out is None else _fits(out, MxFp4, rows, K, x)
     _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, rotate, out._at,
                                                 _stream(stream)))
     return out
@@ -860,7 +891,7 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
     rows, K = codes.shape[0], 2 * codes.shape[1]
     if K <= 0 or K % 32 or tuple(scales.shape) != (rows, K // 32):
         raise W4A4Error(1, "codes [rows][K/2] and scales [rows][K/32] disagree, or K is not a multiple of 32")
-    out = MxFp4(rows, K, codes.device, rotated) if out is None else _fits(out, MxFp4, rows, K, codes)
+    out = _made(stream, MxFp4, rows, K, codes.device, rotated) if out is None else _fits(out, MxFp4, rows, K, codes)
     _check(load_library().mxfp4_import(codes.data_ptr(), scales.data_ptr(), rows, K, rotated, out._at,
                                        _stream(stream)))
     return out
@@ -875,7 +906,7 @@ def _dequantize(call, kind, a, y, dtype, stream) -> torch.Tensor:
     if not isinstance(a, kind) or not (a._gpu if kind is MxFp4 else a.device.type == "cuda"):
         raise ValueError(f"a must be an {kind.__name__} on the GPU")
     if y is None:
-        y, ldy = torch.empty(a.rows, a.K, dtype=dtype, device=a.device), a.K
+        y, ldy = _made(stream, torch.empty, a.rows, a.K, dtype=dtype, device=a.device), a.K
     else:
         ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
     d = _held(a)
@@ -915,7 +946,7 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     if not (isinstance(w, MxFp4) and isinstance(a, MxFp4) and w._gpu and a._gpu):
         raise ValueError("w and a must be MxFp4 operands on the GPU")
     if y is None:
-        y, ldy = torch.empty(a.rows, w.rows, dtype=dtype, device=w.device), w.rows
+        y, ldy = _made(stream, torch.empty, a.rows, w.rows, dtype=dtype, device=w.device), w.rows
     else:
         ldy = _rows(y, "y", (a.rows, w.rows))
     lib, st = load_library(), _stream(stream)
@@ -955,7 +986,7 @@ def _rmsnorm(call, kind, alloc, x, g, residual, residual_out, eps, rotate, out, 
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
         gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
     n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
-    out = alloc(M, K, x.device, rotate) if out is None else _fits(out, kind, M, K, x)
+    out = _made(stream, alloc, M, K, x.device, rotate) if out is None else _fits(out, kind, M, K, x)
     d = _held(out)
     _check(call(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
     return _tagged(out, rotate)
@@ -991,7 +1022,7 @@ def _swiglu(call, kind, alloc, gate, up, rotate, out, stream):
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    out = alloc(M, K, gate.device, rotate) if out is None else _fits(out, kind, M, K, gate)
+    out = _made(stream, alloc, M, K, gate.device, rotate) if out is None else _fits(out, kind, M, K, gate)
     d = _held(out)
     _check(call(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate, ctypes.addressof(d),
                 _stream(stream)))
