@@ -436,10 +436,16 @@ def w4a4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
 
 
 _GEMM_WS: dict = {}
+#: workspaces that were outgrown, or dropped after a timeout: a CUDA graph may hold their address
+_GEMM_WS_OLD: dict = {}
+_WS_COUNTERS = 1 << 20  # bytes at a workspace's start that a product wants zero
 
 
 def gemm_workspace(M: int, N: int, K: int, device, stream=None, need: int | None = None) -> torch.Tensor | None:
     """A zero-initialised GEMM workspace kept per (device, stream), grown on demand.
+
+    One that is outgrown stays allocated, for the graphs that were captured with it.  During a capture a cached one is
+    used if it is large enough, and none is added: the graph then has a workspace of its own.
 
     One per stream, because calls sharing a workspace must not overlap on the GPU; allocated and zeroed on it, so
     that its first product finds it zero whatever the current stream is at.
@@ -451,10 +457,46 @@ def gemm_workspace(M: int, N: int, K: int, device, stream=None, need: int | None
         return None
     key = (torch.device(device).index, _stream(stream))
     ws = _GEMM_WS.get(key)
-    if ws is None or ws.numel() < need:
-        ws = _made(stream, torch.zeros, need, dtype=torch.uint8, device=device)
-        _GEMM_WS[key] = ws
+    if ws is not None and ws.numel() >= need:
+        return ws
+    if _capturing(stream):
+        return _made(stream, _graph_workspace, need, device)
+    old = _GEMM_WS_OLD.setdefault(key, [])
+    if ws is not None:
+        old.append(ws)
+    at = next((i for i, t in enumerate(old) if t.numel() >= need), None)
+    ws = _made(stream, torch.zeros, need, dtype=torch.uint8, device=device) if at is None else old.pop(at)
+    _GEMM_WS[key] = ws
     return ws
+
+
+def _capturing(stream) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_stream_at(_stream(stream))):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _graph_workspace(need: int, device) -> torch.Tensor:
+    """A workspace of the graph being captured, zeroed by the graph: memory of its pool, which no other call may keep."""
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:_WS_COUNTERS].zero_()
+    return ws
+
+
+def _retire_workspaces() -> None:
+    """Zero every workspace, with nothing running that uses one, and take none of them for the current one."""
+    for key, ws in _GEMM_WS.items():
+        _GEMM_WS_OLD.setdefault(key, []).append(ws)
+    _GEMM_WS.clear()
+    kept = [ws for old in _GEMM_WS_OLD.values() for ws in old]
+    devices = {ws.device for ws in kept if ws.is_cuda}
+    for device in devices:
+        torch.cuda.synchronize(device)
+    for ws in kept:
+        ws.zero_()
+    for device in devices:
+        torch.cuda.synchronize(device)
 
 
 def w4a4_gemm(w: Q4_0Weights, a: Act4, y: torch.Tensor | None = None, ws: torch.Tensor | None | bool = True,
@@ -555,13 +597,14 @@ def w4a4_check(stream=None) -> None:
 
     A kernel that gave up may leave stream-K arrival tickets standing in its
     workspace, and a later call on that workspace would then finish its cut
-    tiles wrongly.  So on a timeout every cached per-stream workspace is dropped
-    (the next call allocates a zeroed one); a workspace the caller passed in
-    must be zeroed by the caller before it is used again.
+    tiles wrongly.  So on a timeout the GPU is waited for and every cached
+    per-stream workspace is zeroed, for the next call and for the graphs captured
+    with it; a workspace the caller passed in must be zeroed by the caller before
+    it is used again.
     """
     status = load_library().w4a4_check(_stream(stream))
     if status == 8:  # W4A4_ERR_TIMEOUT
-        _GEMM_WS.clear()
+        _retire_workspaces()
     _check(status)
 
 
