@@ -220,11 +220,13 @@ __device__ __forceinline__ void quad_quantize(float (&v)[8], int q, bool ok, I c
     constexpr float kTop = FMT == kInt4 ? 7.0f : 127.0f;
     constexpr float kLow = FMT == kInt4 ? -8.0f : -127.0f;
     const float d = bad ? __uint_as_float(0x7FC00000u) : div_by(a, kTop);
-    // a scale below the normal range has no finite reciprocal: codes of 0
-    const float inv = d < 1.17549435e-38f ? 0.0f : __frcp_rn(d);
+    // a scale without a finite reciprocal (2^-128 at most, or NaN): codes of 0
+    const float rcp = __frcp_rn(d);
+    const float inv = rcp <= 3.402823466e38f ? rcp : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v2[i] = __fmul2_rn(v2[i], make_float2(inv, inv));
-    // Where the scale is finite, |v| is at most kTop and a few ulp:
+    // Where the scale is finite, |v| is at most kTop and a part in 2^21 of it (a few ulp, and
+    // the rounding of a subnormal d):
     // v + 1.5 * 2^23 is 1.5 * 2^23 plus the nearest integer (ties to even), whose low
     // byte is that integer in two's complement.  It is the rounding half away from zero
     // unless some v lies halfway (or is NaN); then the general path rounds.

@@ -520,7 +520,8 @@ size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * NaN; so does a row of zeros with eps = 0 (0 * infinity).  An infinity, or squares
  * that overflow fp32, make the norm infinite: finite values become 0, the blocks
  * (int4, int8, MXFP4) that hold an infinity read back as NaN.  An int4 or int8 block
- * whose scale would be below 2^-126 reads back as zeros, here and below.
+ * whose scale has no finite reciprocal (2^-128 or less) reads back as zeros, here and
+ * below.
  */
 typedef struct {
   const void* x;
