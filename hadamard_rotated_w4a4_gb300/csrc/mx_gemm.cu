@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kTW = 128;      // weight rows per CTA
 constexpr int kStageK = 256;  // elements of K per stage
-// Bound of every wait, about a second, in SM cycles (of 2 GHz at most).
+// Bound of every wait in SM cycles: 1.04 s at 2.07 GHz, the top clock, longer below it.
 constexpr int64_t kWaitCycles = int64_t(1) << 31;
 constexpr int kWBytes = kTW * 128;
 constexpr int kSfTile = 1024;  // a stage's scales of 128 rows: two 512-byte tiles
@@ -54,7 +54,6 @@ struct MxArgs {
   int apart;    // small kernel: where the partial tiles lie, 0 = over the stages
   // pair kernel
   int mt, wt;   // token tiles (the last one narrower), weight tiles
-  int tiles;
   int whole;    // tiles 0 .. whole - 1 go to the pairs whole, in turn; the rest by stages
   int64_t units;     // stages of the rest (0: none)
   uint32_t* flags;   // [pairs][2 CTAs][8 warps], zero between calls
@@ -801,8 +800,9 @@ size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return use_sma
 
 static int64_t g_wait = kWaitCycles, g_delay = 0;
 void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
-  g_wait = wait_ns ? static_cast<int64_t>(2 * wait_ns) : kWaitCycles;
-  g_delay = static_cast<int64_t>(2 * producer_delay_ns);
+  const auto cycles = [](uint64_t ns) { return static_cast<int64_t>(ns / 100 * 207 + ns % 100 * 207 / 100); };  // 2.07 GHz
+  g_wait = wait_ns ? cycles(wait_ns) : kWaitCycles;
+  g_delay = cycles(producer_delay_ns);
 }
 
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
@@ -821,7 +821,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
     a.box = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   } else {
     q = plan_pair(M, N, K);
-    a.mt = q.mt; a.wt = static_cast<int>((N + 255) / 256); a.tiles = q.tiles; a.whole = q.tiles;
+    a.mt = q.mt; a.wt = static_cast<int>((N + 255) / 256); a.whole = q.tiles;
     if (ws && q.units > 0) {
       a.whole = q.whole;
       a.units = q.units;
