@@ -624,7 +624,8 @@ class Act8:
     """int8 activations of the exact path: codes int8 [rows][K] (element order), scales fp32 [rows][K/32].
 
     Act8(codes, scales_buf, rows, K, rotated) wraps two buffers; alloc_act8 makes one that holds both, and the two
-    fields' views of it are made when they are first asked for.
+    fields' views of it are made when they are first asked for.  Until then its address cannot change, and a C
+    descriptor of it is kept.
     """
     codes: torch.Tensor
     scales_buf: torch.Tensor  # uint8 buffer (padded to 16 bytes) holding the fp32 scales
@@ -633,7 +634,8 @@ class Act8:
     rotated: bool
 
     def __init__(self, codes: torch.Tensor, scales_buf: torch.Tensor, rows: int, K: int, rotated: bool):
-        self._whole, self._codes, self._scales_buf = None, codes, scales_buf
+        self._whole = self._kept = None
+        self._codes, self._scales_buf = codes, scales_buf
         self.rows, self.K, self.rotated = rows, K, rotated
 
     def _split(self) -> None:
@@ -641,7 +643,10 @@ class Act8:
             rows, K = self._shape
             self._codes = self._whole[: rows * K].view(rows, K)
             self._scales_buf = self._whole[rows * K:].view(torch.uint8)
-            self._whole = None
+            self._whole = self._kept = None
+
+    def __getstate__(self):  # copy, deepcopy and pickle: the descriptor is not the copy's
+        return {**self.__dict__, "_kept": None}
 
     @property
     def codes(self) -> torch.Tensor:
@@ -693,9 +698,12 @@ class Act8:
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
     if K <= 0 or K % 32:
         raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
-    a = Act8(None, None, rows, K, rotated)
+    a = Act8.__new__(Act8)
+    a.rows, a.K, a.rotated, a._shape = rows, K, rotated, (rows, K)
     n = rows * K  # then K/32 fp32 scales a row, and a pad to 16 bytes
-    a._whole, a._shape = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device), (rows, K)
+    a._whole = whole = torch.empty(n + n // 8 + 16, dtype=torch.int8, device=device)
+    ptr = whole.data_ptr()
+    a._kept = _Act4Desc(ptr, ptr + n, rows, K, TAG_ACT8 | TAG_ROTATED if rotated else TAG_ACT8)
     return a
 
 
@@ -941,15 +949,24 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
 
 
 def _held(q):
-    """The descriptor that a call reads or stamps: an MxFp4's own, another operand's built from its fields."""
-    return q._desc if isinstance(q, MxFp4) else q.desc()
+    """The descriptor that a call reads, or stamps with q's own rows and K: the kept one where it says what the
+    fields do, else one built from the fields."""
+    if isinstance(q, MxFp4):
+        return q._desc
+    if isinstance(q, Act8):
+        d = q._kept
+        if d is not None and d.rows == q.rows and d.K == q.K:
+            d.tag = TAG_ACT8 | TAG_ROTATED if q.rotated else TAG_ACT8
+            return d
+    return q.desc()
 
 
 def _dequantize(call, kind, a, y, dtype, stream) -> torch.Tensor:
-    if not isinstance(a, kind) or not (a._gpu if kind is MxFp4 else a.device.type == "cuda"):
+    device = a.device if isinstance(a, kind) else None
+    if device is None or device.type != "cuda":
         raise ValueError(f"a must be an {kind.__name__} on the GPU")
     if y is None:
-        y, ldy = _made(stream, torch.empty, a.rows, a.K, dtype=dtype, device=a.device), a.K
+        y, ldy = _made(stream, torch.empty, a.rows, a.K, dtype=dtype, device=device), a.K
     else:
         ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
     d = _held(a)
