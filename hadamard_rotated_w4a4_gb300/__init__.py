@@ -318,6 +318,8 @@ class Act4:
         return _Act4Desc(self.codes.data_ptr(), self.scales_buf.data_ptr(), self.rows, self.K, self.tag,
                          self.expanded.data_ptr() if self.expanded is not None else None)
 
+    _ref = desc
+
 
 def alloc_q4_0(rows: int, K: int, device, rotated: bool = True, expanded: bool = False) -> Q4_0Weights:
     """Buffers for Q4_0 weights.  expanded=True also allocates the optional expanded
@@ -694,6 +696,14 @@ class Act8:
             raise ValueError(f"rows={rows}, K={K}: the buffers hold less")
         return _Act4Desc(codes, scales, rows, K, TAG_ACT8 | TAG_ROTATED if self.rotated else TAG_ACT8)
 
+    def _ref(self) -> _Act4Desc:
+        """The descriptor for a call: the kept one where it says what the fields do."""
+        d = self._kept
+        if d is None or d.rows != self.rows or d.K != self.K:
+            return self.desc()
+        d.tag = TAG_ACT8 | TAG_ROTATED if self.rotated else TAG_ACT8
+        return d
+
 
 def alloc_act8(rows: int, K: int, device, rotated: bool = True) -> Act8:
     if K <= 0 or K % 32:
@@ -836,17 +846,15 @@ class MxFp4:
 
     __slots__ = ("_buf", "_rows", "_K", "_gpu", "_desc", "_at")
 
-    def __init__(self, rows: int, K: int, device, rotated: bool = True):
+    def __init__(self, rows: int, K: int, device, rotated: bool = True, *, buf: torch.Tensor | None = None):
         if K <= 0 or K % 32:
             raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
         nc = rows * (K // 2)  # a multiple of 16
-        self._bind(torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device),
-                   rows, K, rotated)
-
-    def _bind(self, buf: torch.Tensor, rows: int, K: int, rotated: bool) -> None:
+        if buf is None:
+            buf = torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
         self._buf, self._rows, self._K, self._gpu = buf, rows, K, buf.is_cuda
         ptr = buf.data_ptr()
-        self._desc = _Act4Desc(ptr, ptr + rows * (K // 2), rows, K, TAG_MXFP4 | TAG_ROTATED if rotated else TAG_MXFP4)
+        self._desc = _Act4Desc(ptr, ptr + nc, rows, K, TAG_MXFP4 | TAG_ROTATED if rotated else TAG_MXFP4)
         self._at = ctypes.addressof(self._desc)
 
     def __reduce__(self):  # copy, deepcopy and pickle: a descriptor of the copy's own buffer
@@ -879,6 +887,9 @@ class MxFp4:
     def desc(self) -> _Act4Desc:
         return _Act4Desc.from_buffer_copy(self._desc)
 
+    def _ref(self) -> _Act4Desc:
+        return self._desc
+
     @property
     def device(self) -> torch.device:
         return self._buf.device
@@ -901,9 +912,7 @@ class MxFp4:
 
 
 def _mxfp4_of(buf: torch.Tensor, rows: int, K: int, rotated: bool) -> MxFp4:
-    q = MxFp4.__new__(MxFp4)
-    q._bind(buf, rows, K, rotated)
-    return q
+    return MxFp4(rows, K, None, rotated, buf=buf)
 
 
 def alloc_mxfp4(rows: int, K: int, device, rotated: bool = True) -> MxFp4:
@@ -926,7 +935,10 @@ def mxfp4_rotate_quantize(x: torch.Tensor, rotate: bool = True, out: MxFp4 | Non
     """Rotate (H32 per 32-block along K) rows x [rows][K] (bf16 or fp32, CUDA) and round them to MXFP4."""
     ldx = _rows(x, "x")
     rows, K = x.shape
-    out = _made(stream, MxFp4, rows, K, x.device, rotate) if out is None else _fits(out, MxFp4, rows, K, x)
+    if out is None:
+        out = MxFp4(rows, K, x.device, rotate) if stream is None else _made(stream, MxFp4, rows, K, x.device, rotate)
+    else:
+        _fits(out, MxFp4, rows, K, x)
     _check(load_library().mxfp4_rotate_quantize(x.data_ptr(), _DTYPE[x.dtype], rows, K, ldx, rotate, out._at,
                                                 _stream(stream)))
     return out
@@ -948,28 +960,17 @@ def mxfp4_import(codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True
     return out
 
 
-def _held(q):
-    """The descriptor that a call reads, or stamps with q's own rows and K: the kept one where it says what the
-    fields do, else one built from the fields."""
-    if isinstance(q, MxFp4):
-        return q._desc
-    if isinstance(q, Act8):
-        d = q._kept
-        if d is not None and d.rows == q.rows and d.K == q.K:
-            d.tag = TAG_ACT8 | TAG_ROTATED if q.rotated else TAG_ACT8
-            return d
-    return q.desc()
-
-
 def _dequantize(call, kind, a, y, dtype, stream) -> torch.Tensor:
     device = a.device if isinstance(a, kind) else None
     if device is None or device.type != "cuda":
         raise ValueError(f"a must be an {kind.__name__} on the GPU")
     if y is None:
-        y, ldy = _made(stream, torch.empty, a.rows, a.K, dtype=dtype, device=device), a.K
+        M, ldy = a.rows, a.K
+        y = (torch.empty(M, ldy, dtype=dtype, device=device) if stream is None
+             else _made(stream, torch.empty, M, ldy, dtype=dtype, device=device))
     else:
         ldy, dtype = _rows(y, "y", (a.rows, a.K)), y.dtype
-    d = _held(a)
+    d = a._ref()
     _check(call(ctypes.addressof(d), y.data_ptr(), _DTYPE.get(dtype, -1), ldy, _stream(stream)))
     return y
 
@@ -1005,23 +1006,20 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     """
     if not (isinstance(w, MxFp4) and isinstance(a, MxFp4) and w._gpu and a._gpu):
         raise ValueError("w and a must be MxFp4 operands on the GPU")
+    M, N = a._rows, w._rows
     if y is None:
-        y, ldy = _made(stream, torch.empty, a.rows, w.rows, dtype=dtype, device=w.device), w.rows
+        ldy, device = N, w._buf.device
+        y = (torch.empty(M, N, dtype=dtype, device=device) if stream is None
+             else _made(stream, torch.empty, M, N, dtype=dtype, device=device))
     else:
-        ldy = _rows(y, "y", (a.rows, w.rows))
+        ldy = _rows(y, "y", (M, N))
     lib, st = load_library(), _stream(stream)
     if ws is True:  # batches of up to 128 tokens never use one
-        need = lib.mxfp4_gemm_workspace_bytes(a.rows, w.rows, w.K) if a.rows > 128 else 0
-        ws = gemm_workspace(a.rows, w.rows, w.K, y.device, st, need) if need else None
+        need = lib.mxfp4_gemm_workspace_bytes(M, N, w._K) if M > 128 else 0
+        ws = gemm_workspace(M, N, w._K, y.device, st, need) if need else None
     ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
     _check(lib.mxfp4_gemm(w._at, a._at, y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, ws_ptr, ws_bytes, st))
     return y
-
-
-def _tagged(out, rotate):
-    if not isinstance(out, MxFp4):  # the call stamped a descriptor built from the fields
-        out.rotated = bool(rotate)
-    return out
 
 
 def _rmsnorm(call, kind, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
@@ -1046,10 +1044,14 @@ def _rmsnorm(call, kind, alloc, x, g, residual, residual_out, eps, rotate, out, 
             raise ValueError("g must be a contiguous bf16 or fp32 tensor of K gains")
         gp, g_dtype = g.data_ptr(), _DTYPE[g.dtype]
     n = _RmsNorm(x.data_ptr(), r, r_out, gp, M, K, ldx, ldr, ldr_out, _DTYPE[x.dtype], r_dtype, g_dtype, int(rotate), eps)
-    out = _made(stream, alloc, M, K, x.device, rotate) if out is None else _fits(out, kind, M, K, x)
-    d = _held(out)
+    if out is None:
+        out = alloc(M, K, x.device, rotate) if stream is None else _made(stream, alloc, M, K, x.device, rotate)
+    else:
+        _fits(out, kind, M, K, x)
+    d = out._ref()
     _check(call(ctypes.addressof(n), ctypes.addressof(d), _stream(stream)))
-    return _tagged(out, rotate)
+    out.rotated = bool(rotate)
+    return out
 
 
 def w4a4_rmsnorm_quantize_act(x: torch.Tensor, g: torch.Tensor | None = None, eps: float = 1e-6,
@@ -1082,11 +1084,15 @@ def _swiglu(call, kind, alloc, gate, up, rotate, out, stream):
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     M, K = gate.shape
-    out = _made(stream, alloc, M, K, gate.device, rotate) if out is None else _fits(out, kind, M, K, gate)
-    d = _held(out)
+    if out is None:
+        out = alloc(M, K, gate.device, rotate) if stream is None else _made(stream, alloc, M, K, gate.device, rotate)
+    else:
+        _fits(out, kind, M, K, gate)
+    d = out._ref()
     _check(call(gate.data_ptr(), up.data_ptr(), _DTYPE[gate.dtype], M, K, ldg, ldu, rotate, ctypes.addressof(d),
                 _stream(stream)))
-    return _tagged(out, rotate)
+    out.rotated = bool(rotate)
+    return out
 
 
 def w4a4_swiglu_quantize_act(gate: torch.Tensor, up: torch.Tensor, rotate: bool = True, out: Act4 | None = None,
