@@ -8,10 +8,13 @@
 //
 // Bounds and measurements (GB300, CUDA graphs, inputs larger than L2 in rotation; a plain
 // copy reaches 6.8 TB/s).  Between the memory and the issue of instructions (rotation and
-// rounding; ncu: 60-76% of issue slots): M1024 K17408 fp32 rows to MXFP4 14.4 us (5.6
-// TB/s), SwiGLU of bf16 to int8 18.5 us (5.0), its reading back as bf16 9.8 us (5.7), norm
-// of M16384 K5120 bf16 to int8 116 us (5.2), one row 2.5 us.  Two chunks a thread: one
-// loses 13% on bf16 rows, four lose 7% on fp32.
+// rounding; ncu: 60-76% of issue slots).  M1024 K17408, fp32 inputs near the memory: rows to
+// MXFP4 14.0 us (5.8 TB/s), SwiGLU to int8 25.2 (6.5), MXFP4 read back as fp32 13.9 (5.8);
+// bf16 inputs, twice the instructions a byte, by their issue: rows to MXFP4 11.9 (3.8),
+// SwiGLU to int8 17.9 (5.1), MXFP4 read back as bf16 9.8 (4.6).  Norm of bf16 to int8:
+// M16384 K5120 115 us (5.2), M4096 K2048 13.7 (4.4), M16384 K768 19.5 (4.6), one row 2.2;
+// M1024 K17408 72 (1.8: see rmsnorm_quantize_kernel).  Two chunks a thread: one loses 13% on
+// bf16 rows, four lose 7% on fp32.
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -114,9 +117,13 @@ __global__ void __launch_bounds__(kThreads) rows_quantize_kernel(const T* __rest
 struct NoResidual {};
 
 // T threads share a row (T a power of two up to 32, several rows a CTA; or a multiple
-// of 32, one row a CTA) and hold C chunks each, in registers from the load to the
-// store: h = x + r is summed in fp32, squared and summed over the row in a fixed
-// order, and y = h * rsqrt(mean + eps) * g goes on to the rotation and the codes.
+// of 32, one row a CTA) and hold C chunks each from the load to the store: h = x + r is
+// summed in fp32, squared and summed over the row in a fixed order, and y = h *
+// rsqrt(mean + eps) * g goes on to the rotation and the codes.
+// Up to four chunks stay in registers, but for 16-48 bytes of some MXFP4 instances.  Eight,
+// 64 of the 64 registers that 1024 threads leave each, do not: 0.4-1.5 KB a thread goes
+// through local memory, on rows of K above 16384 where there are more rows than SMs, and
+// on all of K above 32768 (M1024 bf16 to int8: K16384 33 us, K17408 72 us).
 template <int FMT, typename TX, typename TR, int C>
 __global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const TX* __restrict__ x, const TR* r, TR* r_out,
                                                                 const void* __restrict__ g, int g_bf16, int64_t M, int cpr,

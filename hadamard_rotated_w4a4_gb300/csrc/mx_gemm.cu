@@ -22,12 +22,14 @@
 //     (32 bytes a cycle and SM at most) overlap the next tile's MMAs.  With a workspace
 //     the last waves' K work is cut evenly over the pairs (stream-K).
 //
-// Bounds and measurements (GB300, CUDA graphs).  Pair: a stage of a 256 x 256 tile is 512
-// cycles of MMA and 530 of shared memory; 574 are measured, and about 1,800 between two
-// tiles.  M4096 K5120 N17408 bf16 101 us (7.2 PFLOP/s; 111 us sustained, under the power
-// cap), M1024 K17408 N5120 30.4 us (6.0).  Small: bound by the weights' stream where K x N
-// is large (K69632 N5120, one token: 6.1 TB/s), else by set-up and round trips: one token
-// K5120 N5120 4.3 us, 64 tokens 6.7, 256 tokens 8.1.
+// Bounds and measurements (GB300, CUDA graphs).  Pair: a stage of a 256 x 256 tile takes 574
+// cycles and is 530 of shared memory by its bytes; about 1,800 pass between two tiles.  The
+// MMAs alone were not timed (at the nominal 13.5 PFLOP/s a stage is 391 cycles).  M4096
+// K5120 N17408 bf16 101 us in a burst on one set of operands (7.2 PFLOP/s), 107 on three in
+// turn, 111 sustained, under the power cap; M1024 K17408 N5120 31 us (5.8).  Small: bound by
+// the weights' stream where K x N is large (K69632 N5120, one token: 6.1 TB/s), else by
+// set-up and round trips.  K5120 N5120, weights from memory: one token 5.0 us, 64 tokens
+// 7.8, 256 tokens 8.6; weights in L2: one token 4.1.
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"

@@ -21,7 +21,8 @@ struct Chunk;
 template <>
 struct Chunk<float> {
   float v[8];
-  // kLast: nothing reads the values again, so L2 may drop them first
+  // kLast: this kernel does not read the values again, and L2 may drop them before its
+  // codes.  Another reader of the same rows then finds fewer of them there.
   template <bool kLast = false>
   __device__ __forceinline__ void load(const float* p, bool wide) {
     if (wide && kLast) {
