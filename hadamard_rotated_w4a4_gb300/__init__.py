@@ -850,8 +850,11 @@ class MxFp4:
         if K <= 0 or K % 32:
             raise W4A4Error(1, f"K={K} must be a positive multiple of 32")
         nc = rows * (K // 2)  # a multiple of 16
+        size = nc + (rows + 127) // 128 * ((K + 127) // 128) * 512
         if buf is None:
-            buf = torch.empty(nc + (rows + 127) // 128 * ((K + 127) // 128) * 512, dtype=torch.uint8, device=device)
+            buf = torch.empty(size, dtype=torch.uint8, device=device)
+        elif buf.dtype != torch.uint8 or buf.shape != (size,) or not buf.is_contiguous():
+            raise ValueError(f"buf must be {size} contiguous bytes")
         self._buf, self._rows, self._K, self._gpu = buf, rows, K, buf.is_cuda
         ptr = buf.data_ptr()
         self._desc = _Act4Desc(ptr, ptr + nc, rows, K, TAG_MXFP4 | TAG_ROTATED if rotated else TAG_MXFP4)

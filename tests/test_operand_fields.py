@@ -131,6 +131,14 @@ def test_mxfp4_shape_is_fixed():
     assert q.desc().scales == q.scales_buf.data_ptr()
 
 
+def test_mxfp4_takes_no_buffer_of_another_size():
+    buf = w4.alloc_mxfp4(130, 160, "cpu").buf
+    assert w4.MxFp4(130, 160, "cpu", buf=buf).buf is buf
+    for other in (buf[:-16], buf.view(torch.int8), torch.zeros(2 * len(buf), dtype=torch.uint8)[::2], buf.view(2, -1)):
+        with pytest.raises(ValueError):
+            w4.MxFp4(130, 160, "cpu", buf=other)
+
+
 # ----------------------------------------------------------------- the same on the GPU
 @pytest.fixture(scope="module")
 def dev():
