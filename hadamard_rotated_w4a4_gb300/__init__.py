@@ -23,6 +23,10 @@ Entry points (same names as the C ABI in ``include/w4a4.h``):
   front of the quantiser
 * ``w4a4_/w4a8_swiglu_quantize_act``, ``mxfp4_swiglu_quantize``: SwiGLU in front of it
 * ``mxfp4_dequantize``, ``w4a4_/w4a8_dequantize_act``: the values that codes stand for
+* ``mxfp4_gemm_epilogue(w, a, bias, activation, residual)``: the product with its epilogue
+* ``kv8_append(cache, k, v, table, lens, ...)``: rotary positions, H32 and int8 into a
+  :class:`KvCache8`, the paged keys and values; ``kv8_read``: the values of its codes
+* ``kv8_attention(q, cache, table, lens, ...)``: attention over those pages
 """
 from __future__ import annotations
 
@@ -45,6 +49,8 @@ __all__ = [
     "mxfp4_gemm_workspace_bytes", "w4a4_dequantize_act", "w4a8_dequantize_act",
     "w4a4_rmsnorm_quantize_act", "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize",
     "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize",
+    "mxfp4_gemm_epilogue", "KvCache8", "alloc_kv8", "rope_freqs", "kv8_append", "kv8_read", "kv8_attention",
+    "kv8_attention_workspace_bytes",
 ]
 
 STATUS = {
@@ -57,6 +63,7 @@ TAG_ACT4 = 0x41340000
 TAG_ACT8 = 0x41380000
 TAG_ACT16 = 0x41420000
 TAG_MXFP4 = 0x4D340000
+TAG_KV8 = 0x4B380000
 TAG_ROTATED = 0x1
 
 #: every symbol include/w4a4.h declares
@@ -72,7 +79,8 @@ EXPORTS = [
     "w4a4_mxfp4_codes_bytes", "w4a4_mxfp4_scales_bytes", "mxfp4_rotate_quantize", "mxfp4_import", "mxfp4_dequantize",
     "w4a4_dequantize_act", "w4a8_dequantize_act", "mxfp4_gemm", "mxfp4_gemm_workspace_bytes", "w4a4_rmsnorm_quantize_act",
     "w4a8_rmsnorm_quantize_act", "mxfp4_rmsnorm_quantize", "w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act",
-    "mxfp4_swiglu_quantize",
+    "mxfp4_swiglu_quantize", "mxfp4_gemm_epilogue", "kv8_append", "kv8_read", "kv8_attention",
+    "kv8_attention_workspace_bytes",
 ]
 
 
@@ -104,6 +112,34 @@ class _RmsNorm(ctypes.Structure):
                 ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
                 ("ldr_out", ctypes.c_int64), ("x_dtype", ctypes.c_int), ("r_dtype", ctypes.c_int),
                 ("g_dtype", ctypes.c_int), ("rotate", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("residual_dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class _Kv8Desc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int), ("page", ctypes.c_int), ("dim", ctypes.c_int), ("tag", ctypes.c_uint32)]
+
+
+class _Kv8Seqs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("width", ctypes.c_int64), ("ldt", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
+class _Kv8New(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("freqs", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in (
+                    "ldk", "ldkh", "ldv", "ldvh", "ldq", "ldqh", "ldo", "ldoh")] + [(n, ctypes.c_int) for n in (
+                        "q_heads", "nf", "interleaved", "x_dtype", "o_dtype")]
+
+
+class _Kv8Attn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("ldqh", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("ldoh", ctypes.c_int64), ("q_heads", ctypes.c_int), ("q_dtype", ctypes.c_int),
+                ("o_dtype", ctypes.c_int), ("causal", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _LIB = None
@@ -165,6 +201,11 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         getattr(lib, name).argtypes = [vp, vp, vp]
     for name in ("w4a4_swiglu_quantize_act", "w4a8_swiglu_quantize_act", "mxfp4_swiglu_quantize"):
         getattr(lib, name).argtypes = [vp, vp, i32, i64, i64, i64, i64, i32, vp, vp]
+    lib.mxfp4_gemm_epilogue.argtypes = [vp, vp, vp, vp, i32, i64, vp, u, vp]
+    lib.kv8_append.argtypes = [vp, vp, vp, vp]
+    lib.kv8_read.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    lib.kv8_attention.argtypes = [vp, vp, vp, vp, u, vp]
+    lib.kv8_attention_workspace_bytes.argtypes, lib.kv8_attention_workspace_bytes.restype = [i32], u
     lib.w4a4_check.argtypes = [vp]
     lib.w4a4_debug_set_wait_limit.argtypes = [ctypes.c_uint64, ctypes.c_uint64]
     lib.w4a4_debug_set_wait_limit.restype = None
@@ -1025,6 +1066,53 @@ def mxfp4_gemm(w: MxFp4, a: MxFp4, y: torch.Tensor | None = None, dtype: torch.d
     return y
 
 
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def mxfp4_gemm_epilogue(w: MxFp4, a: MxFp4, bias: torch.Tensor | None = None, activation: str | None = None,
+                        residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                        dtype: torch.dtype = torch.float32, ws: torch.Tensor | None | bool = True, stream=None) -> torch.Tensor:
+    """act(the product + bias) + residual, in the product's epilogue (fp32 or bf16 [M][N], rounded once).
+
+    bias: fp32 [N]; activation: None, "relu", "silu", "gelu" or "gelu_tanh"; residual: bf16 or fp32 [M][N], which may
+    be y itself; y, dtype, ws as for mxfp4_gemm.
+    """
+    if not (isinstance(w, MxFp4) and isinstance(a, MxFp4) and w._gpu and a._gpu):
+        raise ValueError("w and a must be MxFp4 operands on the GPU")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None")
+    M, N = a._rows, w._rows
+    device = w._buf.device
+    b = r = None
+    ldr = r_dtype = 0
+    if bias is not None:
+        if not bias.is_cuda or bias.dtype != torch.float32 or bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
+            _cuda(bias, "bias")
+            raise ValueError("bias must be a contiguous fp32 tensor of N values")
+        b = bias.data_ptr()
+    if residual is not None:
+        ldr = _rows(residual, "residual", (M, N))
+        r, r_dtype = residual.data_ptr(), _DTYPE[residual.dtype]
+    for t, name in ((a._buf, "a"), (bias, "bias"), (residual, "residual"), (y, "y")):
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, w on {device}")
+    if y is None:
+        ldy = N
+        y = (torch.empty(M, N, dtype=dtype, device=device) if stream is None
+             else _made(stream, torch.empty, M, N, dtype=dtype, device=device))
+    else:
+        ldy = _rows(y, "y", (M, N))
+    e = _Epilogue(b, r, ldr, r_dtype, ACTIVATIONS[activation])
+    lib, st = load_library(), _stream(stream)
+    if ws is True:  # batches of up to 128 tokens never use one
+        need = lib.mxfp4_gemm_workspace_bytes(M, N, w._K) if M > 128 else 0
+        ws = gemm_workspace(M, N, w._K, y.device, st, need) if need else None
+    ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(lib.mxfp4_gemm_epilogue(w._at, a._at, ctypes.addressof(e), y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, ws_ptr,
+                                   ws_bytes, st))
+    return y
+
+
 def _rmsnorm(call, kind, alloc, x, g, residual, residual_out, eps, rotate, out, stream):
     ldx = _rows(x, "x")
     M, K = shape = x.shape
@@ -1114,3 +1202,209 @@ def mxfp4_swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, rotate: bool = T
                           stream=None) -> MxFp4:
     """As w4a4_swiglu_quantize_act, to MXFP4."""
     return _swiglu(load_library().mxfp4_swiglu_quantize, MxFp4, MxFp4, gate, up, rotate, out, stream)
+
+
+# ---------------------------------------------------------------- the 8-bit paged keys and values
+class KvCache8:
+    """Keys and values in 8 bits, in pages: codes int8 [pages][heads][2][page][dim] (of each page and head the keys,
+    then the values), scale bytes uint8 [pages][heads][2][page / 16]: 16 tokens share the power of two 2^(s - 127).
+
+    KvCache8(codes, scales, rotated) wraps two contiguous buffers (alloc_kv8 makes them); both are fixed, and the C
+    descriptor is kept.  rotated: keys and values carry the H32 rotation.
+    """
+
+    __slots__ = ("_codes", "_scales", "_rotated", "_desc", "_at", "_index")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True):
+        if codes.dtype != torch.int8 or codes.dim() != 5 or codes.shape[2] != 2 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous int8 tensor [pages][heads][2][page][dim]")
+        pages, heads, _, page, dim = codes.shape
+        if page not in (16, 32, 64, 128):
+            raise W4A4Error(1, f"page={page} must be 16, 32, 64 or 128")
+        if dim not in (64, 128, 256):
+            raise W4A4Error(4, f"dim={dim} must be 64, 128 or 256")
+        if scales.dtype != torch.uint8 or scales.shape != (pages, heads, 2, page // 16) or not scales.is_contiguous():
+            raise ValueError("scales must be a contiguous uint8 tensor [pages][heads][2][page / 16]")
+        if scales.device != codes.device:
+            raise ValueError(f"scales are on {scales.device}, codes on {codes.device}")
+        self._codes, self._scales, self._rotated = codes, scales, bool(rotated)
+        self._index = codes.get_device()
+        self._desc = _Kv8Desc(codes.data_ptr(), scales.data_ptr(), pages, heads, page, dim,
+                              TAG_KV8 | TAG_ROTATED if rotated else TAG_KV8)
+        self._at = ctypes.addressof(self._desc)
+
+    def __reduce__(self):  # copy, deepcopy and pickle: a descriptor of the copy's own buffers
+        return KvCache8, (self._codes, self._scales, self._rotated)
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
+
+    @property
+    def rotated(self) -> bool:
+        return self._rotated
+
+    @property
+    def pages(self) -> int:
+        return self._desc.pages
+
+    @property
+    def heads(self) -> int:
+        return self._desc.heads
+
+    @property
+    def page(self) -> int:
+        return self._desc.page
+
+    @property
+    def dim(self) -> int:
+        return self._desc.dim
+
+    @property
+    def tag(self) -> int:
+        return self._desc.tag
+
+    @property
+    def device(self) -> torch.device:
+        return self._codes.device
+
+    def desc(self) -> _Kv8Desc:
+        return _Kv8Desc.from_buffer_copy(self._desc)
+
+
+def alloc_kv8(pages: int, heads: int, dim: int, page: int = 64, device="cuda", rotated: bool = True) -> KvCache8:
+    """An empty cache (codes zero): `pages` pages of `page` tokens, 2 * page * (dim + 1 / 16) bytes a head each."""
+    codes = torch.zeros(pages, heads, 2, page, dim, dtype=torch.int8, device=device)
+    return KvCache8(codes, torch.zeros(pages, heads, 2, page // 16, dtype=torch.uint8, device=device), rotated)
+
+
+def rope_freqs(dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Radians a position of the dim / 2 pairs, base^(-2 i / dim), in 64 bits: the freqs of kv8_append."""
+    return base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+
+
+def _kv8_seqs(cache, table, lens, cu, tokens: int) -> _Kv8Seqs:
+    if not isinstance(cache, KvCache8):
+        raise ValueError(f"cache must be KvCache8, not {type(cache).__name__}")
+    at = cache._index
+    if at < 0:
+        raise ValueError("the cache must be on the GPU (there is no CPU path)")
+    if at != torch.cuda.current_device():
+        raise ValueError(f"the cache is on cuda:{at}, the current device is cuda:{torch.cuda.current_device()}")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.get_device() != at or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be a 2-D int32 tensor with unit stride along its rows, on the cache's device")
+    batch, width = table.shape
+    if lens.dtype != torch.int32 or lens.shape != (batch,) or lens.get_device() != at or (batch > 1 and lens.stride(0) != 1):
+        raise ValueError("lens must be a contiguous int32 tensor of one length per row of table, on the cache's device")
+    if cu is not None and (cu.dtype != torch.int32 or cu.shape != (batch + 1,) or cu.get_device() != at or (batch and cu.stride(0) != 1)):
+        raise ValueError("cu must be a contiguous int32 tensor of batch + 1 offsets, on the cache's device")
+    return _Kv8Seqs(table.data_ptr(), lens.data_ptr(), None if cu is None else cu.data_ptr(), batch, width,
+                    table.stride(0) if batch > 1 else width, tokens)
+
+
+def _heads(t: torch.Tensor, name: str, cache: KvCache8, heads: int, tokens: int | None = None, dtype=None):
+    """Checks [tokens][heads][dim] rows (bf16 or fp32, unit stride along dim); strides of tokens and of heads."""
+    if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache._desc.dim or (tokens is not None and t.shape[0] != tokens)
+            or t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype) or t.stride(2) != 1 or t.get_device() != cache._index):
+        _cuda(t, name)
+        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}][{heads}][{cache.dim}] "
+                         f"{dtype or 'bf16 or fp32'} with unit stride along dim, on the cache's device")
+    return t.stride(0), t.stride(1)
+
+
+def kv8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+               cu: torch.Tensor | None = None, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+               freqs: torch.Tensor | None = None, interleaved: bool = False, stream=None) -> torch.Tensor | None:
+    """Write new keys and values k, v [tokens][heads][dim] (bf16 or fp32) into the pages, with their positions on the way.
+
+    table int32 [batch][width]: the pages of each sequence; lens int32 [batch]: its tokens, the new ones included;
+    cu int32 [batch + 1]: the offsets of its new tokens in k and v (None: as many for each).  All are read on the GPU.
+    freqs (rope_freqs; fp64): pair i of k, and of q, turns by position * freqs[i]; pairs (i, i + n), or with
+    interleaved (2i, 2i + 1).  q [tokens][q_heads][dim] is rotated into q_out (None: in place), which is returned.
+    A page, length or offset out of range is skipped, and reported by w4a4_check.
+    """
+    T = k.shape[0]
+    s = _kv8_seqs(cache, table, lens, cu, T)
+    H = cache._desc.heads
+    ldk, ldkh = _heads(k, "k", cache, H)
+    ldv, ldvh = _heads(v, "v", cache, H, T, k.dtype)
+    qp = op = fp = None
+    ldq = ldqh = ldo = ldoh = q_heads = nf = o_dtype = 0
+    if q is not None:
+        q_heads = q.shape[1]
+        ldq, ldqh = _heads(q, "q", cache, q_heads, T, k.dtype)
+        if q_out is None:
+            q_out = q
+        ldo, ldoh = _heads(q_out, "q_out", cache, q_heads, T)
+        qp, op, o_dtype = q.data_ptr(), q_out.data_ptr(), _DTYPE[q_out.dtype]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if freqs is not None:
+        if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.get_device() != cache._index or not freqs.is_contiguous():
+            raise ValueError("freqs must be a contiguous 1-D fp64 tensor on the cache's device")
+        fp, nf = freqs.data_ptr(), freqs.shape[0]
+    n = _Kv8New(k.data_ptr(), v.data_ptr(), qp, op, fp, ldk, ldkh, ldv, ldvh, ldq, ldqh, ldo, ldoh, q_heads, nf,
+                interleaved, _DTYPE[k.dtype], o_dtype)
+    _check(load_library().kv8_append(cache._at, ctypes.addressof(s), ctypes.addressof(n), _stream(stream)))
+    return q_out
+
+
+def kv8_read(cache: KvCache8, table: torch.Tensor, lens: torch.Tensor, tokens: int, cu: torch.Tensor | None = None,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+             stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The values (k, v) [tokens][heads][dim] of each sequence's last tokens, as kv8_append takes them (a rotation by
+    H32 is not undone); rows past cu[-1] are left as they are."""
+    s = _kv8_seqs(cache, table, lens, cu, tokens)
+    H, D = cache._desc.heads, cache._desc.dim
+    made = []
+    for t in (k, v):
+        if t is None:
+            t = (torch.empty(tokens, H, D, dtype=dtype, device=cache.device) if stream is None
+                 else _made(stream, torch.empty, tokens, H, D, dtype=dtype, device=cache.device))
+        made.append(t)
+    k, v = made
+    ldk, ldkh = _heads(k, "k", cache, H, tokens)
+    ldv, ldvh = _heads(v, "v", cache, H, tokens, k.dtype)
+    _check(load_library().kv8_read(cache._at, ctypes.addressof(s), k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], ldk, ldkh,
+                                   ldv, ldvh, _stream(stream)))
+    return k, v
+
+
+def kv8_attention_workspace_bytes(dim: int) -> int:
+    return int(load_library().kv8_attention_workspace_bytes(dim))
+
+
+def kv8_attention(q: torch.Tensor, cache: KvCache8, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor | None = None,
+                  scale: float | None = None, causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                  dtype: torch.dtype = torch.bfloat16, ws: torch.Tensor | None | bool = True, stream=None) -> torch.Tensor:
+    """softmax(scale q K^T) V of the last tokens of each sequence over its pages: q, out [tokens][q_heads][dim].
+
+    table, lens, cu as for kv8_append, after which it is called with the same three.  scale: None = dim^-1/2.
+    causal: a token sees itself and what is before it, with window > 0 the last `window` of that; not causal: the
+    whole sequence.  A token that sees nothing gets zeros.  q is not rotated by H32, whatever the cache is.
+    ws: True = the cached per-stream workspace (in a capture one of the graph's own), a tensor = that workspace (its
+    first MiB zero before its first use), None/False = a sequence is not cut over the SMs.
+    """
+    T, Hq = q.shape[0], q.shape[1]
+    s = _kv8_seqs(cache, table, lens, cu, T)
+    ldq, ldqh = _heads(q, "q", cache, Hq)
+    if out is None:
+        out = (torch.empty(T, Hq, cache._desc.dim, dtype=dtype, device=q.device) if stream is None
+               else _made(stream, torch.empty, T, Hq, cache._desc.dim, dtype=dtype, device=q.device))
+    ldo, ldoh = _heads(out, "out", cache, Hq, T)
+    D = cache._desc.dim
+    a = _Kv8Attn(q.data_ptr(), out.data_ptr(), ldq, ldqh, ldo, ldoh, Hq, _DTYPE[q.dtype], _DTYPE[out.dtype], causal, window,
+                 D ** -0.5 if scale is None else scale)
+    lib, st = load_library(), _stream(stream)
+    if ws is True:
+        need = lib.kv8_attention_workspace_bytes(D)
+        # two graphs of one stream may be replayed side by side: each has its own
+        ws = (_made(st, _graph_workspace, need, q.device) if _capturing(stream)
+              else gemm_workspace(0, 0, 0, q.device, st, need))
+    ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(lib.kv8_attention(cache._at, ctypes.addressof(s), ctypes.addressof(a), ws_ptr, ws_bytes, st))
+    return out

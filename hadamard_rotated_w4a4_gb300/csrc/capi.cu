@@ -141,6 +141,84 @@ w4a4_status check_rows(const void* x, int dtype, int64_t M, int64_t K, int64_t l
   return W4A4_OK;
 }
 
+bool kv8_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
+
+// A cache and the sequences of a call, in the kernels' form.
+w4a4_status open_kv8(const w4a4_kv8* c, const w4a4_kv8_seqs* q, w4a4::KvCache* oc, w4a4::KvSeqs* oq, const char* fn) {
+  if (!c || !q) return fail(W4A4_ERR_INVALID_ARG, "%s: the cache's or the sequences' descriptor is NULL", fn);
+  if ((c->tag & W4A4_TAG_MAGIC_MASK) != W4A4_TAG_KV8)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: descriptor tag 0x%08x is not a KV8 tag", fn, c->tag);
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: page=%d must be 16, 32, 64 or 128", fn, c->page);
+  if (!kv8_dim(c->dim)) return fail(W4A4_ERR_UNSUPPORTED, "%s: dim=%d must be 64, 128 or 256", fn, c->dim);
+  if (c->heads <= 0 || c->heads > 65535 || c->pages < 0 || c->pages >= (int64_t(1) << 31))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: heads=%d or pages=%lld out of range", fn, c->heads, (long long)c->pages);
+  const int64_t most = (int64_t(1) << 31) - 256;
+  if (q->batch < 0 || q->batch > most || q->tokens < 0 || q->tokens > most || q->width < 0 || q->width * c->page > most || q->width > most)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: batch, tokens or width out of range", fn);
+  if (q->ldt < q->width) return fail(W4A4_ERR_INVALID_ARG, "%s: table row stride %lld < width=%lld", fn, (long long)q->ldt, (long long)q->width);
+  if (!q->cu && (q->batch == 0 ? q->tokens != 0 : q->tokens % q->batch != 0))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: %lld tokens are not the same number for each of %lld sequences, and cu is NULL", fn,
+                (long long)q->tokens, (long long)q->batch);
+  if (q->batch == 0 && q->tokens > 0) return fail(W4A4_ERR_INVALID_ARG, "%s: tokens without a sequence", fn);
+  if (q->tokens > 0 && (!q->lens || (!q->table && q->width > 0) || (c->pages > 0 && (!c->codes || !c->scales))))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: table, lens, codes or scales is NULL", fn);
+  if (((reinterpret_cast<uintptr_t>(q->table) | reinterpret_cast<uintptr_t>(q->lens) | reinterpret_cast<uintptr_t>(q->cu)) & 3) != 0)
+    return fail(W4A4_ERR_ALIGNMENT, "%s: table, lens and cu must be 4-byte aligned", fn);
+  if (!aligned16(c->codes)) return fail(W4A4_ERR_ALIGNMENT, "%s: the cache's codes must be 16-byte aligned", fn);
+  *oc = w4a4::KvCache{c->codes, c->scales, static_cast<int>(c->pages), c->heads, c->page, c->dim, (c->tag & W4A4_TAG_ROTATED) ? 1 : 0};
+  *oq = w4a4::KvSeqs{q->table, q->lens, q->cu, q->ldt, static_cast<int>(q->batch), static_cast<int>(q->width),
+                     static_cast<int>(q->tokens), q->batch > 0 ? static_cast<int>(q->tokens / q->batch) : 0};
+  return ok();
+}
+
+// [tokens][heads][dim] rows: type, pointer, strides.
+w4a4_status check_heads(const void* x, int dtype, int64_t tokens, int64_t heads, int64_t dim, int64_t ld, int64_t ldh,
+                        const char* what, const char* fn) {
+  if (dtype != W4A4_DTYPE_BF16 && dtype != W4A4_DTYPE_F32)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: %s dtype %d is neither bf16 (0) nor f32 (1)", fn, what, dtype);
+  if (tokens > 0 && !x) return fail(W4A4_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
+  if ((heads > 1 && ldh < dim) || (tokens > 1 && ld < dim))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: %s strides %lld (tokens), %lld (heads) are below dim=%lld", fn, what, (long long)ld, (long long)ldh,
+                (long long)dim);
+  const int64_t size = dtype == W4A4_DTYPE_BF16 ? 2 : 4;
+  if (!aligned16(x) || (tokens > 1 && ld * size % 16 != 0) || (heads > 1 && ldh * size % 16 != 0))
+    return fail(W4A4_ERR_ALIGNMENT, "%s: %s and its rows must be 16-byte aligned", fn, what);
+  return W4A4_OK;
+}
+
+// The MXFP4 product, with an epilogue or (null) without.
+w4a4_status mx_product(const char* fn, const w4a4_mxfp4* w, const w4a4_mxfp4* a, const w4a4::MxEpilogue* ep, void* y, int y_dtype,
+                       int64_t ldy, void* ws, size_t ws_bytes, w4a4_stream_t stream) {
+  w4a4_status s = check_mx(w, fn);
+  if (s != W4A4_OK) return s;
+  if ((s = check_mx(a, fn)) != W4A4_OK) return s;
+  if (w->K != a->K)
+    return fail(W4A4_ERR_MISMATCH, "%s: weights have K=%lld, activations K=%lld", fn, (long long)w->K, (long long)a->K);
+  if ((w->tag & W4A4_TAG_ROTATED) != (a->tag & W4A4_TAG_ROTATED))
+    return fail(W4A4_ERR_MISMATCH, "%s: one operand is H32-rotated, the other is not; refusing a product that would be "
+                "silently wrong", fn);
+  const int64_t M = a->rows, N = w->rows;
+  if (y_dtype != W4A4_DTYPE_BF16 && y_dtype != W4A4_DTYPE_F32)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: y dtype %d is neither bf16 (0) nor f32 (1)", fn, y_dtype);
+  if (ldy < N) return fail(W4A4_ERR_INVALID_ARG, "%s: ldy=%lld < N=%lld", fn, (long long)ldy, (long long)N);
+  if (M == 0 || N == 0) return ok();
+  if (!y) return fail(W4A4_ERR_INVALID_ARG, "%s: y is NULL", fn);
+  if ((reinterpret_cast<uintptr_t>(y) & (y_dtype == W4A4_DTYPE_BF16 ? 1u : 3u)) != 0)
+    return fail(W4A4_ERR_ALIGNMENT, "%s: y must be aligned to its element", fn);
+  if (N > w4a4::kMxMaxRows || M > w4a4::kMxMaxRows)
+    return fail(W4A4_ERR_UNSUPPORTED, "%s: at most %lld rows an operand", fn, (long long)w4a4::kMxMaxRows);
+  if (ws) {
+    const size_t need = w4a4::mx_gemm_workspace_bytes(M, N, a->K);
+    if (ws_bytes < need)
+      return fail(W4A4_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
+    if (!aligned16(ws)) return fail(W4A4_ERR_ALIGNMENT, "%s: ws must be 16-byte aligned", fn);
+  }
+  return cuda_status(w4a4::launch_mx_gemm(w->codes, w->scales, N, a->codes, a->scales, M, a->K, y,
+                                          y_dtype == W4A4_DTYPE_BF16, ldy, ws, ep, reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
 // The output descriptor of a fused quantiser: pointers, then rows, K and tag.
 w4a4_status open_out(void* codes, void* scales, void* expanded, int64_t M, int64_t K, int rotate, const char* fn) {
   w4a4_status s = check_k_rows(M, K, fn);
@@ -650,34 +728,28 @@ size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_dtype, int64_t ldy, void* ws,
                        size_t ws_bytes, w4a4_stream_t stream) {
-  const char* fn = "mxfp4_gemm";
-  w4a4_status s = check_mx(w, fn);
-  if (s != W4A4_OK) return s;
-  if ((s = check_mx(a, fn)) != W4A4_OK) return s;
-  if (w->K != a->K)
-    return fail(W4A4_ERR_MISMATCH, "%s: weights have K=%lld, activations K=%lld", fn, (long long)w->K, (long long)a->K);
-  if ((w->tag & W4A4_TAG_ROTATED) != (a->tag & W4A4_TAG_ROTATED))
-    return fail(W4A4_ERR_MISMATCH, "%s: one operand is H32-rotated, the other is not; refusing a product that would be "
-                "silently wrong", fn);
-  const int64_t M = a->rows, N = w->rows;
-  if (y_dtype != W4A4_DTYPE_BF16 && y_dtype != W4A4_DTYPE_F32)
-    return fail(W4A4_ERR_INVALID_ARG, "%s: y dtype %d is neither bf16 (0) nor f32 (1)", fn, y_dtype);
-  if (ldy < N) return fail(W4A4_ERR_INVALID_ARG, "%s: ldy=%lld < N=%lld", fn, (long long)ldy, (long long)N);
-  if (M == 0 || N == 0) return ok();
-  if (!y) return fail(W4A4_ERR_INVALID_ARG, "%s: y is NULL", fn);
-  if ((reinterpret_cast<uintptr_t>(y) & (y_dtype == W4A4_DTYPE_BF16 ? 1u : 3u)) != 0)
-    return fail(W4A4_ERR_ALIGNMENT, "%s: y must be aligned to its element", fn);
-  if (N > w4a4::kMxMaxRows || M > w4a4::kMxMaxRows)
-    return fail(W4A4_ERR_UNSUPPORTED, "%s: at most %lld rows an operand", fn, (long long)w4a4::kMxMaxRows);
-  if (ws) {
-    const size_t need = w4a4::mx_gemm_workspace_bytes(M, N, a->K);
-    if (ws_bytes < need)
-      return fail(W4A4_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, ws_bytes, need);
-    if (!aligned16(ws)) return fail(W4A4_ERR_ALIGNMENT, "%s: ws must be 16-byte aligned", fn);
+  return mx_product("mxfp4_gemm", w, a, nullptr, y, y_dtype, ldy, ws, ws_bytes, stream);
+}
+
+w4a4_status mxfp4_gemm_epilogue(const w4a4_mxfp4* w, const w4a4_mxfp4* a, const w4a4_epilogue* e, void* y, int y_dtype,
+                                int64_t ldy, void* ws, size_t ws_bytes, w4a4_stream_t stream) {
+  const char* fn = "mxfp4_gemm_epilogue";
+  if (!e) return fail(W4A4_ERR_INVALID_ARG, "%s: the epilogue is NULL", fn);
+  if (e->act < W4A4_ACT_NONE || e->act > W4A4_ACT_GELU_TANH) return fail(W4A4_ERR_INVALID_ARG, "%s: unknown activation %d", fn, e->act);
+  if ((reinterpret_cast<uintptr_t>(e->bias) & 3) != 0) return fail(W4A4_ERR_ALIGNMENT, "%s: bias must be aligned to its element", fn);
+  const bool bf16 = e->residual_dtype == W4A4_DTYPE_BF16;
+  if (e->residual) {
+    if (!bf16 && e->residual_dtype != W4A4_DTYPE_F32)
+      return fail(W4A4_ERR_INVALID_ARG, "%s: residual dtype %d is neither bf16 (0) nor f32 (1)", fn, e->residual_dtype);
+    if ((reinterpret_cast<uintptr_t>(e->residual) & (bf16 ? 1u : 3u)) != 0)
+      return fail(W4A4_ERR_ALIGNMENT, "%s: residual must be aligned to its element", fn);
+    if (w && a && a->rows > 1 && e->ldr < w->rows)
+      return fail(W4A4_ERR_INVALID_ARG, "%s: ldr=%lld < N=%lld", fn, (long long)e->ldr, (long long)w->rows);
+    if (e->residual == y && (e->residual_dtype != y_dtype || (a && a->rows > 1 && e->ldr != ldy)))
+      return fail(W4A4_ERR_INVALID_ARG, "%s: the residual is y with another stride or type", fn);
   }
-  return cuda_status(w4a4::launch_mx_gemm(w->codes, w->scales, N, a->codes, a->scales, M, a->K, y,
-                                          y_dtype == W4A4_DTYPE_BF16, ldy, ws, reinterpret_cast<cudaStream_t>(stream)),
-                     fn);
+  const w4a4::MxEpilogue ep{e->bias, e->residual, e->ldr, bf16, e->act};
+  return mx_product(fn, w, a, &ep, y, y_dtype, ldy, ws, ws_bytes, stream);
 }
 
 w4a4_status w4a4_rmsnorm_quantize_act(const w4a4_rmsnorm* in, w4a4_act4* out, w4a4_stream_t stream) {
@@ -706,6 +778,81 @@ w4a4_status mxfp4_swiglu_quantize(const void* gate, const void* up, int dtype, i
                        stream);
 }
 
+w4a4_status kv8_append(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, const w4a4_kv8_new* in, w4a4_stream_t stream) {
+  const char* fn = "kv8_append";
+  w4a4::KvCache c;
+  w4a4::KvSeqs q;
+  w4a4_status s = open_kv8(cache, seqs, &c, &q, fn);
+  if (s != W4A4_OK) return s;
+  if (!in) return fail(W4A4_ERR_INVALID_ARG, "%s: in is NULL", fn);
+  if (in->q_heads < 0 || (in->q_heads > 0) != (in->q != nullptr && in->q_out != nullptr))
+    if (q.tokens > 0 || in->q_heads < 0) return fail(W4A4_ERR_INVALID_ARG, "%s: q_heads=%d with q or q_out NULL, or the reverse", fn, in->q_heads);
+  if (in->interleaved != 0 && in->interleaved != 1) return fail(W4A4_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", fn);
+  if (in->nf < 0 || 2 * static_cast<int64_t>(in->nf) > c.dim) return fail(W4A4_ERR_INVALID_ARG, "%s: nf=%d angles for dim %d", fn, in->nf, c.dim);
+  if (in->nf > 0 && !in->freqs) return fail(W4A4_ERR_INVALID_ARG, "%s: freqs is NULL", fn);
+  if ((reinterpret_cast<uintptr_t>(in->freqs) & 7) != 0) return fail(W4A4_ERR_ALIGNMENT, "%s: freqs must be 8-byte aligned", fn);
+  if (!in->interleaved && in->nf % 8 != 0) return fail(W4A4_ERR_UNSUPPORTED, "%s: nf=%d is not a multiple of 8 (pairs i, i + nf)", fn, in->nf);
+  s = check_heads(in->k, in->x_dtype, q.tokens, c.heads, c.dim, in->ldk, in->ldkh, "k", fn);
+  if (s == W4A4_OK) s = check_heads(in->v, in->x_dtype, q.tokens, c.heads, c.dim, in->ldv, in->ldvh, "v", fn);
+  if (s == W4A4_OK && in->q_heads > 0) s = check_heads(in->q, in->x_dtype, q.tokens, in->q_heads, c.dim, in->ldq, in->ldqh, "q", fn);
+  if (s == W4A4_OK && in->q_heads > 0) s = check_heads(in->q_out, in->o_dtype, q.tokens, in->q_heads, c.dim, in->ldo, in->ldoh, "q_out", fn);
+  if (s == W4A4_OK && in->q_heads > 0 && q.tokens > 0 && in->q == in->q_out && (in->x_dtype != in->o_dtype || in->ldq != in->ldo || in->ldqh != in->ldoh))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: q_out is q with other strides or another type", fn);
+  if (s != W4A4_OK) return s;
+  if (q.tokens == 0) return ok();
+  const w4a4::KvNew n{in->k, in->v, in->q, in->q_out, in->freqs, in->ldk, in->ldkh, in->ldv, in->ldvh, in->ldq, in->ldqh,
+                      in->ldo, in->ldoh, in->q_heads, in->nf, in->interleaved, in->x_dtype == W4A4_DTYPE_BF16, in->o_dtype == W4A4_DTYPE_BF16};
+  return cuda_status(w4a4::launch_kv8_append(c, q, n, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+w4a4_status kv8_read(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, void* k, void* v, int y_dtype, int64_t ldk,
+                     int64_t ldkh, int64_t ldv, int64_t ldvh, w4a4_stream_t stream) {
+  const char* fn = "kv8_read";
+  w4a4::KvCache c;
+  w4a4::KvSeqs q;
+  w4a4_status s = open_kv8(cache, seqs, &c, &q, fn);
+  if (s == W4A4_OK) s = check_heads(k, y_dtype, q.tokens, c.heads, c.dim, ldk, ldkh, "k", fn);
+  if (s == W4A4_OK) s = check_heads(v, y_dtype, q.tokens, c.heads, c.dim, ldv, ldvh, "v", fn);
+  if (s != W4A4_OK) return s;
+  if (q.tokens == 0) return ok();
+  return cuda_status(w4a4::launch_kv8_read(c, q, k, v, y_dtype == W4A4_DTYPE_BF16, ldk, ldkh, ldv, ldvh,
+                                           reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
+size_t kv8_attention_workspace_bytes(int dim) { return kv8_dim(dim) ? w4a4::kv8_attention_workspace_bytes(dim) : 0; }
+
+w4a4_status kv8_attention(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, const w4a4_kv8_attn* in, void* ws,
+                          size_t ws_bytes, w4a4_stream_t stream) {
+  const char* fn = "kv8_attention";
+  w4a4::KvCache c;
+  w4a4::KvSeqs q;
+  w4a4_status s = open_kv8(cache, seqs, &c, &q, fn);
+  if (s != W4A4_OK) return s;
+  if (!in) return fail(W4A4_ERR_INVALID_ARG, "%s: in is NULL", fn);
+  if (q.batch > w4a4::kKvMaxBatch) return fail(W4A4_ERR_UNSUPPORTED, "%s: batch=%d is above %d", fn, q.batch, w4a4::kKvMaxBatch);
+  if (in->q_heads <= 0 || in->q_heads % c.heads != 0)
+    return fail(W4A4_ERR_INVALID_ARG, "%s: q_heads=%d is not a positive multiple of the cache's %d heads", fn, in->q_heads, c.heads);
+  if (static_cast<int64_t>(q.tokens) * in->q_heads >= (int64_t(1) << 31))
+    return fail(W4A4_ERR_UNSUPPORTED, "%s: tokens * q_heads is 2^31 or more", fn);
+  if ((in->causal != 0 && in->causal != 1) || in->window < 0 || (in->window > 0 && !in->causal))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: causal must be 0 or 1, window >= 0, and a window needs causal", fn);
+  if (!(in->scale >= -3.402823466e38f && in->scale <= 3.402823466e38f)) return fail(W4A4_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  s = check_heads(in->q, in->q_dtype, q.tokens, in->q_heads, c.dim, in->ldq, in->ldqh, "q", fn);
+  if (s == W4A4_OK) s = check_heads(in->out, in->o_dtype, q.tokens, in->q_heads, c.dim, in->ldo, in->ldoh, "out", fn);
+  if (s == W4A4_OK && q.tokens > 0 && in->q == in->out && (in->q_dtype != in->o_dtype || in->ldq != in->ldo || in->ldqh != in->ldoh))
+    return fail(W4A4_ERR_INVALID_ARG, "%s: out is q with other strides or another type", fn);
+  if (s != W4A4_OK) return s;
+  if (ws) {
+    if (!aligned16(ws)) return fail(W4A4_ERR_ALIGNMENT, "%s: the workspace must be 16-byte aligned", fn);
+    if (ws_bytes < w4a4::kv8_attention_workspace_bytes(c.dim))
+      return fail(W4A4_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, w4a4::kv8_attention_workspace_bytes(c.dim));
+  }
+  if (q.tokens == 0) return ok();
+  const w4a4::KvAttn a{in->q, in->out, in->ldq, in->ldqh, in->ldo, in->ldoh, in->q_heads, in->q_dtype == W4A4_DTYPE_BF16,
+                       in->o_dtype == W4A4_DTYPE_BF16, in->causal, in->window, in->scale};
+  return cuda_status(w4a4::launch_kv8_attention(c, q, a, ws, reinterpret_cast<cudaStream_t>(stream)), fn);
+}
+
 w4a4_status w4a4_check(w4a4_stream_t stream) {
   const char* fn = "w4a4_check";
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
@@ -713,8 +860,10 @@ w4a4_status w4a4_check(w4a4_stream_t stream) {
   int flag = 0;
   e = w4a4::read_and_clear_device_error(&flag);
   if (e != cudaSuccess) return cuda_status(e, fn);
+  if ((flag & ~w4a4::kErrPage) != 0)
+    return fail(W4A4_ERR_TIMEOUT, "%s: a bounded wait inside a kernel gave up; its output is incomplete", fn);
   if (flag != 0)
-    return fail(W4A4_ERR_TIMEOUT, "%s: a bounded wait inside a GEMM kernel gave up; its output is incomplete", fn);
+    return fail(W4A4_ERR_DEVICE_FLAG, "%s: a kv8 call met a page, length or offset outside its range", fn);
   return ok();
 }
 

@@ -62,6 +62,7 @@ struct MxArgs {
   float4* parts;     // [pairs][2][8][32][32]: a warp's 128 accumulators of 32 lanes
   int* err;
   int64_t wait, delay;  // cycles: the pipeline waits' bound; a test's hold on the first copy
+  MxEpilogue ep;
 };
 
 struct Bars {
@@ -243,6 +244,50 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
+// ---------------------------------------------------------------- bias, activation, residual
+// act(r + bias) + residual on tokens m0 .. m0 + lim - 1 of this lane's weight row n, in place
+// in the accumulators (r[i] = token i): nothing but the residual is read, a warp's lanes 32
+// consecutive values of a token.  SiLU and the tanh form of GELU are both x / (1 + exp(-z)),
+// z = x (c1 + c3 x^2), since (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)): one code for both.
+template <int NC>
+__device__ __forceinline__ void epilogue(uint32_t (&r)[NC], const MxEpilogue& e, int64_t n, int64_t N, int64_t m0, int lim) {
+  if (e.bias) {
+    const float b = n < N ? e.bias[n] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + b);
+  }
+  if (e.act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) <= 0.0f ? 0.0f : __uint_as_float(r[i]));
+  } else if (e.act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const float x = __uint_as_float(r[i]);
+      r[i] = __float_as_uint(0.5f * x * (1.0f + erff(x * 0.70710678118654752f)));
+    }
+  } else if (e.act != kActNone) {
+    const float c1 = e.act == kActSilu ? 1.0f : 1.5957691216057308f, c3 = e.act == kActSilu ? 0.0f : 0.07135481282553567f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const float x = __uint_as_float(r[i]);
+      r[i] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x * fmaf(c3 * x, x, c1))));
+    }
+  }
+  if (e.residual && n < N) {
+    if (e.r_bf16) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.residual) + m0 * e.ldr + n;
+#pragma unroll
+      for (int i = 0; i < NC; ++i, p += e.ldr)
+        if (i < lim) r[i] = __float_as_uint(__uint_as_float(r[i]) + __bfloat162float(*p));
+    } else {
+      const float* p = static_cast<const float*>(e.residual) + m0 * e.ldr + n;
+#pragma unroll
+      for (int i = 0; i < NC; ++i, p += e.ldr)
+        if (i < lim) r[i] = __float_as_uint(__uint_as_float(r[i]) + *p);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- stores of Y
 // Tokens 0 .. lim - 1 of this lane's weight row n from NC accumulators (r[i] = token
 // i); y points at token 0.  bf16: neighbouring lanes trade so that the even lane
@@ -307,7 +352,7 @@ struct Small {
 constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
 
 // grid (S, weight tiles, token tiles), cluster (S, 1, 1).
-template <int NT, bool BF16>
+template <int NT, bool BF16, bool EPI>
 __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                     const __grid_constant__ CUtensorMap amap,
                                                                     const __grid_constant__ CUtensorMap wsmap,
@@ -403,6 +448,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   constexpr int NC = NT < 32 ? NT : 32;  // columns per pass
   constexpr int kEsz = BF16 ? 2 : 4;
   uint8_t* const y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * kEsz;
+  if (EPI) grid_dep_wait();  // the residual and the bias may be what is in front of this kernel's
   if (split == 1) {
     if (whole)
 #pragma unroll
@@ -412,6 +458,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         for (int i = 0; i < NC; i += 16) tmem_ld16(lanes + c + i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
 #pragma unroll
         for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
+        if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0 + c, tok - c);
         store_cols<BF16>(r, y + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
   } else {
@@ -449,8 +496,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
           const float4 o = *reinterpret_cast<const float4*>(part + 16 * ((q * (share >> 2) + (i >> 2)) * kTW));
           v = make_float4(__fadd_rn(v.x, o.x), __fadd_rn(v.y, o.y), __fadd_rn(v.z, o.z), __fadd_rn(v.w, o.w));
         }
-        const uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+        uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
         const int64_t m = static_cast<int64_t>(rank) * share + i;
+        if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0 + m, static_cast<int>(tok - m));
         store_cols<BF16>(r, y + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
       }
     }
@@ -519,7 +567,7 @@ struct Work {
 
 // Persistent.  CTA `rank` of the pair holds weight rows 128 rank .. of the tile, one
 // half of its tokens as its part of the N operand, and every token's scales.
-template <bool BF16>
+template <bool BF16, bool EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap asmap, const MxArgs p) {
@@ -682,8 +730,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       }
       const int64_t n = static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3) + lane;
       const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * kMaxTok + 128 * (warp >> 2);
-      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N,
-                         static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
+      const int lim = static_cast<int>(min(static_cast<int64_t>(128), p.M - m0));
+      if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0, lim);
+      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N, lim);
     }
   }
   tc_fence_before();
@@ -740,7 +789,7 @@ int small_split(int nt, int64_t tiles, int stages) {
   return best;
 }
 
-template <int NT>
+template <int NT, bool EPI>
 cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16, cudaStream_t st) {
   using C = Small<NT>;
   static bool configured[2][64] = {};
@@ -754,8 +803,8 @@ cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16,
   if (b.ring > (a.stages + split - 1) / split) b.ring = (a.stages + split - 1) / split;
   b.apart = split > 1 && C::apart(b.ring, most) ? b.ring * C::kStageBytes : 0;
   const int smem = C::smem(b.ring, most);
-  return y_bf16 ? launch(mx_small_kernel<NT, true>, configured[1], grid, kSmallThreads, smem, split, m, b, st)
-                : launch(mx_small_kernel<NT, false>, configured[0], grid, kSmallThreads, smem, split, m, b, st);
+  return y_bf16 ? launch(mx_small_kernel<NT, true, EPI>, configured[1], grid, kSmallThreads, smem, split, m, b, st)
+                : launch(mx_small_kernel<NT, false, EPI>, configured[0], grid, kSmallThreads, smem, split, m, b, st);
 }
 
 // The small kernel serves up to 128 tokens, and more while its tiles (128 x 128) have an
@@ -807,9 +856,25 @@ void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
   g_delay = cycles(producer_delay_ns);
 }
 
+template <bool EPI>
+static cudaError_t launch_mx(const CUtensorMap (&m)[4], const MxArgs& a, bool small, int pairs, int y_bf16, cudaStream_t stream) {
+  if (!small) {
+    static bool configured[2][64] = {};
+    const dim3 grid(static_cast<unsigned>(2 * pairs));
+    return y_bf16 ? launch(mx_pair_kernel<true, EPI>, configured[1], grid, kPairThreads, kPairSmem, 0, m, a, stream)
+                  : launch(mx_pair_kernel<false, EPI>, configured[0], grid, kPairThreads, kPairSmem, 0, m, a, stream);
+  }
+  switch (a.box) {
+    case 16: return launch_small<16, EPI>(m, a, y_bf16, stream);
+    case 32: return launch_small<32, EPI>(m, a, y_bf16, stream);
+    case 64: return launch_small<64, EPI>(m, a, y_bf16, stream);
+    default: return launch_small<128, EPI>(m, a, y_bf16, stream);
+  }
+}
+
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
-                           cudaStream_t stream) {
+                           const MxEpilogue* ep, cudaStream_t stream) {
   MxArgs a{};
   a.y = y; a.ldy = ldy; a.M = M; a.N = N;
   a.K = static_cast<int>(K);
@@ -817,6 +882,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
   a.err = device_error_word();
   a.wait = g_wait;
   a.delay = g_delay;
+  if (ep) a.ep = *ep;
   PairPlan q{};
   const bool small = use_small(M, N);
   if (small) {
@@ -847,18 +913,7 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
     e = encode_2d_map(&m[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kt, static_cast<uint64_t>((M + 127) / 128), kt * 4,
                       256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (e != cudaSuccess) return e;
-  if (!small) {
-    static bool configured[2][64] = {};
-    const dim3 grid(static_cast<unsigned>(2 * q.pairs));
-    return y_bf16 ? launch(mx_pair_kernel<true>, configured[1], grid, kPairThreads, kPairSmem, 0, m, a, stream)
-                  : launch(mx_pair_kernel<false>, configured[0], grid, kPairThreads, kPairSmem, 0, m, a, stream);
-  }
-  switch (a.box) {
-    case 16: return launch_small<16>(m, a, y_bf16, stream);
-    case 32: return launch_small<32>(m, a, y_bf16, stream);
-    case 64: return launch_small<64>(m, a, y_bf16, stream);
-    default: return launch_small<128>(m, a, y_bf16, stream);
-  }
+  return ep ? launch_mx<true>(m, a, small, q.pairs, y_bf16, stream) : launch_mx<false>(m, a, small, q.pairs, y_bf16, stream);
 }
 
 }  // namespace w4a4

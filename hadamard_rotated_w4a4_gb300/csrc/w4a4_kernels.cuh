@@ -142,11 +142,56 @@ cudaError_t launch_import_mx(const uint8_t* codes, const uint8_t* scales, int64_
 // The MXFP4 product (mx_gemm.cu); ws: null, or mx_gemm_workspace_bytes(M, N, K) bytes,
 // zero before their first use.
 constexpr int64_t kMxMaxRows = 65535 * 128;  // rows of an operand: a tile of 128 or more per grid index
+// ep: null, or y = act(W a + bias) + residual.
+enum MxAct : int { kActNone, kActRelu, kActSilu, kActGelu, kActGeluTanh };
+struct MxEpilogue {
+  const float* bias;     // [N], may be null
+  const void* residual;  // [M][ldr], may be null
+  int64_t ldr;
+  int r_bf16, act;
+};
 cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, const uint8_t* a_codes,
                            const uint8_t* a_scales, int64_t M, int64_t K, void* y, int y_bf16, int64_t ldy, void* ws,
-                           cudaStream_t stream);
+                           const MxEpilogue* ep, cudaStream_t stream);
 size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 // Test hook, as grp_set_wait_limit, of the MXFP4 product's waits.
 void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
+
+// ---- the 8-bit paged key/value cache (kv_cache.cu, kv_attention.cu)
+struct KvCache {
+  int8_t* codes;    // [pages][heads][2][page][dim]
+  uint8_t* scales;  // [pages][heads][2][page / 16]
+  int pages, heads, page, dim, rotated;
+};
+// The sequences of a call: cu null = `each` tokens of every sequence.
+struct KvSeqs {
+  const int32_t* table;  // [batch][ldt], `width` pages a sequence
+  const int32_t* lens;   // [batch]
+  const int32_t* cu;     // [batch + 1] or null
+  int64_t ldt;
+  int batch, width, tokens, each;
+};
+// New keys and values, and (optional) queries: strides of tokens and of heads, in elements.
+struct KvNew {
+  const void *k, *v, *q;
+  void* q_out;
+  const double* freqs;  // nf radians a position
+  int64_t ldk, ldkh, ldv, ldvh, ldq, ldqh, ldo, ldoh;
+  int q_heads, nf, interleaved, x_bf16, o_bf16;
+};
+cudaError_t launch_kv8_append(const KvCache& c, const KvSeqs& s, const KvNew& a, cudaStream_t st);
+cudaError_t launch_kv8_read(const KvCache& c, const KvSeqs& s, void* k, void* v, int bf16, int64_t ldk, int64_t ldkh,
+                            int64_t ldv, int64_t ldvh, cudaStream_t st);
+struct KvAttn {
+  const void* q;
+  void* out;
+  int64_t ldq, ldqh, ldo, ldoh;
+  int q_heads, q_bf16, o_bf16, causal, window;
+  float scale;
+};
+constexpr int kErrPage = 1 << 16;  // bit of the device error word: a page, length or offset out of range
+constexpr int kKvMaxBatch = 2048;  // sequences of an attention call
+cudaError_t launch_kv8_attention(const KvCache& c, const KvSeqs& s, const KvAttn& a, void* ws, cudaStream_t st);
+size_t kv8_attention_workspace_bytes(int dim);
 
 }  // namespace w4a4

@@ -70,6 +70,7 @@ typedef enum {
 #define W4A4_TAG_ACT8 0x41380000u    /* int8 activations (the exact path)     */
 #define W4A4_TAG_ACT16 0x41420000u   /* bf16 activations (rotate-only route)  */
 #define W4A4_TAG_MXFP4 0x4D340000u   /* MXFP4 weights or activations          */
+#define W4A4_TAG_KV8 0x4B380000u     /* 8-bit paged keys and values           */
 #define W4A4_TAG_MAGIC_MASK 0xFFFF0000u
 #define W4A4_TAG_ROTATED 0x00000001u /* values were rotated by H32 per block  */
 
@@ -505,6 +506,33 @@ w4a4_status mxfp4_gemm(const w4a4_mxfp4* w, const w4a4_mxfp4* a, void* y, int y_
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /*
+ * mxfp4_gemm_epilogue -- Y = act(W a + bias) + residual, the MXFP4 product with what
+ * stands behind a projection in its epilogue; operands, output, workspace and order of
+ * sums as in mxfp4_gemm.  The fp32 sum takes the bias, the activation and the residual in
+ * fp32; Y is rounded once.
+ *   bias    : device, N fp32 values, or NULL.
+ *   residual: device, [M][ldr] of residual_dtype, aligned to its element, or NULL.  It may
+ *             be y itself (same type and stride), no other overlap with y.
+ *   act     : W4A4_ACT_NONE, _RELU (max(x, 0); a NaN stays one), _SILU (x / (1 + exp(-x))),
+ *             _GELU (x (1 + erf(x / sqrt 2)) / 2) or _GELU_TANH (x (1 + tanh(sqrt(2 / pi)
+ *             (x + 0.044715 x^3))) / 2).
+ */
+#define W4A4_ACT_NONE 0
+#define W4A4_ACT_RELU 1
+#define W4A4_ACT_SILU 2
+#define W4A4_ACT_GELU 3
+#define W4A4_ACT_GELU_TANH 4
+typedef struct {
+  const float* bias;
+  const void* residual;
+  int64_t ldr;
+  int residual_dtype; /* W4A4_DTYPE_BF16 or W4A4_DTYPE_F32 */
+  int act;
+} w4a4_epilogue;
+w4a4_status mxfp4_gemm_epilogue(const w4a4_mxfp4* w, const w4a4_mxfp4* a, const w4a4_epilogue* e, void* y, int y_dtype,
+                                int64_t ldy, void* ws, size_t ws_bytes, w4a4_stream_t stream);
+
+/*
  * Residual addition + RMS norm + rotation + quantisation, in one pass: what stands
  * in front of a projection.
  *   h = x + r (fp32);  r_out = h (rounded to r's type);
@@ -551,10 +579,123 @@ w4a4_status mxfp4_swiglu_quantize(const void* gate, const void* up, int dtype, i
                                   int64_t ldu, int rotate, w4a4_mxfp4* out, w4a4_stream_t stream);
 
 /*
- * w4a4_check -- synchronise `stream`, then report whether any GEMM kernel run
+ * Keys and values in 8 bits, in pages: what attention reads of the tokens before.
+ *   codes : device, [pages][heads][2][page][dim] int8: of each page and head its tokens'
+ *           keys, then their values.
+ *   scales: device, [pages][heads][2][page / 16]: 16 tokens share a scale per head, for K
+ *           and for V, the power of two 2^(s - 127) of byte s, 87 <= s <= 167 (255 = NaN).
+ *   page  : tokens of a page, 16, 32, 64 or 128.   dim: 64, 128 or 256.
+ *   tag   : W4A4_TAG_KV8 | (W4A4_TAG_ROTATED if keys and values are rotated by H32 per 32
+ *           elements, which spreads loud channels over the codes of their block).
+ * A scale is 2^E with E the least integer that has amax <= 127 * 2^E, -40 <= E <= 40, and a
+ * code the integer nearest to value / 2^E, ties to even (what is past 127 * 2^40 saturates).
+ * codes are 16-byte aligned.
+ */
+typedef struct {
+  int8_t* codes;
+  uint8_t* scales;
+  int64_t pages;
+  int heads, page, dim;
+  uint32_t tag;
+} w4a4_kv8;
+
+/*
+ * The sequences of a call.  Token t of sequence b stands in page table[b][t / page] at row
+ * t % page; the call's tokens are the last ones of each sequence, one sequence's after the
+ * other's in k, v and q.
+ *   table: device, [batch][ldt] int32, width entries a sequence (width * page < 2^31).
+ *   lens : device, [batch] int32: tokens of each sequence, the new ones among them.
+ *   cu   : device, [batch + 1] int32: sequence b has the call's tokens cu[b] .. cu[b + 1] - 1
+ *          (0 <= cu[0], never falling, cu[batch] <= tokens; what lies outside is left as it
+ *          was); NULL: tokens / batch each.
+ * These are read on the device, so that a captured call follows them.  A table entry
+ * outside 0 .. pages - 1 counts as a page without tokens (append skips its tokens, read gives
+ * zeros, attention does not see them); a length past the table is cut, offsets are clamped;
+ * so are tokens before a sequence's start (cu longer than lens) skipped.  Each of these sets
+ * the flag that w4a4_check reports as W4A4_ERR_DEVICE_FLAG.
+ */
+typedef struct {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* cu;
+  int64_t batch, width, ldt, tokens;
+} w4a4_kv8_seqs;
+
+/*
+ * kv8_append -- new keys and values into the pages: rotary positions (optional; k, and q if
+ * there is one), then H32 (if the cache is rotated; k and v), then codes.
+ *   k, v : device, [tokens][heads][dim] of x_dtype; ld.. are the strides of tokens, ld..h of
+ *          heads, in elements.
+ *   q    : device, [tokens][q_heads][dim] of x_dtype, or NULL (q_heads 0).  Rotated by its
+ *          position (not by H32) into q_out, which may be q itself.
+ *   freqs: device, nf radians a position (double), or NULL (nf 0) for no positions.  Pair i
+ *          is turned by position * freqs[i], reduced in 64 bits.  interleaved 0: pairs
+ *          (i, i + nf), nf a multiple of 8; 1: (2i, 2i + 1); 2 nf <= dim, elements past 2 nf
+ *          pass as they are.  A token's position is its place in the sequence.
+ * A block of 16 tokens that a call fills further keeps its scale unless the new tokens need
+ * a larger one: then the codes before them are rounded to that (a shift; all such steps
+ * together are less than one step of the last scale).  A block that gets an infinity or a
+ * NaN gets scale byte 255: its tokens read back as NaN until its first row is written again.
+ * Rows of a block past the new tokens are left as they were.  Two tokens of a call must not
+ * share a row, nor two sequences a block that either writes.
+ */
+typedef struct {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  const double* freqs;
+  int64_t ldk, ldkh, ldv, ldvh, ldq, ldqh, ldo, ldoh;
+  int q_heads, nf, interleaved;
+  int x_dtype, o_dtype; /* W4A4_DTYPE_BF16 or W4A4_DTYPE_F32 */
+} w4a4_kv8_new;
+w4a4_status kv8_append(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, const w4a4_kv8_new* in, w4a4_stream_t stream);
+
+/*
+ * kv8_read -- the values that the codes of the call's tokens stand for, k and v
+ * [tokens][heads][dim] of y_dtype (an H32 rotation is not undone).  Strides as above.
+ */
+w4a4_status kv8_read(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, void* k, void* v, int y_dtype, int64_t ldk,
+                     int64_t ldkh, int64_t ldv, int64_t ldvh, w4a4_stream_t stream);
+
+/*
+ * kv8_attention -- softmax(scale q K^T) V over the pages, for one token to long prompts.
+ *   q     : device, [tokens][q_heads][dim] of q_dtype, not rotated by H32 whatever the cache
+ *           is; q_heads a multiple of the cache's heads: query head h reads head
+ *           h / (q_heads / heads).
+ *   out   : device, [tokens][q_heads][dim] of o_dtype.  It may be q itself.
+ *   scale : finite.
+ *   causal: 1: a token sees its own place and those before; 0: the whole sequence (the
+ *           states of an encoder, for instance).   window > 0 (with causal): the last
+ *           `window` of them.
+ * A token that sees no key gets zeros.  q is rounded to 11 bits (bf16 values without H32
+ * exactly), the weights to 11 bits; products and sums are fp32.  A NaN in q makes its rows
+ * NaN, a block of NaN scale the rows that see a token of it.
+ *   ws: optional device workspace (kv8_attention_workspace_bytes or more, 16-byte aligned,
+ *       its first MiB zero before its first use; a smaller one is W4A4_ERR_WORKSPACE; it may
+ *       be one that a product uses as well).  With it long sequences are cut over the SMs
+ *       and joined; without it few sequences leave SMs idle.  Every call leaves it as it
+ *       needs to find it.  Calls that share one must not overlap on the GPU.
+ * batch <= 2048 (W4A4_ERR_UNSUPPORTED above).  The order of every sum is fixed on a given
+ * device: equal inputs give equal bits.
+ */
+typedef struct {
+  const void* q;
+  void* out;
+  int64_t ldq, ldqh, ldo, ldoh;
+  int q_heads, q_dtype, o_dtype, causal, window;
+  float scale;
+} w4a4_kv8_attn;
+w4a4_status kv8_attention(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, const w4a4_kv8_attn* in, void* ws,
+                          size_t ws_bytes, w4a4_stream_t stream);
+size_t kv8_attention_workspace_bytes(int dim);
+
+/*
+ * w4a4_check -- synchronise `stream`, then report whether any GEMM or attention kernel run
  * since the last check gave up on one of its bounded internal waits (a pipeline
  * that stopped making progress for a second).  Such a kernel stops early, so
- * its output is incomplete: W4A4_ERR_TIMEOUT.  Clears the condition.  Returns
+ * its output is incomplete: W4A4_ERR_TIMEOUT.  Without one, W4A4_ERR_DEVICE_FLAG if a kv8
+ * call met a page, length or offset outside its range.  Clears both conditions.  Returns
  * W4A4_ERR_CUDA for an error already pending on the stream.
  *
  * The library caches, per device, the addresses of its device-side state (this

@@ -56,6 +56,13 @@ weighted``                     than the plain scale; 2^k weight invariance
 ``quantize_mxfp4`` /           powers of two, zero, subnormal and non-finite
 ``mxfp4_values``               blocks by hand; round trip of every code
 ``mxfp4_matmul``               brute-force loops in exact fractions
+``rope``                       a rotation in the complex plane; dot products depend
+                               on the difference of positions alone
+``kv8_exponent`` /             powers of two, border and zero blocks by hand;
+``kv8_append`` /               half-step round trip; growing scales stay within
+``kv8_values``                 a step whatever the order of the tokens
+``kv8_attention``              equal keys average the values; a far larger key picks
+                               its value; windows and empty rows by hand
 =============================  ==============================================
 
 Every function above is pinned; none is "parity unpinned".  The informative
@@ -87,6 +94,7 @@ from .quant import (
     effective_importance,
 )
 from .mxfp4 import E2M1, e2m1_code, quantize_mxfp4, mxfp4_values, mxfp4_matmul
+from .kv8 import KV8_TOKENS, rope, kv8_exponent, kv8_append, kv8_values, kv8_attention
 from .matmul import block_partials, w4a4_matmul, w4a4_matmul_id, w4a8_matmul, w4a16_matmul, exact_matmul
 
 __all__ = [
@@ -99,5 +107,6 @@ __all__ = [
     "rotate_importance", "weighted_block_scale", "quantize_weights_q4_0_weighted", "pack_weights_imatrix",
     "effective_importance",
     "E2M1", "e2m1_code", "quantize_mxfp4", "mxfp4_values", "mxfp4_matmul",
+    "KV8_TOKENS", "rope", "kv8_exponent", "kv8_append", "kv8_values", "kv8_attention",
     "block_partials", "w4a4_matmul", "w4a4_matmul_id", "w4a8_matmul", "w4a16_matmul", "exact_matmul",
 ]
