@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 
 LIB_SOURCES = ["act_quant.cu", "pack_weights.cu", "gemm_tc.cu", "gemm_grp.cu", "gemm_id.cu", "gemm_small_m.cu", "fused_quant.cu",
-               "mx_gemm.cu", "kv_cache.cu", "kv_decode.cu", "capi.cu"]
+               "mx_gemm.cu", "kv_cache.cu", "kv_decode.cu", "kv_prompt.cu", "capi.cu"]
 PROBE_SOURCES = ["probes.cu"]
 LIB = os.path.join(PKG, "libw4a4.so")
 PROBE_LIB = os.path.join(PKG, "libw4a4_probes.so")

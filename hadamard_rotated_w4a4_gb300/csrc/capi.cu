@@ -151,7 +151,7 @@ w4a4_status open_kv8(const w4a4_kv8* c, const w4a4_kv8_seqs* q, w4a4::KvCache* o
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
     return fail(W4A4_ERR_INVALID_ARG, "%s: page=%d must be 16, 32, 64 or 128", fn, c->page);
   if (!kv8_dim(c->dim)) return fail(W4A4_ERR_UNSUPPORTED, "%s: dim=%d must be 64, 128 or 256", fn, c->dim);
-  if (c->heads <= 0 || c->heads > 65535 || c->pages < 0 || c->pages >= (int64_t(1) << 31))
+  if (c->heads <= 0 || c->heads > 65535 || c->pages < (q->tokens > 0) || c->pages >= (int64_t(1) << 31))
     return fail(W4A4_ERR_INVALID_ARG, "%s: heads=%d or pages=%lld out of range", fn, c->heads, (long long)c->pages);
   const int64_t most = (int64_t(1) << 31) - 256;
   if (q->batch < 0 || q->batch > most || q->tokens < 0 || q->tokens > most || q->width < 0 || q->width * c->page > most || q->width > most)
@@ -161,7 +161,7 @@ w4a4_status open_kv8(const w4a4_kv8* c, const w4a4_kv8_seqs* q, w4a4::KvCache* o
     return fail(W4A4_ERR_INVALID_ARG, "%s: %lld tokens are not the same number for each of %lld sequences, and cu is NULL", fn,
                 (long long)q->tokens, (long long)q->batch);
   if (q->batch == 0 && q->tokens > 0) return fail(W4A4_ERR_INVALID_ARG, "%s: tokens without a sequence", fn);
-  if (q->tokens > 0 && (!q->lens || (!q->table && q->width > 0) || (c->pages > 0 && (!c->codes || !c->scales))))
+  if (q->tokens > 0 && (!q->lens || (!q->table && q->width > 0) || !c->codes || !c->scales))
     return fail(W4A4_ERR_INVALID_ARG, "%s: table, lens, codes or scales is NULL", fn);
   if (((reinterpret_cast<uintptr_t>(q->table) | reinterpret_cast<uintptr_t>(q->lens) | reinterpret_cast<uintptr_t>(q->cu)) & 3) != 0)
     return fail(W4A4_ERR_ALIGNMENT, "%s: table, lens and cu must be 4-byte aligned", fn);
@@ -870,6 +870,7 @@ w4a4_status w4a4_check(w4a4_stream_t stream) {
 void w4a4_debug_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
   w4a4::grp_set_wait_limit(wait_ns, producer_delay_ns);
   w4a4::mx_set_wait_limit(wait_ns, producer_delay_ns);
+  w4a4::kv8_set_wait_limit(wait_ns, producer_delay_ns);
 }
 
 const char* w4a4_last_error(void) { return g_err; }

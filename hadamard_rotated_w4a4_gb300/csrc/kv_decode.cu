@@ -527,8 +527,12 @@ cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
 
 }  // namespace
 
+// Few query rows (tokens x query heads per head of K and V), up to a tile of this kernel, are its work; more
+// go to the tensor cores.  A call with offsets may hold both kinds: each kernel takes its own.
 size_t kv8_attention_workspace_bytes(int dim) {
-  return kWsCounters + static_cast<size_t>(num_sms()) * 2 * kRows * (dim + 2) * sizeof(float);
+  const size_t mine = kWsCounters + static_cast<size_t>(num_sms()) * 2 * kRows * (dim + 2) * sizeof(float);
+  const size_t other = kv8_prompt_workspace_bytes(dim);
+  return mine > other ? mine : other;
 }
 
 cudaError_t launch_kv8_attention(const KvCache& c, const KvSeqs& s, const KvAttn& a, void* ws, cudaStream_t st) {
@@ -537,15 +541,16 @@ cudaError_t launch_kv8_attention(const KvCache& c, const KvSeqs& s, const KvAttn
   p.s = s;
   p.a = a;
   p.group = a.q_heads / c.heads;
-  p.most_rows = 1 << 30;
+  p.most_rows = kRows;
   p.tickets = static_cast<uint32_t*>(ws);
   p.parts = ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounters) : nullptr;
   p.err = device_error_word();
-  switch (c.dim) {
-    case 64: return launch_decode<64>(p, st);
-    case 128: return launch_decode<128>(p, st);
-    default: return launch_decode<256>(p, st);
-  }
+  const bool few = s.cu ? p.group <= kRows : static_cast<int64_t>(s.each) * p.group <= kRows;
+  const bool many = static_cast<int64_t>(s.cu ? s.tokens : s.each) * p.group > kRows;
+  cudaError_t e = cudaSuccess;
+  if (few) e = c.dim == 64 ? launch_decode<64>(p, st) : c.dim == 128 ? launch_decode<128>(p, st) : launch_decode<256>(p, st);
+  if (e == cudaSuccess && many) e = launch_kv8_prompt(c, s, a, kRows + 1, ws, st);
+  return e;
 }
 
 }  // namespace w4a4

@@ -1,0 +1,727 @@
+// Attention of many query rows over the 8-bit paged cache: prompts and pieces of them.
+//
+// A CTA takes up to 256 query rows (128 with heads of 256) of one head of K and V, rows being
+// tokens x the heads that share it, and goes over the keys in tiles of 128 with the running
+// maximum and sum of a softmax.  S = Q K^T and O += P V run on the tensor cores
+// (tcgen05.mma kind::f16), accumulators in TMEM; P overwrites its S there and is the second
+// product's A operand.  Bounds: the two products, 4 D operations a row and key; the exponential,
+// one a row and key; and the way from codes to fp16.
+//
+// Warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread, so that no maximum crosses
+// lanes; 8-11 the codes: copied (cp.async) to a ring that each thread alone reads, converted, and
+// written as both products' B operand: keys are rows of 128 bytes in the 128-byte swizzle either
+// way, K read along d (K-major), V along the keys (MN-major); 12 issues the MMAs.  The two row
+// tiles take turns: while one's weights are computed the other's products run.  With heads of
+// 256 TMEM has room for one row tile with two S, and the next tile's S runs beside the softmax.
+//
+// O is rescaled only when a row's maximum grew by more than 2^8: the weights then still fit fp16.
+#include <cuda_bf16.h>
+
+#include "kv_attention.cuh"
+#include "tc_ptx.cuh"
+
+namespace w4a4 {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kBK = 128;                         // keys of a tile
+constexpr int kBlocks = kBK / kKvTokens;         // blocks of 16 keys, each with its scales
+constexpr int64_t kWaitCycles = int64_t(1) << 31;  // 1.04 s at the top clock, longer below it
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 256 threads each; together the launch's 512 x 128
+static_assert(kSoftmaxRegs + kOtherRegs <= 2 * 128);
+constexpr size_t kWsCounters = size_t(1) << 20;
+
+template <int D>
+struct Shape {
+  static constexpr int kTiles = D == 256 ? 1 : 2;   // row tiles of 128
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kBufs = D == 256 ? 1 : 2;    // converted tiles of K, and of V
+  static constexpr int kTile = kBK * D * 2;         // bytes of one
+  static constexpr int kPanel = 128 * 128;          // bytes of 64 elements of 128 rows
+  static constexpr int kQ = 0, kK = kQ + kRows * D * 2, kV = kK + kBufs * kTile, kRaw = kV + kBufs * kTile;
+  static constexpr int kChunks = kBK * D / 16 / 128;  // 16-code pieces of a thread in a tile of K
+  static constexpr int kGroup = 4, kRing = 4;         // pieces of a copy group; groups in flight
+  static constexpr int kGroups = kChunks / kGroup;    // groups of a tile of K
+  static constexpr int kPrefix = kK;  // find_work's sums, before the first tile of K
+  static constexpr int kSmem = 1024 + kRaw + kRing * kGroup * 128 * 16;
+  static constexpr int kS = 0, kO = 256;            // TMEM columns
+  static constexpr int kPart = kRows * (D + 2);     // floats of a cut tile's part
+  static_assert(kSmem <= 227 * 1024 - 2 * 1024 && kO + kTiles * D <= 512 && 4 * (kKvMaxBatch + 1) <= kBufs * kTile);
+};
+
+struct PromptArgs {
+  KvCache c;
+  KvSeqs s;
+  KvAttn a;
+  int group;
+  int least_rows;  // sequences with fewer query rows are another kernel's
+  int sms;
+  float* parts;    // [sms][kPart]: with few tiles, their keys cut over the SMs; null: not cut
+  int* err;
+  int64_t wait, delay;
+};
+
+struct Bars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], sc_full[4];
+  uint32_t tmem;
+  volatile int abort;
+};
+
+__device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, const PromptArgs& p) {
+  if (mbar_try(b, parity)) return true;
+  const int64_t t0 = clock64();
+  while (!mbar_try(b, parity)) {
+    if (S.abort) return false;
+    if (clock64() - t0 > p.wait) {
+      S.abort = 1;
+      if (p.err) atomicOr(p.err, 64);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Operand descriptors in the 128-byte swizzle (layout type 2): K-major, 8-row groups 1024 bytes
+// apart; MN-major, groups of 8 keys 1024 bytes apart and 64-element panels `panel` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t smem) {
+  return static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t smem, uint32_t panel) {
+  return static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | (static_cast<uint64_t>(panel >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16, fp16 operands, fp32 sums, 128 rows; bit 16: B is MN-major.
+__device__ __forceinline__ constexpr uint32_t idesc_f16(int n, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// A from TMEM: row = lane, two fp16 of K a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// H32 of 32 values of one thread, the butterfly of quad_rotate.
+__device__ __forceinline__ void rotate32(float (&v)[32]) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= c_h32();
+}
+
+// Row tiles of a sequence, all heads.
+template <int D>
+__device__ __forceinline__ int tiles_of(const PromptArgs& p, const Seq& q) {
+  const int64_t rows = static_cast<int64_t>(q.n) * p.group;
+  return q.n == 0 || rows < p.least_rows ? 0 : static_cast<int>((rows + Shape<D>::kRows - 1) / Shape<D>::kRows) * p.c.heads;
+}
+
+// What a CTA does: rows row0 .. row0 + rows - 1 of (sequence, head), key tiles t0 .. t1 - 1 of
+// those that start at key0, as part `part` of `parts`.
+struct Work {
+  int b, head, row0, rows;
+  Seq q;
+  int key0, t0, t1, part, parts;
+};
+// By whole CTAs; prefix: shared, of batch + 1 entries; carry: shared, of 32.  False: nothing to do.
+// Tiles in descending order: with a causal mask a sequence's later rows see more keys, and go first.
+template <int D>
+__device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int* carry, int threads, int cta, Work& w) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int total = 0;
+  for (int b0 = 0; b0 < p.s.batch; b0 += threads) {
+    const int b = b0 + tid;
+    const int mine = b < p.s.batch ? tiles_of<D>(p, kv_seq(p.s, b, p.c.page, p.err)) : 0;
+    int at = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, at, d);
+      if (lane >= d) at += o;
+    }
+    if (lane == 31) carry[warp] = at;
+    __syncthreads();
+    int before = total;
+    for (int i = 0; i < threads / 32; ++i) {
+      if (i < warp) before += carry[i];
+      total += carry[i];
+    }
+    if (b < p.s.batch) prefix[b] = before + at - mine;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[p.s.batch] = total;
+  __syncthreads();
+  if (total == 0) return false;
+  const int most = p.parts ? max(1, p.sms / total) : 1;  // parts that a tile's keys may be cut into
+  if (cta >= total * most) return false;
+  const int tile = total - 1 - cta % total;
+  w.part = cta / total;
+  int b = 0;
+  for (int hi = p.s.batch; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (prefix[mid] <= tile) b = mid;
+    else hi = mid;
+  }
+  w.b = b;
+  w.q = kv_seq(p.s, b, p.c.page, nullptr);
+  const int in = tile - prefix[b];
+  w.head = in % p.c.heads;
+  w.row0 = in / p.c.heads * Shape<D>::kRows;
+  w.rows = min(Shape<D>::kRows, w.q.n * p.group - w.row0);
+  int lo, hi, ignore;
+  seen(p.a, w.q.len - w.q.n + w.row0 / p.group, w.q.len, lo, ignore);
+  seen(p.a, w.q.len - w.q.n + (w.row0 + w.rows - 1) / p.group, w.q.len, ignore, hi);
+  hi = max(hi, 0);
+  w.key0 = min(lo, w.q.len) / kKvTokens * kKvTokens;
+  const int n = max(1, (hi - w.key0 + kBK - 1) / kBK);
+  // two tiles a part at least: a part costs its Q, its first copies and its write of O
+  w.parts = min(most, (n + 1) / 2);
+  w.t0 = static_cast<int>(static_cast<int64_t>(n) * w.part / w.parts);
+  w.t1 = static_cast<int>(static_cast<int64_t>(n) * (w.part + 1) / w.parts);
+  return w.part < w.parts;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_constant__ PromptArgs p) {
+  using C = Shape<D>;
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ Bars S;
+  __shared__ float sm_f[C::kRows];
+  // per tile of keys: K scales, V exponents, 2^-exponent
+  __shared__ __align__(16) float sm_sc[4][3][kBlocks];
+  __shared__ int sm_carry[32];
+  uint8_t* const smem = raw_smem + ((1024u - (su32(raw_smem) & 1023u)) & 1023u);
+  const uint32_t sbase = su32(smem);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 4);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_ready[i], 4);
+      mbar_init(&S.pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], 1);
+    S.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&S.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_fence_before();
+  }
+  __syncthreads();
+  grid_dep_launch();  // behind the allocation
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  grid_dep_wait();
+  Work w;
+  const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), w);
+  if (!some) {
+    __syncthreads();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    return;
+  }
+  const int n = w.t1 - w.t0;
+  const int key0 = w.key0 + w.t0 * kBK;
+  const int qtiles = C::kTiles == 2 && w.rows > 128 ? 2 : 1;
+
+  // copies of codes: the thread's pieces of group g (K's groups of a tile, then V's), into ring slot g % kRing
+  const int ctid = tid - 256;
+  const auto page_of = [&](int tile) {  // lanes 0-7: the page of the tile's block `lane`, -1: none
+    const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
+    return tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
+  };
+  int pages = -1, pages_next = -1, issued = 0;  // pages of the tile to be copied next, and of the one after it
+  const auto issue = [&]() {
+    const int tile = issued / (2 * C::kGroups), in = issued % (2 * C::kGroups), v = in / C::kGroups;
+    if (tile < n) {
+#pragma unroll
+      for (int i = 0; i < C::kGroup; ++i) {
+        const int piece = ((in % C::kGroups) * C::kGroup + i) * 128 + ctid;
+        const int row = piece / (D / 16), cc = piece % (D / 16);
+        const int pg = __shfl_sync(0xFFFFFFFFu, pages, row / kKvTokens);
+        const int at = (key0 + tile * kBK + row) % p.c.page;
+        const int8_t* const src = p.c.codes + (pg >= 0 ? kv_at(p.c, pg, w.head, v) + static_cast<int64_t>(at) * D + 16 * cc : 0);
+        cp_async16(sbase + C::kRaw + (((issued % C::kRing) * C::kGroup + i) * 128 + ctid) * 16, src, pg >= 0);
+      }
+      if (in == 2 * C::kGroups - 1) {
+        pages = pages_next;
+        pages_next = page_of(tile + 2);
+      }
+    }
+    cp_commit();
+    ++issued;
+  };
+  if (warp >= 8 && warp < 12) {
+    pages = page_of(0);
+    pages_next = page_of(1);
+    if (p.delay == 0)
+#pragma unroll
+      for (int i = 0; i < C::kRing; ++i) issue();
+  }
+
+  // q: rotated as the keys are, scaled by a power of two per row, in the swizzle
+  const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
+  for (int ch = tid; ch < qtiles * 128 * (D / 8); ch += kThreads) {
+    const int row = ch / (D / 8), cc = ch % (D / 8);
+    float v[8] = {};
+    if (row < w.rows) {
+      const int g = w.row0 + row;
+      const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldq + (w.head * p.group + g % p.group) * p.a.ldqh + 8 * cc;
+      if (p.a.q_bf16) {
+        Chunk<__nv_bfloat16> x;
+        x.load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
+        x.get(v);
+      } else {
+        Chunk<float> x;
+        x.load(static_cast<const float*>(p.a.q) + at, false);
+        x.get(v);
+      }
+    }
+    if (p.c.rotated) quad_rotate(v, lane & 3);
+    float amax = lane_amax(v);
+#pragma unroll
+    for (int d = 1; d < D / 8; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
+    const int e = row_exponent(amax);
+    const float f = sign * pow2i(-e);  // the scale's sign goes to q: the scores' factors are positive
+    *reinterpret_cast<uint4*>(smem + C::kQ + (row >> 7) * 128 * D * 2 + (cc >> 3) * C::kPanel + (row & 127) * 128 + (((cc & 7) ^ (row & 7)) << 4)) =
+        make_uint4(pack_half(v[0] * f, v[1] * f), pack_half(v[2] * f, v[3] * f), pack_half(v[4] * f, v[5] * f), pack_half(v[6] * f, v[7] * f));
+    if (cc == 0) sm_f[row] = fabsf(p.a.scale) * 1.4426950408889634f * pow2i(e);
+  }
+  fence_async_smem();
+  __syncthreads();
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 12) {
+      if (p.delay > 0) {
+        const int64_t t0 = clock64();
+        while (clock64() - t0 < p.delay) {
+        }
+#pragma unroll
+        for (int i = 0; i < C::kRing; ++i) issue();
+      }
+      // warp 8, lanes 0-15: scale byte of the next tile's block lane % 8, K's and V's
+      const auto scale_of = [&](int tile) {
+        const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
+        const int pg = tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, nullptr) : -1;
+        return pg >= 0 ? static_cast<int>(p.c.scales[kv_scale_at(p.c, pg, w.head, (lane >> 3) & 1) + t % p.c.page / kKvTokens]) : -1;
+      };
+      int scale = warp == 8 ? scale_of(0) : -1;
+      int group = 0;
+      bool live = true;
+      for (int j = 0; live && j < n; ++j) {
+        const int buf = j % C::kBufs;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (j >= C::kBufs && !__all_sync(0xFFFFFFFFu, wait_bar(S, v ? &S.v_empty[buf] : &S.k_empty[buf], (j / C::kBufs - 1) & 1, p))) {
+            live = false;
+            break;
+          }
+          if (v == 0 && warp == 8) {
+            if (lane < 16) {
+              // a block without a page, or past the sequence: no weight (its codes are zeros)
+              const float s = kv_scale(scale);
+              if (lane < 8) {
+                sm_sc[j & 3][0][lane] = scale < 0 ? 0.0f : s;
+              } else {
+                sm_sc[j & 3][1][lane - 8] = scale < 0 ? kNegInf : scale == 255 ? s : static_cast<float>(scale - 127);
+                sm_sc[j & 3][2][lane - 8] = scale < 0 ? 0.0f : scale == 255 ? s : ex2(static_cast<float>(127 - scale));
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.sc_full[j & 3]);
+            scale = scale_of(j + 1);
+          }
+          uint8_t* const out = smem + (v ? C::kV : C::kK) + buf * C::kTile;
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g, ++group) {
+            cp_wait<C::kRing - 1>();
+            uint4 x[C::kGroup];
+#pragma unroll
+            for (int i = 0; i < C::kGroup; ++i)
+              x[i] = *reinterpret_cast<const uint4*>(smem + C::kRaw + (((group % C::kRing) * C::kGroup + i) * 128 + ctid) * 16);
+#pragma unroll
+            for (int i = 0; i < C::kGroup; ++i) {
+              const int piece = (g * C::kGroup + i) * 128 + ctid;
+              const int row = piece / (D / 16), cc = piece % (D / 16);
+              const uint32_t a = x[i].x ^ 0x80808080u, b = x[i].y ^ 0x80808080u, c = x[i].z ^ 0x80808080u, d = x[i].w ^ 0x80808080u;
+              const uint4 lo = make_uint4(codes_half2(a, 0x4140u), codes_half2(a, 0x4342u), codes_half2(b, 0x4140u), codes_half2(b, 0x4342u));
+              const uint4 hi = make_uint4(codes_half2(c, 0x4140u), codes_half2(c, 0x4342u), codes_half2(d, 0x4140u), codes_half2(d, 0x4342u));
+              uint8_t* const to = out + (cc >> 2) * C::kPanel + row * 128;
+              // the halves in an order that keeps eight neighbours on different banks
+              const int odd = (cc >> 2) & 1, at = 2 * (cc & 3);
+              *reinterpret_cast<uint4*>(to + (((at + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+              *reinterpret_cast<uint4*>(to + (((at + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+            }
+            issue();
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v ? &S.v_full[buf] : &S.k_full[buf]);
+        }
+      }
+      cp_wait<0>();
+    } else if (warp == 12) {
+      const auto qk = [&](int t, int s, int j) {  // row tile t, into S number s
+        const uint32_t q = sbase + C::kQ + t * 128 * D * 2, k = sbase + C::kK + (j % C::kBufs) * C::kTile;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            mma_f16(tmem + C::kS + s * 128, desc_k(q + (i >> 2) * C::kPanel + (i & 3) * 32), desc_k(k + (i >> 2) * C::kPanel + (i & 3) * 32),
+                    idesc_f16(kBK, false), i > 0);
+          mma_commit(&S.s_full[s]);
+        }
+        __syncwarp();
+      };
+      const auto pv = [&](int t, int s, int j, bool last) {
+        const uint32_t v = sbase + C::kV + (j % C::kBufs) * C::kTile;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < kBK / 16; ++i)
+            mma_ts(tmem + C::kO + t * D, tmem + C::kS + s * 128 + 8 * i, desc_mn(v + i * 2048, C::kPanel), idesc_f16(D, true), j > 0 || i > 0);
+          if (last) mma_commit(&S.v_empty[j % C::kBufs]);
+          mma_commit(&S.pv_done[t]);
+        }
+        __syncwarp();
+      };
+      const auto ready = [&](uint64_t* b, int phase) {
+        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(S, b, phase & 1, p));
+        tc_fence_after();
+        return ok;
+      };
+      const auto free_k = [&](int j) {
+        if (elect_one()) mma_commit(&S.k_empty[j % C::kBufs]);
+        __syncwarp();
+      };
+      bool live = true;
+      if constexpr (C::kTiles == 2) {
+        for (int j = 0; live && j <= n; ++j) {
+          if (j < n && !(live = ready(&S.k_full[j % C::kBufs], j / C::kBufs))) break;
+          for (int t = 0; t < qtiles; ++t) {
+            if (j > 0) {
+              if (t == 0 && !(live = ready(&S.v_full[(j - 1) % C::kBufs], (j - 1) / C::kBufs))) break;
+              if (!(live = ready(&S.p_ready[t], j - 1))) break;
+              pv(t, t, j - 1, t == qtiles - 1);
+            }
+            if (j < n) qk(t, t, j);
+          }
+          if (live && j < n) free_k(j);
+        }
+      } else {
+        if ((live = ready(&S.k_full[0], 0))) {
+          qk(0, 0, 0);
+          free_k(0);
+        }
+        for (int j = 0; live && j < n; ++j) {
+          if (j + 1 < n) {
+            if (!(live = ready(&S.k_full[(j + 1) % C::kBufs], (j + 1) / C::kBufs))) break;
+            qk(0, (j + 1) & 1, j + 1);
+            free_k(j + 1);
+          }
+          if (!(live = ready(&S.v_full[j % C::kBufs], j / C::kBufs)) || !(live = ready(&S.p_ready[j & 1], j >> 1))) break;
+          pv(0, j & 1, j, true);
+        }
+      }
+    }
+  } else if ((warp >> 2) < qtiles) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int t = warp >> 2, row = tid & (C::kRows - 1);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16), o_at = lanes + C::kO + t * D;
+    const float f = sm_f[row];
+    int lo, hi;
+    seen(p.a, w.q.len - w.q.n + (w.row0 + min(row, w.rows - 1)) / p.group, w.q.len, lo, hi);
+    int lo_all = lo, hi_all = hi;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      lo_all = max(lo_all, __shfl_xor_sync(0xFFFFFFFFu, lo_all, d));
+      hi_all = min(hi_all, __shfl_xor_sync(0xFFFFFFFFu, hi_all, d));
+    }
+    float m = kNegInf, l = 0.0f;
+    bool live = true;
+    for (int j = 0; j < n; ++j) {
+      const int s = C::kTiles == 2 ? t : j & 1, phase = C::kTiles == 2 ? j : j >> 1;
+      live = __all_sync(0xFFFFFFFFu, wait_bar(S, &S.s_full[s], phase & 1, p) && wait_bar(S, &S.sc_full[j & 3], (j >> 2) & 1, p));
+      if (!live) break;
+      tc_fence_after();
+      const uint32_t s_at = lanes + C::kS + s * 128;
+      uint32_t r[kBK];
+#pragma unroll
+      for (int c = 0; c < kBK; c += 32) tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+      float g[kBlocks], ev[kBlocks];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        g[b] = sm_sc[j & 3][0][b] * f;
+        ev[b] = sm_sc[j & 3][1][b];
+      }
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int c = 0; c < kBK; c += 16) tie16(r + c);
+      float (&x)[kBK] = *reinterpret_cast<float(*)[kBK]>(&r);
+      const int k0 = key0 + j * kBK;
+      const bool masked = k0 < lo_all || k0 + kBK > hi_all;
+      float top = kNegInf;
+      if (masked) {
+        const int a = lo - k0, e = hi - k0;
+#pragma unroll
+        for (int c = 0; c < kBK; ++c) {
+          const float y = fmaf(x[c], g[c >> 4], ev[c >> 4]);
+          x[c] = c >= a && c < e ? y : kNegInf;
+          top = fmaxf(top, x[c]);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          float y = fmaxf(x[16 * b], x[16 * b + 1]);
+#pragma unroll
+          for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
+          top = fmaxf(top, fmaf(y, g[b], ev[b]));
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, top > m + (kShift + kLag))) {
+        const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
+        m = next;
+        l *= c;
+        if (j > 0) {  // O so far: the product before this one is done
+          live = __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t], (j - 1) & 1, p));
+          if (!live) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + d, o);
+            tmem_wait32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+            tmem_st32(o_at + d, o);
+          }
+        }
+      }
+      const float z = m == kNegInf ? 0.0f : m;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        float2 sum = make_float2(0.0f, 0.0f);
+        const float gb = masked ? 1.0f : g[b], cb = masked ? -z : ev[b] - z;
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const float2 y = __ffma2_rn(make_float2(x[16 * b + c], x[16 * b + c + 1]), make_float2(gb, gb), make_float2(cb, cb));
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          sum = __fadd2_rn(sum, e);
+          r[8 * b + c / 2] = pack_half(e.x, e.y);
+        }
+        const float all = sum.x + sum.y;
+        l = all == 0.0f ? l : fmaf(all, sm_sc[j & 3][2][b], l);  // a NaN scale that the row does not see counts for nothing
+      }
+      tmem_st32(s_at, r);
+      tmem_st32(s_at + 32, r + 32);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_ready[s]);
+    }
+    if (live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t], (n - 1) & 1, p))) {
+      tc_fence_after();
+      const int g = w.row0 + row;
+      const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldo + (w.head * p.group + g % p.group) * p.a.ldoh;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float* const part = w.parts > 1 ? p.parts + static_cast<int64_t>(blockIdx.x) * C::kPart : nullptr;
+      if (part) {
+        part[C::kRows * D + row] = m;
+        part[C::kRows * (D + 1) + row] = l;
+      }
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + d, o);
+        tmem_wait32(o);
+        float (&v)[32] = *reinterpret_cast<float(*)[32]>(&o);
+        if (part) {
+          float4* const to = reinterpret_cast<float4*>(part + row * D + d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
+        if (p.c.rotated) rotate32(v);
+        if (row < w.rows) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            const float (&y)[8] = *reinterpret_cast<const float(*)[8]>(v + i);
+            if (p.a.o_bf16) store8(static_cast<__nv_bfloat16*>(p.a.out) + at + d + i, y, false);
+            else store8(static_cast<float*>(p.a.out) + at + d + i, y, false);
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (S.abort) {  // MMAs in flight read shared memory and write TMEM: wait out the bound
+    const int64_t t0 = clock64();
+    while (clock64() - t0 < kWaitCycles) {
+    }
+  }
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// The parts of cut tiles together, in the order of their keys.  grid (tiles x parts at most, shares of a
+// tile's rows): CTA (x, y) takes share y of the tile whose first part CTA x was.
+constexpr int kJoinThreads = 256, kJoinShares = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
+  using C = Shape<D>;
+  __shared__ int prefix[kKvMaxBatch + 1], carry[32];
+  grid_dep_launch();
+  grid_dep_wait();
+  Work w;
+  if (!find_work<D>(p, prefix, carry, kJoinThreads, static_cast<int>(blockIdx.x), w) || w.part > 0 || w.parts == 1) return;
+  const int total = prefix[p.s.batch];  // part i is CTA blockIdx.x + i * total's
+  constexpr int kShare = C::kRows / kJoinShares;
+  for (int ch = threadIdx.x; ch < kShare * D / 8; ch += kJoinThreads) {
+    const int row = blockIdx.y * kShare + ch / (D / 8), cc = ch % (D / 8);
+    if (blockIdx.y * kShare >= w.rows) return;
+    float top = kNegInf, l = 0.0f, v[8] = {};
+    const auto part = [&](int i) { return p.parts + (static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(i) * total) * C::kPart; };
+    const bool in = row < w.rows;
+    if (in) {
+      for (int i = 0; i < w.parts; ++i) top = fmaxf(top, part(i)[C::kRows * D + row]);
+#pragma unroll 4
+      for (int i = 0; i < w.parts; ++i) {
+        const float* const s = part(i);
+        const float m = s[C::kRows * D + row], x = s[C::kRows * (D + 1) + row];
+        const float4 y = *reinterpret_cast<const float4*>(s + row * D + 8 * cc), z = *reinterpret_cast<const float4*>(s + row * D + 8 * cc + 4);
+        const float f = m == kNegInf ? (x == x ? 0.0f : 1.0f) : ex2(m - top);
+        l += x * f;
+        v[0] += y.x * f; v[1] += y.y * f; v[2] += y.z * f; v[3] += y.w * f;
+        v[4] += z.x * f; v[5] += z.y * f; v[6] += z.z * f; v[7] += z.w * f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : v[i] / l;
+    if (p.c.rotated) quad_rotate(v, threadIdx.x & 3);
+    if (in) {
+      const int g = w.row0 + row;
+      const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldo + (w.head * p.group + g % p.group) * p.a.ldoh + 8 * cc;
+      if (p.a.o_bf16) store8(static_cast<__nv_bfloat16*>(p.a.out) + at, v, false);
+      else store8(static_cast<float*>(p.a.out) + at, v, false);
+    }
+  }
+}
+
+template <typename K>
+cudaError_t launch(K kernel, dim3 grid, int threads, int smem, const PromptArgs& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptArgs& p, int64_t most_tiles, cudaStream_t st) {
+  using C = Shape<D>;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(kv8_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  const int64_t grid = most_tiles > p.sms ? most_tiles : p.sms;
+  e = launch(kv8_prompt_kernel<D>, dim3(static_cast<unsigned>(p.parts ? grid : most_tiles)), kThreads, C::kSmem, p, st);
+  if (e != cudaSuccess || !p.parts) return e;
+  // cut tiles are at most half as many as the SMs
+  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(p.sms / 2 < grid ? p.sms / 2 : grid), kJoinShares), kJoinThreads, 0, p, st);
+}
+
+int64_t g_wait = kWaitCycles, g_delay = 0;
+
+}  // namespace
+
+void kv8_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
+  const auto cycles = [](uint64_t ns) { return static_cast<int64_t>(ns / 100 * 207 + ns % 100 * 207 / 100); };  // 2.07 GHz
+  g_wait = wait_ns ? cycles(wait_ns) : kWaitCycles;
+  g_delay = cycles(producer_delay_ns);
+}
+
+size_t kv8_prompt_workspace_bytes(int dim) {
+  const size_t part = dim == 64 ? Shape<64>::kPart : dim == 128 ? Shape<128>::kPart : Shape<256>::kPart;
+  return kWsCounters + static_cast<size_t>(num_sms()) * part * sizeof(float);
+}
+
+cudaError_t launch_kv8_prompt(const KvCache& c, const KvSeqs& s, const KvAttn& a, int least_rows, void* ws, cudaStream_t st) {
+  PromptArgs p{};
+  p.c = c;
+  p.s = s;
+  p.a = a;
+  p.group = a.q_heads / c.heads;
+  p.least_rows = least_rows;
+  p.sms = num_sms();
+  p.parts = ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounters) : nullptr;
+  p.err = device_error_word();
+  p.wait = g_wait;
+  p.delay = g_delay;
+  // row tiles at most: each sequence's last may be short
+  const int64_t rows = c.dim == 256 ? Shape<256>::kRows : Shape<128>::kRows;
+  const int64_t few = s.batch < s.tokens ? s.batch : s.tokens;
+  const int64_t most = c.heads * (s.cu ? static_cast<int64_t>(s.tokens) * p.group / rows + few
+                                       : s.batch * ((static_cast<int64_t>(s.each) * p.group + rows - 1) / rows));
+  switch (c.dim) {
+    case 64: return launch_prompt<64>(p, most, st);
+    case 128: return launch_prompt<128>(p, most, st);
+    default: return launch_prompt<256>(p, most, st);
+  }
+}
+
+}  // namespace w4a4

@@ -193,5 +193,10 @@ constexpr int kErrPage = 1 << 16;  // bit of the device error word: a page, leng
 constexpr int kKvMaxBatch = 2048;  // sequences of an attention call
 cudaError_t launch_kv8_attention(const KvCache& c, const KvSeqs& s, const KvAttn& a, void* ws, cudaStream_t st);
 size_t kv8_attention_workspace_bytes(int dim);
+// Its kernel for sequences of least_rows query rows and more (kv_prompt.cu).
+cudaError_t launch_kv8_prompt(const KvCache& c, const KvSeqs& s, const KvAttn& a, int least_rows, void* ws, cudaStream_t st);
+size_t kv8_prompt_workspace_bytes(int dim);
+// Test hook, as grp_set_wait_limit, of that kernel's waits.
+void kv8_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
 
 }  // namespace w4a4

@@ -708,9 +708,10 @@ w4a4_status w4a4_check(w4a4_stream_t stream);
 /*
  * w4a4_debug_set_wait_limit -- a test hook for the bounded waits.  Later launches
  * of the super-tile GEMM kernel (w4a4_gemm with the expanded activation operand,
- * and w4a4_gemm_id) and of mxfp4_gemm give up on a pipeline wait after wait_ns nanoseconds instead
+ * and w4a4_gemm_id), of mxfp4_gemm and of kv8_attention with more than 16 query rows a head
+ * give up on a pipeline wait after wait_ns nanoseconds instead
  * of one second, and their producer holds its first copy back for
- * producer_delay_ns (mxfp4_gemm counts both in SM cycles of the top clock, 2.07
+ * producer_delay_ns (mxfp4_gemm and kv8_attention count both in SM cycles of the top clock, 2.07
  * GHz: at a lower one they last longer).  With a delay longer than the limit every CTA gives up: the
  * kernel returns by itself, with its output incomplete, and w4a4_check reports
  * W4A4_ERR_TIMEOUT.  (0, 0) restores the defaults.  Not synchronised with other
