@@ -166,7 +166,7 @@ w4a4_status open_kv8(const w4a4_kv8* c, const w4a4_kv8_seqs* q, w4a4::KvCache* o
   if (((reinterpret_cast<uintptr_t>(q->table) | reinterpret_cast<uintptr_t>(q->lens) | reinterpret_cast<uintptr_t>(q->cu)) & 3) != 0)
     return fail(W4A4_ERR_ALIGNMENT, "%s: table, lens and cu must be 4-byte aligned", fn);
   if (!aligned16(c->codes)) return fail(W4A4_ERR_ALIGNMENT, "%s: the cache's codes must be 16-byte aligned", fn);
-  *oc = w4a4::KvCache{c->codes, c->scales, static_cast<int>(c->pages), c->heads, c->page, c->dim, (c->tag & W4A4_TAG_ROTATED) ? 1 : 0};
+  *oc = w4a4::KvCache{c->codes, c->scales, static_cast<int>(c->pages), c->heads, c->page, __builtin_ctz(c->page), c->dim, (c->tag & W4A4_TAG_ROTATED) ? 1 : 0};
   *oq = w4a4::KvSeqs{q->table, q->lens, q->cu, q->ldt, static_cast<int>(q->batch), static_cast<int>(q->width),
                      static_cast<int>(q->tokens), q->batch > 0 ? static_cast<int>(q->tokens / q->batch) : 0};
   return ok();

@@ -39,7 +39,7 @@ __device__ __forceinline__ Seq kv_seq(const KvSeqs& s, int b, int page, int* err
 
 // Page that holds token t of sequence b, or -1 where the table's entry is not one.
 __device__ __forceinline__ int kv_page(const KvSeqs& s, const KvCache& c, int b, int t, int* err) {
-  const int p = s.table[static_cast<int64_t>(b) * s.ldt + t / c.page];
+  const int p = s.table[static_cast<int64_t>(b) * s.ldt + (t >> c.page_log)];
   if (static_cast<unsigned>(p) < static_cast<unsigned>(c.pages)) return p;
   kv_flag(err);
   return -1;

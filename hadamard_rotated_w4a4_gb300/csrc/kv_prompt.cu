@@ -264,39 +264,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   const int key0 = w.key0 + w.t0 * kBK;
   const int qtiles = C::kTiles == 2 && w.rows > 128 ? 2 : 1;
 
-  // copies of codes: the thread's pieces of group g (K's groups of a tile, then V's), into ring slot g % kRing
+  // copies of codes: a tile is kGroups groups of K, then as many of V; group g of the order goes to ring slot
+  // g % kRing, each thread's pieces to places that it alone reads.  Lanes 0-7 hold where the tile's blocks of 16
+  // keys stand, for the tile to be copied next.
   const int ctid = tid - 256;
+  const int64_t v_off = static_cast<int64_t>(p.c.page) * D;
   const auto page_of = [&](int tile) {  // lanes 0-7: the page of the tile's block `lane`, -1: none
     const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
     return tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
   };
-  int pages = -1, pages_next = -1, issued = 0;  // pages of the tile to be copied next, and of the one after it
-  const auto issue = [&]() {
-    const int tile = issued / (2 * C::kGroups), in = issued % (2 * C::kGroups), v = in / C::kGroups;
-    if (tile < n) {
+  int64_t block_at = -1;
+  int page_next = -1, to_copy = 0;
+  const auto next_tile = [&]() {
+    const int t = key0 + to_copy * kBK + (lane & 7) * kKvTokens;
+    block_at = page_next < 0 ? -1 : kv_at(p.c, page_next, w.head, 0) + static_cast<int64_t>(t & (p.c.page - 1)) * D;
+    page_next = page_of(++to_copy);
+  };
+  const auto copy = [&](int in, int slot) {  // group `in` of the tile
+    const int v = in / C::kGroups, g = in % C::kGroups;
 #pragma unroll
-      for (int i = 0; i < C::kGroup; ++i) {
-        const int piece = ((in % C::kGroups) * C::kGroup + i) * 128 + ctid;
-        const int row = piece / (D / 16), cc = piece % (D / 16);
-        const int pg = __shfl_sync(0xFFFFFFFFu, pages, row / kKvTokens);
-        const int at = (key0 + tile * kBK + row) % p.c.page;
-        const int8_t* const src = p.c.codes + (pg >= 0 ? kv_at(p.c, pg, w.head, v) + static_cast<int64_t>(at) * D + 16 * cc : 0);
-        cp_async16(sbase + C::kRaw + (((issued % C::kRing) * C::kGroup + i) * 128 + ctid) * 16, src, pg >= 0);
-      }
-      if (in == 2 * C::kGroups - 1) {
-        pages = pages_next;
-        pages_next = page_of(tile + 2);
-      }
+    for (int i = 0; i < C::kGroup; ++i) {
+      const int piece = (g * C::kGroup + i) * 128 + ctid, row = piece / (D / 16), cc = piece % (D / 16);
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, block_at, row / kKvTokens);
+      const int8_t* const src = p.c.codes + (at >= 0 ? at + (v ? v_off : 0) + (row % kKvTokens) * D + 16 * cc : 0);
+      cp_async16(sbase + C::kRaw + ((slot * C::kGroup + i) * 128 + ctid) * 16, src, at >= 0);
     }
     cp_commit();
-    ++issued;
+  };
+  constexpr int kIn = 2 * C::kGroups;  // groups of a tile: 2, 4 or 8
+  const auto first_copies = [&]() {
+#pragma unroll
+    for (int i = 0; i < C::kRing; ++i) {
+      if (i % kIn == 0) next_tile();
+      copy(i % kIn, i);
+    }
   };
   if (warp >= 8 && warp < 12) {
-    pages = page_of(0);
-    pages_next = page_of(1);
-    if (p.delay == 0)
-#pragma unroll
-      for (int i = 0; i < C::kRing; ++i) issue();
+    page_next = page_of(0);
+    if (p.delay == 0) first_copies();
   }
 
   // q: rotated as the keys are, scaled by a power of two per row, in the swizzle
@@ -337,17 +342,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         const int64_t t0 = clock64();
         while (clock64() - t0 < p.delay) {
         }
-#pragma unroll
-        for (int i = 0; i < C::kRing; ++i) issue();
+        first_copies();
       }
       // warp 8, lanes 0-15: scale byte of the next tile's block lane % 8, K's and V's
       const auto scale_of = [&](int tile) {
         const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
         const int pg = tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, nullptr) : -1;
-        return pg >= 0 ? static_cast<int>(p.c.scales[kv_scale_at(p.c, pg, w.head, (lane >> 3) & 1) + t % p.c.page / kKvTokens]) : -1;
+        return pg >= 0 ? static_cast<int>(p.c.scales[kv_scale_at(p.c, pg, w.head, (lane >> 3) & 1) + (t & (p.c.page - 1)) / kKvTokens]) : -1;
       };
       int scale = warp == 8 ? scale_of(0) : -1;
-      int group = 0;
       bool live = true;
       for (int j = 0; live && j < n; ++j) {
         const int buf = j % C::kBufs;
@@ -374,12 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
           }
           uint8_t* const out = smem + (v ? C::kV : C::kK) + buf * C::kTile;
 #pragma unroll
-          for (int g = 0; g < C::kGroups; ++g, ++group) {
+          for (int g = 0; g < C::kGroups; ++g) {
+            const int in = v * C::kGroups + g, slot = kIn == 2 ? 2 * (j & 1) + in : in % C::kRing;
             cp_wait<C::kRing - 1>();
             uint4 x[C::kGroup];
 #pragma unroll
             for (int i = 0; i < C::kGroup; ++i)
-              x[i] = *reinterpret_cast<const uint4*>(smem + C::kRaw + (((group % C::kRing) * C::kGroup + i) * 128 + ctid) * 16);
+              x[i] = *reinterpret_cast<const uint4*>(smem + C::kRaw + ((slot * C::kGroup + i) * 128 + ctid) * 16);
 #pragma unroll
             for (int i = 0; i < C::kGroup; ++i) {
               const int piece = (g * C::kGroup + i) * 128 + ctid;
@@ -393,7 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
               *reinterpret_cast<uint4*>(to + (((at + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(to + (((at + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
             }
-            issue();
+            // the group kRing further on, into this one's place
+            if (in == (kIn == 8 ? 4 : 0)) next_tile();
+            copy(kIn == 8 ? (in + 4) % 8 : in, slot);
           }
           fence_async_smem();
           __syncwarp();

@@ -161,7 +161,7 @@ void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
 struct KvCache {
   int8_t* codes;    // [pages][heads][2][page][dim]
   uint8_t* scales;  // [pages][heads][2][page / 16]
-  int pages, heads, page, dim, rotated;
+  int pages, heads, page, page_log, dim, rotated;  // page = 2^page_log
 };
 // The sequences of a call: cu null = `each` tokens of every sequence.
 struct KvSeqs {
