@@ -8,13 +8,13 @@
 // one a row and key; and the way from codes to fp16.
 //
 // Warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread, so that no maximum crosses
-// lanes; 8-11 the codes: copied (cp.async) to a ring that each thread alone reads, converted, and
-// written as both products' B operand: keys are rows of 128 bytes in the 128-byte swizzle either
-// way, K read along d (K-major), V along the keys (MN-major); 12 issues the MMAs.  The two row
-// tiles take turns: while one's weights are computed the other's products run.  With heads of
-// 256 TMEM has room for one row tile with two S, and the next tile's S runs beside the softmax.
+// lanes; 8 issues the MMAs; 9-15 take blocks of 16 keys or values in turn, load their codes ahead
+// into registers and write them as the products' B operands: keys are rows of 128 bytes in the
+// 128-byte swizzle either way, K read along d (K-major), V along the keys (MN-major).  The two
+// row tiles take turns: while one's weights are computed the other's products run.  With heads
+// of 256 TMEM has room for one row tile with two S, and the next tile's S runs beside the softmax.
 //
-// O is rescaled only when a row's maximum grew by more than 2^8: the weights then still fit fp16.
+// The running maximum is looked for, and O rescaled, only where a weight might not fit fp16.
 #include <cuda_bf16.h>
 
 #include "kv_attention.cuh"
@@ -28,9 +28,14 @@ constexpr int kThreads = 512;
 constexpr int kBK = 128;                         // keys of a tile
 constexpr int kBlocks = kBK / kKvTokens;         // blocks of 16 keys, each with its scales
 constexpr int64_t kWaitCycles = int64_t(1) << 31;  // 1.04 s at the top clock, longer below it
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 256 threads each; together the launch's 512 x 128
-static_assert(kSoftmaxRegs + kOtherRegs <= 2 * 128);
 constexpr size_t kWsCounters = size_t(1) << 20;
+constexpr float kMost = 32768.0f;  // of 16 weights together, below fp16's largest
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 template <int D>
 struct Shape {
@@ -39,12 +44,14 @@ struct Shape {
   static constexpr int kBufs = D == 256 ? 1 : 2;    // converted tiles of K, and of V
   static constexpr int kTile = kBK * D * 2;         // bytes of one
   static constexpr int kPanel = 128 * 128;          // bytes of 64 elements of 128 rows
-  static constexpr int kQ = 0, kK = kQ + kRows * D * 2, kV = kK + kBufs * kTile, kRaw = kV + kBufs * kTile;
-  static constexpr int kChunks = kBK * D / 16 / 128;  // 16-code pieces of a thread in a tile of K
-  static constexpr int kGroup = 4, kRing = 4;         // pieces of a copy group; groups in flight
-  static constexpr int kGroups = kChunks / kGroup;    // groups of a tile of K
+  static constexpr int kQ = 0, kK = kQ + kRows * D * 2, kV = kK + kBufs * kTile;
+  static constexpr int kPieces = D / 32;              // 16-code pieces of a lane in a block of 16 keys
   static constexpr int kPrefix = kK;  // find_work's sums, before the first tile of K
-  static constexpr int kSmem = 1024 + kRaw + kRing * kGroup * 128 * 16;
+  static constexpr int kSmem = 1024 + kV + kBufs * kTile;
+  // registers a thread: warps 0-3, 4-7 (which heads of 256 leave idle), 8-11 and 12-15;
+  // together no more than the launch's 4 x 128
+  static constexpr int kRegs0 = 176, kRegs1 = D == 256 ? 24 : 176, kRegs2 = D == 256 ? 152 : 80;
+  static_assert(kRegs0 + kRegs1 + 2 * kRegs2 <= 4 * 128);
   static constexpr int kS = 0, kO = 256;            // TMEM columns
   static constexpr int kPart = kRows * (D + 2);     // floats of a cut tile's part
   static_assert(kSmem <= 227 * 1024 - 2 * 1024 && kO + kTiles * D <= 512 && 4 * (kKvMaxBatch + 1) <= kBufs * kTile);
@@ -63,15 +70,23 @@ struct PromptArgs {
 };
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], pv_done[2], sc_full[4];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], sc_full[4];
+  uint64_t p_ready[2][2];  // [S][half of the keys]
+  uint64_t pv_done[2][2];  // [row tile][half]
+  uint64_t o_done[2];      // once, at the end
   uint32_t tmem;
   volatile int abort;
 };
 
+// Bounded wait; on giving up, every other wait of the CTA gives up too.  The clock is read every 64 tries: sixteen
+// warps wait about half of the time, and what they do meanwhile takes issue slots from the others.
 __device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, const PromptArgs& p) {
   if (mbar_try(b, parity)) return true;
   const int64_t t0 = clock64();
-  while (!mbar_try(b, parity)) {
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try(b, parity)) return true;
     if (S.abort) return false;
     if (clock64() - t0 > p.wait) {
       S.abort = 1;
@@ -79,7 +94,6 @@ __device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, 
       return false;
     }
   }
-  return true;
 }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -88,15 +102,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Operand descriptors in the 128-byte swizzle (layout type 2): K-major, 8-row groups 1024 bytes
 // apart; MN-major, groups of 8 keys 1024 bytes apart and 64-element panels `panel` bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t smem) {
@@ -217,6 +222,88 @@ __device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int*
   return w.part < w.parts;
 }
 
+// Blocks of 16 keys of tiles 0 .. n - 1, in the order of the tiles, K's eight and then V's, of which warp `first` of
+// `kWarps` takes every kWarps-th: codes to fp16 in the swizzled rows of the tile's buffer, and with K's the block's
+// scales.  A lane takes 16 codes of rows lane / 4 and lane / 4 + 8 in every panel of 64: eight neighbours read 64 bytes
+// of two rows each, write on different banks, and find the swizzle's share of an address in a register.
+constexpr int kConvertWarps = 7;
+template <int D>
+__device__ __forceinline__ void convert(const PromptArgs& p, const Work& w, int key0, int n, int first, uint8_t* smem, Bars& S,
+                                        float (&sc)[4][3][kBlocks]) {
+  using C = Shape<D>;
+  const int lane = threadIdx.x & 31, units = n * 2 * kBlocks;
+  const uint32_t k0 = su32(smem + C::kK) + (lane >> 2) * 128;
+  const uint32_t lo = k0 + (((2 * (lane & 3)) ^ (lane >> 2)) << 4), hi = k0 + (((2 * (lane & 3) + 1) ^ (lane >> 2)) << 4);
+  const int64_t v_off = static_cast<int64_t>(p.c.page) * D;
+  const auto page_of = [&](int u) {  // of unit u, -1: none
+    const int t = key0 + (u >> 4) * kBK + (u & 7) * kKvTokens;
+    return u < units && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
+  };
+  struct Unit {
+    uint4 x[C::kPieces];
+    int scale;  // lane 0: K's byte, lane 1: V's; -1: no page
+  };
+  const auto load = [&](int u, int page, Unit& o) {
+    const int t = key0 + (u >> 4) * kBK + (u & 7) * kKvTokens, v = (u >> 3) & 1, at = t & (p.c.page - 1);
+    o.scale = -1;
+    if (page >= 0) {
+      const int8_t* const src = p.c.codes + kv_at(p.c, page, w.head, 0) + (v ? v_off : 0) + static_cast<int64_t>(at + (lane >> 2)) * D + 16 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < C::kPieces; ++i) o.x[i] = __ldg(reinterpret_cast<const uint4*>(src + (i & 1) * 8 * D + (i >> 1) * 64));
+      if (!v && lane < 2) o.scale = p.c.scales[kv_scale_at(p.c, page, w.head, lane) + at / kKvTokens];
+    } else {
+#pragma unroll
+      for (int i = 0; i < C::kPieces; ++i) o.x[i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  const auto store = [&](int u, const Unit& o) {
+    const int j = u >> 4, v = (u >> 3) & 1, b = u & 7, buf = j % C::kBufs;
+    if (j >= C::kBufs && !__all_sync(0xFFFFFFFFu, wait_bar(S, v ? &S.v_empty[buf] : &S.k_empty[buf], (j / C::kBufs - 1) & 1, p))) return false;
+    if (!v) {
+      // a block without a page, or past the sequence: no weight (its codes are zeros)
+      const float f = kv_scale(o.scale);
+      if (lane == 0) sc[j & 3][0][b] = o.scale < 0 ? 0.0f : f;
+      if (lane == 1) {
+        sc[j & 3][1][b] = o.scale < 0 ? kNegInf : o.scale == 255 ? f : static_cast<float>(o.scale - 127);
+        sc[j & 3][2][b] = o.scale < 0 ? 0.0f : o.scale == 255 ? f : ex2(static_cast<float>(127 - o.scale));
+      }
+    }
+    const uint32_t at = (v ? C::kV - C::kK : 0) + buf * C::kTile + b * kKvTokens * 128;
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) {
+      const uint32_t a = o.x[i].x ^ 0x80808080u, b4 = o.x[i].y ^ 0x80808080u, c = o.x[i].z ^ 0x80808080u, d = o.x[i].w ^ 0x80808080u;
+      const uint32_t to = at + (i & 1) * 1024 + (i >> 1) * C::kPanel;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(lo + to), "r"(codes_half2(a, 0x4140u)), "r"(codes_half2(a, 0x4342u)),
+                   "r"(codes_half2(b4, 0x4140u)), "r"(codes_half2(b4, 0x4342u))
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(hi + to), "r"(codes_half2(c, 0x4140u)), "r"(codes_half2(c, 0x4342u)),
+                   "r"(codes_half2(d, 0x4140u)), "r"(codes_half2(d, 0x4342u))
+                   : "memory");
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(v ? &S.v_full[buf] : &S.k_full[buf]);
+      if (!v) mbar_arrive(&S.sc_full[j & 3]);
+    }
+    return true;
+  };
+  Unit a, b;
+  int u = first, page = page_of(u + kConvertWarps);
+  load(u, page_of(u), a);
+  while (u < units) {
+    load(u + kConvertWarps, page, b);
+    page = page_of(u + 2 * kConvertWarps);
+    if (!store(u, a)) return;
+    u += kConvertWarps;
+    if (u >= units) return;
+    load(u + kConvertWarps, page, a);
+    page = page_of(u + 2 * kConvertWarps);
+    if (!store(u, b)) return;
+    u += kConvertWarps;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_constant__ PromptArgs p) {
   using C = Shape<D>;
@@ -231,19 +318,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.k_full[i], kBlocks);
       mbar_init(&S.k_empty[i], 1);
-      mbar_init(&S.v_full[i], 4);
+      mbar_init(&S.v_full[i], kBlocks);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_ready[i], 4);
-      mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.p_ready[i][0], 4);
+      mbar_init(&S.p_ready[i][1], 4);
+      mbar_init(&S.pv_done[i][0], 1);
+      mbar_init(&S.pv_done[i][1], 1);
+      mbar_init(&S.o_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], kBlocks);
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&S.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
@@ -257,52 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), w);
   if (!some) {
     __syncthreads();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
   }
   const int n = w.t1 - w.t0;
   const int key0 = w.key0 + w.t0 * kBK;
   const int qtiles = C::kTiles == 2 && w.rows > 128 ? 2 : 1;
-
-  // copies of codes: a tile is kGroups groups of K, then as many of V; group g of the order goes to ring slot
-  // g % kRing, each thread's pieces to places that it alone reads.  Lanes 0-7 hold where the tile's blocks of 16
-  // keys stand, for the tile to be copied next.
-  const int ctid = tid - 256;
-  const int64_t v_off = static_cast<int64_t>(p.c.page) * D;
-  const auto page_of = [&](int tile) {  // lanes 0-7: the page of the tile's block `lane`, -1: none
-    const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
-    return tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
-  };
-  int64_t block_at = -1;
-  int page_next = -1, to_copy = 0;
-  const auto next_tile = [&]() {
-    const int t = key0 + to_copy * kBK + (lane & 7) * kKvTokens;
-    block_at = page_next < 0 ? -1 : kv_at(p.c, page_next, w.head, 0) + static_cast<int64_t>(t & (p.c.page - 1)) * D;
-    page_next = page_of(++to_copy);
-  };
-  const auto copy = [&](int in, int slot) {  // group `in` of the tile
-    const int v = in / C::kGroups, g = in % C::kGroups;
-#pragma unroll
-    for (int i = 0; i < C::kGroup; ++i) {
-      const int piece = (g * C::kGroup + i) * 128 + ctid, row = piece / (D / 16), cc = piece % (D / 16);
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, block_at, row / kKvTokens);
-      const int8_t* const src = p.c.codes + (at >= 0 ? at + (v ? v_off : 0) + (row % kKvTokens) * D + 16 * cc : 0);
-      cp_async16(sbase + C::kRaw + ((slot * C::kGroup + i) * 128 + ctid) * 16, src, at >= 0);
-    }
-    cp_commit();
-  };
-  constexpr int kIn = 2 * C::kGroups;  // groups of a tile: 2, 4 or 8
-  const auto first_copies = [&]() {
-#pragma unroll
-    for (int i = 0; i < C::kRing; ++i) {
-      if (i % kIn == 0) next_tile();
-      copy(i % kIn, i);
-    }
-  };
-  if (warp >= 8 && warp < 12) {
-    page_next = page_of(0);
-    if (p.delay == 0) first_copies();
-  }
 
   // q: rotated as the keys are, scaled by a power of two per row, in the swizzle
   const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
@@ -336,78 +386,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   __syncthreads();
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 12) {
-      if (p.delay > 0) {
-        const int64_t t0 = clock64();
-        while (clock64() - t0 < p.delay) {
-        }
-        first_copies();
+    if constexpr (C::kRegs2 < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegs2));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs2));
+    if (p.delay > 0 && warp != 8) {
+      const int64_t t0 = clock64();
+      while (clock64() - t0 < p.delay) {
       }
-      // warp 8, lanes 0-15: scale byte of the next tile's block lane % 8, K's and V's
-      const auto scale_of = [&](int tile) {
-        const int t = key0 + tile * kBK + (lane & 7) * kKvTokens;
-        const int pg = tile < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, nullptr) : -1;
-        return pg >= 0 ? static_cast<int>(p.c.scales[kv_scale_at(p.c, pg, w.head, (lane >> 3) & 1) + (t & (p.c.page - 1)) / kKvTokens]) : -1;
-      };
-      int scale = warp == 8 ? scale_of(0) : -1;
-      bool live = true;
-      for (int j = 0; live && j < n; ++j) {
-        const int buf = j % C::kBufs;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          if (j >= C::kBufs && !__all_sync(0xFFFFFFFFu, wait_bar(S, v ? &S.v_empty[buf] : &S.k_empty[buf], (j / C::kBufs - 1) & 1, p))) {
-            live = false;
-            break;
-          }
-          if (v == 0 && warp == 8) {
-            if (lane < 16) {
-              // a block without a page, or past the sequence: no weight (its codes are zeros)
-              const float s = kv_scale(scale);
-              if (lane < 8) {
-                sm_sc[j & 3][0][lane] = scale < 0 ? 0.0f : s;
-              } else {
-                sm_sc[j & 3][1][lane - 8] = scale < 0 ? kNegInf : scale == 255 ? s : static_cast<float>(scale - 127);
-                sm_sc[j & 3][2][lane - 8] = scale < 0 ? 0.0f : scale == 255 ? s : ex2(static_cast<float>(127 - scale));
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.sc_full[j & 3]);
-            scale = scale_of(j + 1);
-          }
-          uint8_t* const out = smem + (v ? C::kV : C::kK) + buf * C::kTile;
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const int in = v * C::kGroups + g, slot = kIn == 2 ? 2 * (j & 1) + in : in % C::kRing;
-            cp_wait<C::kRing - 1>();
-            uint4 x[C::kGroup];
-#pragma unroll
-            for (int i = 0; i < C::kGroup; ++i)
-              x[i] = *reinterpret_cast<const uint4*>(smem + C::kRaw + ((slot * C::kGroup + i) * 128 + ctid) * 16);
-#pragma unroll
-            for (int i = 0; i < C::kGroup; ++i) {
-              const int piece = (g * C::kGroup + i) * 128 + ctid;
-              const int row = piece / (D / 16), cc = piece % (D / 16);
-              const uint32_t a = x[i].x ^ 0x80808080u, b = x[i].y ^ 0x80808080u, c = x[i].z ^ 0x80808080u, d = x[i].w ^ 0x80808080u;
-              const uint4 lo = make_uint4(codes_half2(a, 0x4140u), codes_half2(a, 0x4342u), codes_half2(b, 0x4140u), codes_half2(b, 0x4342u));
-              const uint4 hi = make_uint4(codes_half2(c, 0x4140u), codes_half2(c, 0x4342u), codes_half2(d, 0x4140u), codes_half2(d, 0x4342u));
-              uint8_t* const to = out + (cc >> 2) * C::kPanel + row * 128;
-              // the halves in an order that keeps eight neighbours on different banks
-              const int odd = (cc >> 2) & 1, at = 2 * (cc & 3);
-              *reinterpret_cast<uint4*>(to + (((at + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-              *reinterpret_cast<uint4*>(to + (((at + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
-            }
-            // the group kRing further on, into this one's place
-            if (in == (kIn == 8 ? 4 : 0)) next_tile();
-            copy(kIn == 8 ? (in + 4) % 8 : in, slot);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v ? &S.v_full[buf] : &S.k_full[buf]);
-        }
-      }
-      cp_wait<0>();
-    } else if (warp == 12) {
+    }
+    if (warp > 8) {
+      convert<D>(p, w, key0, n, warp - 9, smem, S, sm_sc);
+    } else {
       const auto qk = [&](int t, int s, int j) {  // row tile t, into S number s
         const uint32_t q = sbase + C::kQ + t * 128 * D * 2, k = sbase + C::kK + (j % C::kBufs) * C::kTile;
         if (elect_one()) {
@@ -419,14 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         }
         __syncwarp();
       };
-      const auto pv = [&](int t, int s, int j, bool last) {
+      // half h of the tile's keys
+      const auto pv = [&](int t, int s, int j, int h, bool last) {
         const uint32_t v = sbase + C::kV + (j % C::kBufs) * C::kTile;
         if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i)
-            mma_ts(tmem + C::kO + t * D, tmem + C::kS + s * 128 + 8 * i, desc_mn(v + i * 2048, C::kPanel), idesc_f16(D, true), j > 0 || i > 0);
+          for (int i = 0; i < kBK / 32; ++i)
+            mma_ts(tmem + C::kO + t * D, tmem + C::kS + s * 128 + 32 * h + 8 * i, desc_mn(v + 8192 * h + i * 2048, C::kPanel), idesc_f16(D, true),
+                   j > 0 || h > 0 || i > 0);
           if (last) mma_commit(&S.v_empty[j % C::kBufs]);
-          mma_commit(&S.pv_done[t]);
+          mma_commit(&S.pv_done[t][h]);
+          if (j == n - 1 && h == 1) mma_commit(&S.o_done[t]);
         }
         __syncwarp();
       };
@@ -446,8 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
           for (int t = 0; t < qtiles; ++t) {
             if (j > 0) {
               if (t == 0 && !(live = ready(&S.v_full[(j - 1) % C::kBufs], (j - 1) / C::kBufs))) break;
-              if (!(live = ready(&S.p_ready[t], j - 1))) break;
-              pv(t, t, j - 1, t == qtiles - 1);
+              if (!(live = ready(&S.p_ready[t][0], j - 1))) break;
+              pv(t, t, j - 1, 0, false);
+              if (!(live = ready(&S.p_ready[t][1], j - 1))) break;
+              pv(t, t, j - 1, 1, t == qtiles - 1);
             }
             if (j < n) qk(t, t, j);
           }
@@ -464,13 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
             qk(0, (j + 1) & 1, j + 1);
             free_k(j + 1);
           }
-          if (!(live = ready(&S.v_full[j % C::kBufs], j / C::kBufs)) || !(live = ready(&S.p_ready[j & 1], j >> 1))) break;
-          pv(0, j & 1, j, true);
+          if (!(live = ready(&S.v_full[j % C::kBufs], j / C::kBufs))) break;
+          for (int h = 0; h < 2; ++h) {
+            if (!(live = ready(&S.p_ready[j & 1][h], j >> 1))) break;
+            pv(0, j & 1, j, h, h == 1);
+          }
         }
       }
     }
   } else if ((warp >> 2) < qtiles) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs0));
     const int t = warp >> 2, row = tid & (C::kRows - 1);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16), o_at = lanes + C::kO + t * D;
     const float f = sm_f[row];
@@ -482,89 +478,113 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       lo_all = max(lo_all, __shfl_xor_sync(0xFFFFFFFFu, lo_all, d));
       hi_all = min(hi_all, __shfl_xor_sync(0xFFFFFFFFu, hi_all, d));
     }
+    constexpr int kHalf = kBK / 2, kHB = kBlocks / 2;
+    // scores to the exponents of their weights, -infinity where the row does not see the key
+    const auto mask = [&](float (&x)[kHalf], const float* sc, int key) {
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) {
+        const float y = fmaf(x[c], sc[c >> 4] * f, sc[kBlocks + (c >> 4)]);
+        x[c] = key + c >= lo && key + c < hi ? y : kNegInf;
+      }
+    };
+    // 16 weights 2^(x g + c), as fp16, and their sum
+    const auto weights = [&](const float* x, float g, float c, uint32_t* o) {
+      float2 all = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float2 a = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(g, g), make_float2(c, c));
+        const float2 e = make_float2(ex2(a.x), ex2(a.y));
+        all = i == 0 ? e : __fadd2_rn(all, e);
+        o[i / 2] = pack_half(e.x, e.y);
+      }
+      return all.x + all.y;
+    };
     float m = kNegInf, l = 0.0f;
     bool live = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; live && j < n; ++j) {
       const int s = C::kTiles == 2 ? t : j & 1, phase = C::kTiles == 2 ? j : j >> 1;
       live = __all_sync(0xFFFFFFFFu, wait_bar(S, &S.s_full[s], phase & 1, p) && wait_bar(S, &S.sc_full[j & 3], (j >> 2) & 1, p));
       if (!live) break;
       tc_fence_after();
       const uint32_t s_at = lanes + C::kS + s * 128;
-      uint32_t r[kBK];
-#pragma unroll
-      for (int c = 0; c < kBK; c += 32) tmem_ld32(s_at + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
-      float g[kBlocks], ev[kBlocks];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        g[b] = sm_sc[j & 3][0][b] * f;
-        ev[b] = sm_sc[j & 3][1][b];
-      }
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-      for (int c = 0; c < kBK; c += 16) tie16(r + c);
-      float (&x)[kBK] = *reinterpret_cast<float(*)[kBK]>(&r);
       const int k0 = key0 + j * kBK;
-      const bool masked = k0 < lo_all || k0 + kBK > hi_all;
-      float top = kNegInf;
-      if (masked) {
-        const int a = lo - k0, e = hi - k0;
-#pragma unroll
-        for (int c = 0; c < kBK; ++c) {
-          const float y = fmaf(x[c], g[c >> 4], ev[c >> 4]);
-          x[c] = c >= a && c < e ? y : kNegInf;
-          top = fmaxf(top, x[c]);
-        }
-      } else {
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          float y = fmaxf(x[16 * b], x[16 * b + 1]);
-#pragma unroll
-          for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
-          top = fmaxf(top, fmaf(y, g[b], ev[b]));
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, top > m + (kShift + kLag))) {
-        const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
-        m = next;
-        l *= c;
-        if (j > 0) {  // O so far: the product before this one is done
-          live = __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t], (j - 1) & 1, p));
-          if (!live) break;
-          tc_fence_after();
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_at + d, o);
-            tmem_wait32(o);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[kHalf];
+        tmem_ld32(s_at + h * kHalf, *reinterpret_cast<uint32_t(*)[32]>(r));
+        tmem_ld32(s_at + h * kHalf + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-            tmem_st32(o_at + d, o);
+        for (int c = 0; c < kHalf; c += 16) tie16(r + c);
+        const bool masked = k0 + h * kHalf < lo_all || k0 + (h + 1) * kHalf > hi_all;
+        // Weights against the maximum so far.  None is negative, so that sums of 16 of at most kMost say that each fits
+        // fp16: the maximum itself is looked for, and O and the sums rescaled, only where a sum does not.
+        float (&x)[kHalf] = *reinterpret_cast<float(*)[kHalf]>(&r);
+        const float* const sc = &sm_sc[j & 3][0][h * kHB];  // scales of K; exponents and back factors of V behind them
+        if (masked) mask(x, sc, k0 + h * kHalf);
+        bool sure = false;
+        while (true) {
+          const float z = m == kNegInf ? 0.0f : m;
+          float sum = 0.0f, most = 0.0f;
+          uint32_t w2[kHalf / 2];
+          if (!masked) {
+#pragma unroll
+            for (int b = 0; b < kHB; ++b) {
+              const float all = weights(x + 16 * b, sc[b] * f, sc[kBlocks + b] - z, w2 + 8 * b);
+              most = max_nan(most, all);
+              sum = fmaf(all, sc[2 * kBlocks + b], sum);
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < kHB; ++b) {
+              const float all = weights(x + 16 * b, 1.0f, -z, w2 + 8 * b);
+              most = max_nan(most, all);
+              if (all != 0.0f) sum = fmaf(all, sc[2 * kBlocks + b], sum);  // a NaN scale that the row does not see counts for nothing
+            }
+          }
+          if (sure || !__any_sync(0xFFFFFFFFu, !(most <= kMost) || m == kNegInf)) {
+            l += sum;
+            tmem_st32(s_at + h * (kHalf / 2), w2);
+            break;
+          }
+          sure = true;
+          float top = kNegInf;
+#pragma unroll
+          for (int b = 0; b < kHB; ++b) {
+            float y = fmaxf(x[16 * b], x[16 * b + 1]);
+#pragma unroll
+            for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
+            top = fmaxf(top, masked ? y : fmaf(y, sc[b] * f, sc[kBlocks + b]));
+          }
+          const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
+          m = next;
+          l *= c;
+          if (j + h > 0) {
+            // O so far: the product before this one has to be done.  The product of the tile before that one is (this
+            // tile's S came behind it), so that a phase's parity tells which of the two is meant.
+            live = (j == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][1], (j - 1) & 1, p))) &&
+                   (h == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][0], j & 1, p)));
+            if (!live) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + d, o);
+              tmem_wait32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+              tmem_st32(o_at + d, o);
+            }
           }
         }
+        if (!live) break;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_ready[s][h]);
       }
-      const float z = m == kNegInf ? 0.0f : m;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        float2 sum = make_float2(0.0f, 0.0f);
-        const float gb = masked ? 1.0f : g[b], cb = masked ? -z : ev[b] - z;
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float2 y = __ffma2_rn(make_float2(x[16 * b + c], x[16 * b + c + 1]), make_float2(gb, gb), make_float2(cb, cb));
-          const float2 e = make_float2(ex2(y.x), ex2(y.y));
-          sum = __fadd2_rn(sum, e);
-          r[8 * b + c / 2] = pack_half(e.x, e.y);
-        }
-        const float all = sum.x + sum.y;
-        l = all == 0.0f ? l : fmaf(all, sm_sc[j & 3][2][b], l);  // a NaN scale that the row does not see counts for nothing
-      }
-      tmem_st32(s_at, r);
-      tmem_st32(s_at + 32, r + 32);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_ready[s]);
     }
-    if (live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t], (n - 1) & 1, p))) {
+    if (live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.o_done[t], 0, p))) {
       tc_fence_after();
       const int g = w.row0 + row;
       const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldo + (w.head * p.group + g % p.group) * p.a.ldoh;
@@ -600,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if constexpr (C::kRegs1 < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegs1));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs1));
   }
   tc_fence_before();
   __syncthreads();
@@ -609,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
     while (clock64() - t0 < kWaitCycles) {
     }
   }
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // The parts of cut tiles together, in the order of their keys.  grid (tiles x parts at most, shares of a
