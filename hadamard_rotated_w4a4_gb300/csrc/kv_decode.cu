@@ -2,17 +2,19 @@
 // batches, the stream of the cache's codes.
 //
 // A tile is a sequence's head of K and V with up to 16 query rows (tokens x the heads that
-// share it).  Its keys are cut in units of 128 and the units of all tiles dealt evenly to one
-// CTA per SM, so that sequences of any lengths fill the GPU; a tile cut between CTAs is
+// share it).  Its keys are cut in units of 128 and the units of all tiles dealt evenly to two
+// CTAs per SM, so that sequences of any lengths fill the GPU; a tile cut between CTAs is
 // joined by the last of them to arrive, its parts added in the order of their CTAs: equal
 // inputs give equal bits.
 //
-// In a CTA each warp takes blocks of 16 keys by itself, with its own running maximum and sum:
-// no barrier until the tile's end.  A lane copies (cp.async) just the 16-byte pieces that its
-// own fragments need, into a ring that only it reads.  That works without a transposition
-// because the order of a contraction is free: for Q K^T, lane (r, c) = (lane / 4, lane % 4)
-// takes 16 consecutive elements 64 j + 16 c of key r, and Q is read in the same order; for
-// P V, it takes elements 16 r .. of the four keys whose weights its accumulators hold.
+// In a CTA each warp takes blocks of 16 keys by itself, with its own running maximum and sum
+// and its own ring of copies (cp.async): no barrier until the tile's end.  No transposition
+// either, because the order of a contraction is free: for Q K^T, lane (r, c) = (lane / 4,
+// lane % 4) takes 16 consecutive elements 64 j + 16 c of key r, and Q is read in the same
+// order; for P V, it takes elements 16 r .. of the four keys whose weights its accumulators
+// hold.  Eight neighbouring lanes copy 128 bytes on end (copies of what each lane itself reads
+// moved every sector twice: 131072 keys, 4 sequences 245 us), and the pieces of a row trade
+// places by its number so that the reads meet no bank twice.
 #include <cuda_bf16.h>
 
 #include "kv_attention.cuh"
@@ -21,13 +23,15 @@ namespace w4a4 {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
 constexpr int kRows = 16;          // query rows of a tile
-constexpr int kUnit = kWarps;      // blocks of 16 keys in a unit
 constexpr size_t kWsCounters = size_t(1) << 20;  // as in the other workspaces: zero between calls
 
 template <int D>
 struct Shape {
+  // Two CTAs of four warps an SM (registers hold no more: the accumulators alone are D / 2 a lane): one's lookups,
+  // joins and stores run beside the other's stream.
+  static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+  static constexpr int kUnit = kWarps;   // blocks of 16 keys in a unit
   static constexpr int kStage = 32 * D;  // bytes of 16 keys and values
   static constexpr int kRing = D == 256 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kRingBytes = kWarps * kRing * kStage;
@@ -53,21 +57,22 @@ struct DecodeArgs {
 
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
-  if constexpr (N == 16)  // past L1: nothing is read twice
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+// Where 16-byte piece ch of a block's row lies: piece ch ^ place of that row.  A read of K by eight lanes takes four
+// neighbouring pieces of two rows, one of V two pieces of every second row of eight.
+template <int D>
+__device__ __forceinline__ int k_place(int row) { return D == 64 ? 0 : (row & 1) << 2; }
+template <int D>
+__device__ __forceinline__ int v_place(int row) { return D == 64 ? (row >> 1) & 3 : row & 6; }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -78,7 +83,9 @@ struct Plan {
   int units;        // of a tile
   int step0, step1;  // blocks of 16 keys that some query of the sequence sees
 };
+template <int D>
 __device__ __forceinline__ Plan plan_of(const DecodeArgs& p, const Seq& q) {
+  constexpr int kUnit = Shape<D>::kUnit;
   Plan o{0, 1, 0, 0};
   const int64_t rows = static_cast<int64_t>(q.n) * p.group;
   if (q.n == 0 || rows > p.most_rows) return o;
@@ -92,8 +99,9 @@ __device__ __forceinline__ Plan plan_of(const DecodeArgs& p, const Seq& q) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArgs p) {
+__global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const DecodeArgs p) {
   using C = Shape<D>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kUnit = C::kUnit;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows], sm_f[kRows];
   __shared__ int sm_lo[kRows], sm_hi[kRows];
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
     const int b = b0 + tid;
     int64_t mine = 0;
     if (b < p.s.batch) {
-      const Plan o = plan_of(p, kv_seq(p.s, b, p.c.page, p.err));
+      const Plan o = plan_of<D>(p, kv_seq(p.s, b, p.c.page, p.err));
       mine = static_cast<int64_t>(o.tiles) * o.units;
     }
     int64_t at = mine;
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
       else hi = mid;
     }
     const Seq q = kv_seq(p.s, b, p.c.page, nullptr);
-    const Plan plan = plan_of(p, q);
+    const Plan plan = plan_of<D>(p, q);
     const int64_t in = u - prefix[b];
     const int tile = static_cast<int>(in / plan.units), u0 = static_cast<int>(in % plan.units);
     const int64_t tile_u = u - u0;  // the tile's first unit
@@ -222,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
     float o[D / 8][4] = {};
     float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
     const int steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kRing * C::kStage + 16 * lane;
-    const uint8_t* const ring_p = smem + warp * C::kRing * C::kStage + 16 * lane;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kRing * C::kStage;
+    const uint8_t* const ring_p = smem + warp * C::kRing * C::kStage;
     // lane i looks up the page and the scales of this warp's i-th block of 32
     int64_t look_at = -1;  // its first K code
     int look_s = 0;        // scale bytes of K and V
@@ -248,26 +256,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
         const int64_t at = __shfl_sync(0xFFFFFFFFu, look_at, i & 31);
         const int sc = __shfl_sync(0xFFFFFFFFu, look_s, i & 31);
         const int st = i % C::kRing;
-        const bool there = at >= 0;
-        const int8_t* const k = p.c.codes + (there ? at : 0);
-        const int8_t* const v = k + (there ? static_cast<int64_t>(p.c.page) * D : 0);
+        const bool there = at >= 0;  // nothing is read where there is no page
+        const int8_t* const k = p.c.codes + (there ? at : 0) + 16 * lane;
+        const int8_t* const v = k + static_cast<int64_t>(p.c.page) * D;
         const uint32_t dst = ring + st * C::kStage;
-        const int kr = there ? r * D + 16 * c : 0;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j)
-            cp_async<16>(dst + 512 * (n * (D / 64) + j), k + kr + (there ? n * 8 * D + 64 * j : 0), there);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int key = (kk >> 1) * 8 + 2 * c + (kk & 1);
-          if constexpr (D == 64) {
-            cp_async<8>(dst + 1024 + 256 * kk - 8 * lane, v + (there ? key * D + 8 * r : 0), there);
-          } else {
-#pragma unroll
-            for (int h = 0; h < D / 128; ++h)
-              cp_async<16>(dst + 16 * D + 512 * (kk * (D / 128) + h), v + (there ? key * D + 128 * h + 16 * r : 0), there);
-          }
+        for (int m = 0; m < D / 32; ++m) {
+          const int piece = 32 * m + lane, row = piece / (D / 16), ch = piece % (D / 16);
+          cp_async16(dst + row * D + ((ch ^ k_place<D>(row)) << 4), k + 512 * m, there);
+          cp_async16(dst + 16 * D + row * D + ((ch ^ v_place<D>(row)) << 4), v + 512 * m, there);
         }
         if (lane == 0)  // a block without a page: codes of zero, whose weights are taken out below
           sm_scale[warp][st] = make_float2(there ? kv_scale(sc & 255) : 0.0f, (sc >> 8) == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>((sc >> 8) - 127));
@@ -285,25 +282,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
       const uint8_t* const src = ring_p + st * C::kStage;
       float s[2][4] = {};
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j)
+      for (int j = 0; j < D / 64; ++j) {
+        const uint8_t* const at = src + r * D + (((4 * j + c) ^ k_place<D>(r)) << 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(at), v = *reinterpret_cast<const uint4*>(at + 8 * D);
+        const uint32_t w[2][4] = {{u.x, u.y, u.z, u.w}, {v.x, v.y, v.z, v.w}};
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(src + 512 * (n * (D / 64) + j));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        for (int k = 0; k < 4; ++k) {
+          uint32_t f[4];
+          if constexpr (kQRegs) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = w[k] ^ 0x80808080u;
-            const uint32_t b0 = codes_half2(x, 0x4140u), b1 = codes_half2(x, 0x4342u);
-            if constexpr (kQRegs) {
-              const uint32_t (&f)[4] = qa[4 * j + k];
-              mma16816(s[n], f[0], f[1], f[2], f[3], b0, b1);
-            } else {
-              uint32_t f[4];
-              q_frag(4 * j + k, f);
-              mma16816(s[n], f[0], f[1], f[2], f[3], b0, b1);
-            }
+            for (int i2 = 0; i2 < 4; ++i2) f[i2] = qa[4 * j + k][i2];
+          } else {
+            q_frag(4 * j + k, f);
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t x = w[n][k] ^ 0x80808080u;
+            mma16816(s[n], f[0], f[1], f[2], f[3], codes_half2(x, 0x4140u), codes_half2(x, 0x4342u));
           }
         }
+      }
       const float g0 = f0 * sc.x, g1 = f1 * sc.x, ev = sc.y;
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -365,12 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_decode_kernel(const DecodeArg
         uint32_t w[4][kWords];
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
+          const int key = (kk >> 1) * 8 + 2 * c + (kk & 1);
+          const uint8_t* const at = src + 16 * D + key * D;
           if constexpr (D == 64) {
-            const uint2 x = *reinterpret_cast<const uint2*>(src + 1024 + 256 * kk - 8 * lane);
+            const uint2 x = *reinterpret_cast<const uint2*>(at + (((r >> 1) ^ v_place<D>(key)) << 4) + 8 * (r & 1));
             w[kk][0] = x.x ^ 0x80808080u;
             w[kk][1] = x.y ^ 0x80808080u;
           } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + 16 * D + 512 * (kk * (D / 128) + h));
+            const uint4 x = *reinterpret_cast<const uint4*>(at + (((8 * h + r) ^ v_place<D>(key)) << 4));
             w[kk][0] = x.x ^ 0x80808080u;
             w[kk][1] = x.y ^ 0x80808080u;
             w[kk][2 % kWords] = x.z ^ 0x80808080u;
@@ -513,8 +513,8 @@ cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
     configured[dev] = true;
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(num_sms());
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(2 * num_sms());
+  cfg.blockDim = dim3(Shape<D>::kThreads);
   cfg.dynamicSmemBytes = Shape<D>::smem(p.s.batch);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -530,7 +530,7 @@ cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
 // Few query rows (tokens x query heads per head of K and V), up to a tile of this kernel, are its work; more
 // go to the tensor cores.  A call with offsets may hold both kinds: each kernel takes its own.
 size_t kv8_attention_workspace_bytes(int dim) {
-  const size_t mine = kWsCounters + static_cast<size_t>(num_sms()) * 2 * kRows * (dim + 2) * sizeof(float);
+  const size_t mine = kWsCounters + static_cast<size_t>(2 * num_sms()) * 2 * kRows * (dim + 2) * sizeof(float);
   const size_t other = kv8_prompt_workspace_bytes(dim);
   return mine > other ? mine : other;
 }
