@@ -32,11 +32,14 @@ struct Shape {
   // joins and stores run beside the other's stream.
   static constexpr int kWarps = 4, kThreads = 32 * kWarps;
   static constexpr int kUnit = kWarps;   // blocks of 16 keys in a unit
+  // What a tile costs beside its keys (lookups, q, the join), in units: without it the CTAs that got many short
+  // sequences finished last.
+  static constexpr int kOnce = 8;
+  static constexpr int kLeast = 2;  // units of a CTA at least, for fewer parts to join
   static constexpr int kStage = 32 * D;  // bytes of 16 keys and values
   static constexpr int kRing = D == 256 ? 3 : D == 128 ? 5 : 8;
   static constexpr int kRingBytes = kWarps * kRing * kStage;
-  static constexpr int kMergeLd = D + 4;
-  static constexpr int kMergeBytes = kWarps * kRows * kMergeLd * 4;
+  static constexpr int kMergeBytes = kWarps * kRows * D * 4;
   static constexpr int kQLd = 2 * D + 8;  // bytes of a row of q: two lanes' 8-byte reads share no bank
   static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
   static constexpr int kQ = kMain, kPrefix = kQ + kRows * kQLd;
@@ -66,6 +69,12 @@ template <int D>
 __device__ __forceinline__ int k_place(int row) { return D == 64 ? 0 : (row & 1) << 2; }
 template <int D>
 __device__ __forceinline__ int v_place(int row) { return D == 64 ? (row >> 1) & 3 : row & 6; }
+// Where the four floats from element d of a row lie in the warps' sums: by the lane that wrote them and the row, so that
+// neither the writes (four lanes 128 bytes apart, of two rows) nor the reads meet a bank more than twice.
+template <int D>
+__device__ __forceinline__ int merge_place(int row, int d) {
+  return ((d >> 2) ^ ((D == 64 ? d >> 4 : d >> 5) & 3) ^ ((row & 1) << 2)) << 2;
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -80,7 +89,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // A sequence's tiles, and the units of each.
 struct Plan {
   int tiles;        // row tiles x heads
-  int units;        // of a tile
+  int units;        // of a tile: kOnce and those of its keys
   int step0, step1;  // blocks of 16 keys that some query of the sequence sees
 };
 template <int D>
@@ -94,7 +103,7 @@ __device__ __forceinline__ Plan plan_of(const DecodeArgs& p, const Seq& q) {
   seen(p.a, q.len - q.n, q.len, lo, hi);
   o.step0 = min(lo, q.len) / kKvTokens;
   o.step1 = (q.len + kKvTokens - 1) / kKvTokens;
-  if (p.tickets) o.units = max(1, (o.step1 - o.step0 + kUnit - 1) / kUnit);
+  if (p.tickets) o.units = Shape<D>::kOnce + max(1, (o.step1 - o.step0 + kUnit - 1) / kUnit);
   return o;
 }
 
@@ -113,13 +122,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
   grid_dep_wait();
   grid_dep_launch();
 
-  // units before each sequence
-  int64_t total = 0;
-  for (int b0 = 0; b0 < p.s.batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    int64_t mine = 0;
-    if (b < p.s.batch) {
-      const Plan o = plan_of<D>(p, kv_seq(p.s, b, p.c.page, p.err));
+  // units before each sequence: of up to 32 in the lanes of every warp, else in shared memory
+  const bool small = p.s.batch <= 32;
+  int64_t total = 0, mine = 0, before = 0;
+  Seq seq{};
+  if (small) {
+    if (lane < p.s.batch) {
+      seq = kv_seq(p.s, lane, p.c.page, p.err);
+      const Plan o = plan_of<D>(p, seq);
       mine = static_cast<int64_t>(o.tiles) * o.units;
     }
     int64_t at = mine;
@@ -128,38 +138,66 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
       const int64_t o = __shfl_up_sync(0xFFFFFFFFu, at, d);
       if (lane >= d) at += o;
     }
-    if (lane == 31) sm_carry[warp] = at;
-    __syncthreads();
-    int64_t before = total;
+    before = at - mine;
+    total = __shfl_sync(0xFFFFFFFFu, at, 31);
+  } else {
+    for (int b0 = 0; b0 < p.s.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      mine = 0;
+      if (b < p.s.batch) {
+        const Plan o = plan_of<D>(p, kv_seq(p.s, b, p.c.page, p.err));
+        mine = static_cast<int64_t>(o.tiles) * o.units;
+      }
+      int64_t at = mine;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm_carry[w];
-      total += sm_carry[w];
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, at, d);
+        if (lane >= d) at += o;
+      }
+      if (lane == 31) sm_carry[warp] = at;
+      __syncthreads();
+      before = total;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm_carry[w];
+        total += sm_carry[w];
+      }
+      if (b < p.s.batch) prefix[b] = before + at - mine;
+      __syncthreads();
     }
-    if (b < p.s.batch) prefix[b] = before + at - mine;
-    __syncthreads();
   }
-  if (tid == 0) prefix[p.s.batch] = total;
-  __syncthreads();
-  const int64_t G = total < gridDim.x ? total : gridDim.x;  // CTAs at work: each has a unit at least
+  const int64_t G = total == 0 ? 0 : max(int64_t(1), min(static_cast<int64_t>(gridDim.x), total / C::kLeast));  // CTAs at work
   if (static_cast<int64_t>(blockIdx.x) >= G) return;
   const auto range = [&](int64_t cta) { return total * cta / G; };
   const int64_t u_end = range(blockIdx.x + 1);
 
-  for (int64_t u = range(blockIdx.x), done = 0; u < u_end; ++done) {
+  for (int64_t u = range(blockIdx.x); u < u_end;) {
     // the tile of unit u
-    int b = 0;
-    for (int hi = p.s.batch; hi - b > 1;) {
-      const int mid = (b + hi) >> 1;
-      if (prefix[mid] <= u) b = mid;
-      else hi = mid;
+    int b;
+    Seq q;
+    int64_t in;
+    if (small) {
+      b = 31 - __clz(__ballot_sync(0xFFFFFFFFu, lane < p.s.batch && before <= u));
+      q.first = __shfl_sync(0xFFFFFFFFu, seq.first, b);
+      q.n = __shfl_sync(0xFFFFFFFFu, seq.n, b);
+      q.len = __shfl_sync(0xFFFFFFFFu, seq.len, b);
+      in = u - __shfl_sync(0xFFFFFFFFu, before, b);
+    } else {
+      b = 0;
+      for (int hi = p.s.batch; hi - b > 1;) {
+        const int mid = (b + hi) >> 1;
+        if (prefix[mid] <= u) b = mid;
+        else hi = mid;
+      }
+      q = kv_seq(p.s, b, p.c.page, nullptr);
+      in = u - prefix[b];
     }
-    const Seq q = kv_seq(p.s, b, p.c.page, nullptr);
     const Plan plan = plan_of<D>(p, q);
-    const int64_t in = u - prefix[b];
     const int tile = static_cast<int>(in / plan.units), u0 = static_cast<int>(in % plan.units);
     const int64_t tile_u = u - u0;  // the tile's first unit
     const int u1 = static_cast<int>(min(static_cast<int64_t>(plan.units), u0 + (u_end - u)));
+    const int once = p.tickets ? C::kOnce : 0;
+    if (u1 <= once) break;  // no key of this tile, the CTA's last
     const int head = tile % p.c.heads, row0 = tile / p.c.heads * kRows;
     const int rows = min(kRows, q.n * p.group - row0);
     int first, last, ignore;  // keys of the tile's first and last query
@@ -167,25 +205,76 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
     seen(p.a, q.len - q.n + (row0 + rows - 1) / p.group, q.len, ignore, last);
     int s0 = max(plan.step0, min(first, q.len) / kKvTokens), s1 = min(plan.step1, (max(last, 0) + kKvTokens - 1) / kKvTokens);
     if (p.tickets) {
-      s0 = max(s0, plan.step0 + u0 * kUnit);
-      s1 = min(s1, plan.step0 + u1 * kUnit);
+      s0 = max(s0, plan.step0 + max(u0 - once, 0) * kUnit);
+      s1 = min(s1, plan.step0 + (u1 - once) * kUnit);
     }
 
+    const int steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kRing * C::kStage;
+    const uint8_t* const ring_p = smem + warp * C::kRing * C::kStage;
+    // q's loads go out first: 8 elements a pass
+    constexpr int kPasses = kRows * D / 8 / kThreads;
+    Chunk<float> q_raw[kPasses];
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int ch = pass * kThreads + tid, row = ch / (D / 8), g = row0 + row;
+      if (row < rows) {
+        const int64_t at = static_cast<int64_t>(q.first + g / p.group) * p.a.ldq + (head * p.group + g % p.group) * p.a.ldqh + 8 * (ch % (D / 8));
+        if (p.a.q_bf16) reinterpret_cast<Chunk<__nv_bfloat16>&>(q_raw[pass]).load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
+        else q_raw[pass].load(static_cast<const float*>(p.a.q) + at, false);
+      }
+    }
+    // lane i looks up the page and the scales of this warp's i-th block of 32
+    int64_t look_at = -1;  // its first K code
+    int look_s = 0;        // scale bytes of K and V
+    const auto look = [&](int i0) {
+      const int i = i0 + lane;
+      look_at = -1;
+      look_s = 0x7F7F;
+      if (i < steps) {
+        const int t = (s0 + warp + kWarps * i) * kKvTokens;
+        const int page = kv_page(p.s, p.c, b, t, p.err);
+        if (page >= 0) {
+          const int in_page = t % p.c.page;
+          const int64_t sc = kv_scale_at(p.c, page, head, 0) + in_page / kKvTokens;
+          look_at = kv_at(p.c, page, head, 0) + static_cast<int64_t>(in_page) * D;
+          look_s = p.c.scales[sc] | p.c.scales[sc + p.c.page / kKvTokens] << 8;
+        }
+      }
+    };
+    const auto issue = [&](int i) {
+      if (i < steps) {
+        if ((i & 31) == 0) look(i);
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, look_at, i & 31);
+        const int st = i % C::kRing;
+        const bool there = at >= 0;  // nothing is read where there is no page
+        const int8_t* const k = p.c.codes + (there ? at : 0) + 16 * lane;
+        const int8_t* const v = k + static_cast<int64_t>(p.c.page) * D;
+        const uint32_t dst = ring + st * C::kStage;
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+          const int piece = 32 * m + lane, row = piece / (D / 16), ch = piece % (D / 16);
+          cp_async16(dst + row * D + ((ch ^ k_place<D>(row)) << 4), k + 512 * m, there);
+          cp_async16(dst + 16 * D + row * D + ((ch ^ v_place<D>(row)) << 4), v + 512 * m, there);
+        }
+        const int sc = __shfl_sync(0xFFFFFFFFu, look_s, i & 31);
+        if (lane == 0)  // a block without a page: codes of zero, whose weights are taken out below
+          sm_scale[warp][st] = make_float2(there ? kv_scale(sc & 255) : 0.0f, (sc >> 8) == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>((sc >> 8) - 127));
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::kRing - 1; ++i) issue(i);
     // q: rotated as the keys are, scaled by a power of two per row
-    for (int ch = tid; ch < kRows * D / 8; ch += kThreads) {
-      const int row = ch / (D / 8), cc = ch % (D / 8);
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int ch = pass * kThreads + tid, row = ch / (D / 8), cc = ch % (D / 8);
       float v[8] = {};
       if (row < rows) {
-        const int g = row0 + row;
-        const int64_t at = static_cast<int64_t>(q.first + g / p.group) * p.a.ldq + (head * p.group + g % p.group) * p.a.ldqh + 8 * cc;
         if (p.a.q_bf16) {
-          Chunk<__nv_bfloat16> x;
-          x.load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
-          x.get(v);
+          reinterpret_cast<const Chunk<__nv_bfloat16>&>(q_raw[pass]).get(v);
         } else {
-          Chunk<float> x;
-          x.load(static_cast<const float*>(p.a.q) + at, false);
-          x.get(v);
+          q_raw[pass].get(v);
         }
       }
       if (p.c.rotated) quad_rotate(v, lane & 3);
@@ -229,50 +318,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
 
     float o[D / 8][4] = {};
     float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
-    const int steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kRing * C::kStage;
-    const uint8_t* const ring_p = smem + warp * C::kRing * C::kStage;
-    // lane i looks up the page and the scales of this warp's i-th block of 32
-    int64_t look_at = -1;  // its first K code
-    int look_s = 0;        // scale bytes of K and V
-    const auto look = [&](int i0) {
-      const int i = i0 + lane;
-      look_at = -1;
-      look_s = 0x7F7F;
-      if (i < steps) {
-        const int t = (s0 + warp + kWarps * i) * kKvTokens;
-        const int page = kv_page(p.s, p.c, b, t, p.err);
-        if (page >= 0) {
-          const int in_page = t % p.c.page;
-          const int64_t sc = kv_scale_at(p.c, page, head, 0) + in_page / kKvTokens;
-          look_at = kv_at(p.c, page, head, 0) + static_cast<int64_t>(in_page) * D;
-          look_s = p.c.scales[sc] | p.c.scales[sc + p.c.page / kKvTokens] << 8;
-        }
-      }
-    };
-    const auto issue = [&](int i) {
-      if (i < steps) {
-        if ((i & 31) == 0) look(i);
-        const int64_t at = __shfl_sync(0xFFFFFFFFu, look_at, i & 31);
-        const int sc = __shfl_sync(0xFFFFFFFFu, look_s, i & 31);
-        const int st = i % C::kRing;
-        const bool there = at >= 0;  // nothing is read where there is no page
-        const int8_t* const k = p.c.codes + (there ? at : 0) + 16 * lane;
-        const int8_t* const v = k + static_cast<int64_t>(p.c.page) * D;
-        const uint32_t dst = ring + st * C::kStage;
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
-          const int piece = 32 * m + lane, row = piece / (D / 16), ch = piece % (D / 16);
-          cp_async16(dst + row * D + ((ch ^ k_place<D>(row)) << 4), k + 512 * m, there);
-          cp_async16(dst + 16 * D + row * D + ((ch ^ v_place<D>(row)) << 4), v + 512 * m, there);
-        }
-        if (lane == 0)  // a block without a page: codes of zero, whose weights are taken out below
-          sm_scale[warp][st] = make_float2(there ? kv_scale(sc & 255) : 0.0f, (sc >> 8) == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>((sc >> 8) - 127));
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < C::kRing - 1; ++i) issue(i);
     for (int i = 0; i < steps; ++i) {
       issue(i + C::kRing - 1);
       cp_wait<C::kRing - 1>();
@@ -411,20 +456,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
       top1 = fmaxf(top1, sm_m[w][r + 8]);
     }
     const float c0 = m0 == kNegInf ? (l0 == l0 ? 0.0f : 1.0f) : ex2(m0 - top0), c1 = m1 == kNegInf ? (l1 == l1 ? 0.0f : 1.0f) : ex2(m1 - top1);
-    float* const merge = reinterpret_cast<float*>(smem) + warp * kRows * C::kMergeLd;
+    float* const merge = reinterpret_cast<float*>(smem) + warp * kRows * D;
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t)
+    for (int t = 0; t < D / 8; t += 4)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int d = D == 64 ? 8 * (2 * c + e) + t : 128 * (t >> 4) + 16 * (2 * c + e) + (t & 15);
-        merge[r * C::kMergeLd + d] = o[t][e] * c0;
-        merge[(r + 8) * C::kMergeLd + d] = o[t][2 + e] * c1;
+        *reinterpret_cast<float4*>(merge + r * D + merge_place<D>(r, d)) = make_float4(o[t][e] * c0, o[t + 1][e] * c0, o[t + 2][e] * c0, o[t + 3][e] * c0);
+        *reinterpret_cast<float4*>(merge + (r + 8) * D + merge_place<D>(r, d)) =
+            make_float4(o[t][2 + e] * c1, o[t + 1][2 + e] * c1, o[t + 2][2 + e] * c1, o[t + 3][2 + e] * c1);
       }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == plan.units;
-    const int64_t c_first = whole ? 0 : ((tile_u + 1) * G - 1) / total;
+    const bool whole = u0 <= once && u1 == plan.units;
+    const int64_t c_first = whole ? 0 : ((tile_u + once + 1) * G - 1) / total;  // the CTA of the tile's first keys
     const int parts = whole ? 1 : static_cast<int>(((tile_u + plan.units) * G - 1) / total - c_first) + 1;
-    float* const mine = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done > 0)) * C::kPart;
+    float* const mine = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (range(blockIdx.x) < tile_u)) * C::kPart;
     const auto write = [&](int row, int cc, float (&v)[8], float l) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : v[i] / l;
@@ -436,7 +482,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
         else store8(static_cast<float*>(p.a.out) + at, v, false);
       }
     };
-    for (int ch = tid; ch < kRows * D / 8; ch += kThreads) {
+    constexpr int kTogether = D < 256 ? 256 / D : 1;  // rows of a warp's pass over 8-element pieces
+    const int pieces = (rows + kTogether - 1) / kTogether * kTogether * (D / 8);
+    for (int ch = tid; ch < pieces; ch += kThreads) {
       const int row = ch / (D / 8), cc = ch % (D / 8);
       float top = kNegInf, l = 0.0f, v[8] = {};
 #pragma unroll
@@ -445,9 +493,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
       for (int w = 0; w < kWarps; ++w) {
         const float m = sm_m[w][row], x = sm_l[w][row];
         l += m == kNegInf ? (x == x ? 0.0f : x) : x * ex2(m - top);
-        const float* const s = reinterpret_cast<const float*>(smem) + (w * kRows + row) * C::kMergeLd + 8 * cc;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += s[i];
+        const float* const s = reinterpret_cast<const float*>(smem) + (w * kRows + row) * D;
+        const float4 y = *reinterpret_cast<const float4*>(s + merge_place<D>(row, 8 * cc));
+        const float4 z = *reinterpret_cast<const float4*>(s + merge_place<D>(row, 8 * cc + 4));
+        v[0] += y.x; v[1] += y.y; v[2] += y.z; v[3] += y.w;
+        v[4] += z.x; v[5] += z.y; v[6] += z.z; v[7] += z.w;
       }
       if (whole) {
         write(row, cc, v, l);
@@ -462,10 +512,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
       }
     }
     if (!whole) {
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
         uint32_t* const ticket = p.tickets + c_first;  // a CTA is the first of one cut tile at most
+        __threadfence();  // the CTA's parts, which the barrier has put before this
         const uint32_t got = atomicAdd(ticket, 1u);
         sm_last = got == static_cast<uint32_t>(parts - 1);
         if (sm_last) *ticket = 0u;
@@ -476,11 +526,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
         // part i is CTA c_first + i's; its first tile's unless the tile begins inside its range
         const int64_t part0 = 2 * c_first + (range(c_first) < tile_u);
         const auto part = [&](int i) { return p.parts + (i == 0 ? part0 : 2 * (c_first + i)) * C::kPart; };
-        for (int ch = tid; ch < kRows * D / 8; ch += kThreads) {
+        for (int ch = tid; ch < pieces; ch += kThreads) {
           const int row = ch / (D / 8), cc = ch % (D / 8);
           float top = kNegInf, l = 0.0f, v[8] = {};
+#pragma unroll 8
           for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(part(i) + kRows * D + row));
-#pragma unroll 4
+#pragma unroll 8
           for (int i = 0; i < parts; ++i) {
             const float* const s = part(i);
             const float m = __ldcg(s + kRows * D + row), x = __ldcg(s + kRows * (D + 1) + row);
