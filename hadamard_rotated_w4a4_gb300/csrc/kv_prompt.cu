@@ -54,7 +54,7 @@ struct Shape {
   static_assert(kRegs0 + kRegs1 + 2 * kRegs2 <= 4 * 128);
   static constexpr int kS = 0, kO = 256;            // TMEM columns
   static constexpr int kPart = kRows * (D + 2);     // floats of a cut tile's part
-  static_assert(kSmem <= 227 * 1024 - 2 * 1024 && kO + kTiles * D <= 512 && 4 * (kKvMaxBatch + 1) <= kBufs * kTile);
+  static_assert(kSmem <= 227 * 1024 - 2 * 1024 && kO + kTiles * D <= 512 && 4 * kKvMaxBatch <= kBufs * kTile);
 };
 
 struct PromptArgs {
@@ -74,6 +74,7 @@ struct Bars {
   uint64_t p_ready[2][2];  // [S][half of the keys]
   uint64_t pv_done[2][2];  // [row tile][half]
   uint64_t o_done[2];      // once, at the end
+  uint64_t q_full;         // once
   uint32_t tmem;
   volatile int abort;
 };
@@ -151,72 +152,139 @@ __device__ __forceinline__ void rotate32(float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] *= c_h32();
 }
 
-// Row tiles of a sequence, all heads.
+// Keys that the rows row0 .. row0 + rows - 1 see, from a block's start on, and the tiles of them.
+__device__ __forceinline__ int key_tiles(const PromptArgs& p, const Seq& q, int row0, int rows, int& key0) {
+  int lo, hi, ignore;
+  seen(p.a, q.len - q.n + row0 / p.group, q.len, lo, ignore);
+  seen(p.a, q.len - q.n + (row0 + rows - 1) / p.group, q.len, ignore, hi);
+  key0 = min(lo, q.len) / kKvTokens * kKvTokens;
+  return max(1, (max(hi, 0) - key0 + kBK - 1) / kBK);
+}
+
+// A sequence's row tiles, all heads, and the key tiles of its last.
+struct Plan {
+  int tiles, keys;
+};
 template <int D>
-__device__ __forceinline__ int tiles_of(const PromptArgs& p, const Seq& q) {
+__device__ __forceinline__ Plan plan_of(const PromptArgs& p, const Seq& q) {
   const int64_t rows = static_cast<int64_t>(q.n) * p.group;
-  return q.n == 0 || rows < p.least_rows ? 0 : static_cast<int>((rows + Shape<D>::kRows - 1) / Shape<D>::kRows) * p.c.heads;
+  if (q.n == 0 || rows < p.least_rows) return {0, 0};
+  const int n = static_cast<int>((rows + Shape<D>::kRows - 1) / Shape<D>::kRows), row0 = (n - 1) * Shape<D>::kRows;
+  int key0;
+  return {n * p.c.heads, key_tiles(p, q, row0, static_cast<int>(rows) - row0, key0)};
 }
 
 // What a CTA does: rows row0 .. row0 + rows - 1 of (sequence, head), key tiles t0 .. t1 - 1 of
-// those that start at key0, as part `part` of `parts`.
+// those that start at key0, as part `part` of `parts`; part i of a tile is kept at slot0 + i.
 struct Work {
   int b, head, row0, rows;
   Seq q;
-  int key0, t0, t1, part, parts;
+  int key0, t0, t1, part, parts, slot0;
 };
-// By whole CTAs; prefix: shared, of batch + 1 entries; carry: shared, of 32.  False: nothing to do.
-// Tiles in descending order: with a causal mask a sequence's later rows see more keys, and go first.
+// Sum of v over the CTA's threads, and before this one's.  carry: shared, of 32.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* carry, int threads, int64_t& before) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t at = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, at, d);
+    if (lane >= d) at += o;
+  }
+  __syncthreads();
+  if (lane == 31) carry[warp] = at;
+  __syncthreads();
+  int64_t total = 0;
+  before = at - v;
+  for (int i = 0; i < threads / 32; ++i) {
+    if (i < warp) before += carry[i];
+    total += carry[i];
+  }
+  return total;
+}
+// By whole CTAs; prefix: shared, of batch entries, not used for up to 32 sequences: then each warp finds it by itself,
+// without a barrier.  False: nothing to do.
+// With fewer row tiles than SMs and a workspace, a sequence's tiles have their keys cut into parts, each of as
+// many key tiles at most as let all parts have an SM; two at least, since a part costs its q, its first copies
+// and its write of O.  Tiles in descending order: with a causal mask a sequence's later rows see more keys.
 template <int D>
-__device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int* carry, int threads, int cta, Work& w) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int total = 0;
-  for (int b0 = 0; b0 < p.s.batch; b0 += threads) {
-    const int b = b0 + tid;
-    const int mine = b < p.s.batch ? tiles_of<D>(p, kv_seq(p.s, b, p.c.page, p.err)) : 0;
-    int at = mine;
+__device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int64_t* carry, int threads, int cta, Work& w) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool small = p.s.batch <= 32;
+  int64_t tiles = 0, keys = 0, total = 0, before = 0;
+  Plan o{0, 0};
+  Seq seq{};
+  if (small) {
+    if (lane < p.s.batch) {
+      seq = kv_seq(p.s, lane, p.c.page, p.err);
+      o = plan_of<D>(p, seq);
+    }
+    tiles = o.tiles;
+    keys = static_cast<int64_t>(o.tiles) * o.keys;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, at, d);
-      if (lane >= d) at += o;
+      tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+      keys += __shfl_xor_sync(0xFFFFFFFFu, keys, d);
     }
-    if (lane == 31) carry[warp] = at;
-    __syncthreads();
-    int before = total;
-    for (int i = 0; i < threads / 32; ++i) {
-      if (i < warp) before += carry[i];
-      total += carry[i];
+  } else {
+    for (int b0 = 0; b0 < p.s.batch; b0 += threads) {
+      o = Plan{0, 0};
+      if (b0 + tid < p.s.batch) o = plan_of<D>(p, kv_seq(p.s, b0 + tid, p.c.page, p.err));
+      tiles += block_scan(o.tiles, carry, threads, before);
+      keys += block_scan(static_cast<int64_t>(o.tiles) * o.keys, carry, threads, before);
     }
-    if (b < p.s.batch) prefix[b] = before + at - mine;
-    __syncthreads();
   }
-  if (tid == 0) prefix[p.s.batch] = total;
-  __syncthreads();
-  if (total == 0) return false;
-  const int most = p.parts ? max(1, p.sms / total) : 1;  // parts that a tile's keys may be cut into
-  if (cta >= total * most) return false;
-  const int tile = total - 1 - cta % total;
-  w.part = cta / total;
-  int b = 0;
-  for (int hi = p.s.batch; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (prefix[mid] <= tile) b = mid;
-    else hi = mid;
+  if (tiles == 0) return false;
+  // ceil(n / most) a tile, at most n / most + 1: keys / most + tiles parts
+  int most = 0;
+  if (p.parts && 2 * tiles <= p.sms) most = static_cast<int>(max(int64_t(2), (keys + p.sms - tiles - 1) / (p.sms - tiles)));
+  const auto ctas = [&](const Plan& o) { return most ? static_cast<int64_t>(o.tiles) * ((o.keys + most - 1) / most) : o.tiles; };
+  int at, b = 0, in;
+  if (small) {
+    int64_t sum = ctas(o);
+    before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += x;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, before, 31);
+    before -= sum;
+    if (cta >= total) return false;
+    at = static_cast<int>(total) - 1 - cta;
+    b = 31 - __clz(__ballot_sync(0xFFFFFFFFu, lane < p.s.batch && before <= at));
+    w.q.first = __shfl_sync(0xFFFFFFFFu, seq.first, b);
+    w.q.n = __shfl_sync(0xFFFFFFFFu, seq.n, b);
+    w.q.len = __shfl_sync(0xFFFFFFFFu, seq.len, b);
+    in = at - static_cast<int>(__shfl_sync(0xFFFFFFFFu, before, b));
+  } else {
+    for (int b0 = 0; b0 < p.s.batch; b0 += threads) {
+      o = Plan{0, 0};
+      if (b0 + tid < p.s.batch) o = plan_of<D>(p, kv_seq(p.s, b0 + tid, p.c.page, nullptr));
+      const int64_t sum = block_scan(ctas(o), carry, threads, before);
+      if (b0 + tid < p.s.batch) prefix[b0 + tid] = static_cast<int>(total + before);
+      total += sum;
+    }
+    __syncthreads();
+    if (cta >= total) return false;
+    at = static_cast<int>(total) - 1 - cta;
+    for (int hi = p.s.batch; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (prefix[mid] <= at) b = mid;
+      else hi = mid;
+    }
+    w.q = kv_seq(p.s, b, p.c.page, nullptr);
+    in = at - prefix[b];
   }
   w.b = b;
-  w.q = kv_seq(p.s, b, p.c.page, nullptr);
-  const int in = tile - prefix[b];
+  const int parts = most ? (plan_of<D>(p, w.q).keys + most - 1) / most : 1;
+  w.part = in % parts;
+  in /= parts;
+  w.slot0 = at - w.part;
   w.head = in % p.c.heads;
   w.row0 = in / p.c.heads * Shape<D>::kRows;
   w.rows = min(Shape<D>::kRows, w.q.n * p.group - w.row0);
-  int lo, hi, ignore;
-  seen(p.a, w.q.len - w.q.n + w.row0 / p.group, w.q.len, lo, ignore);
-  seen(p.a, w.q.len - w.q.n + (w.row0 + w.rows - 1) / p.group, w.q.len, ignore, hi);
-  hi = max(hi, 0);
-  w.key0 = min(lo, w.q.len) / kKvTokens * kKvTokens;
-  const int n = max(1, (hi - w.key0 + kBK - 1) / kBK);
-  // two tiles a part at least: a part costs its Q, its first copies and its write of O
-  w.parts = min(most, (n + 1) / 2);
+  const int n = key_tiles(p, w.q, w.row0, w.rows, w.key0);
+  w.parts = min(parts, (n + 1) / 2);  // an earlier row tile may see fewer keys than the last
   w.t0 = static_cast<int>(static_cast<int64_t>(n) * w.part / w.parts);
   w.t1 = static_cast<int>(static_cast<int64_t>(n) * (w.part + 1) / w.parts);
   return w.part < w.parts;
@@ -304,6 +372,51 @@ __device__ __forceinline__ void convert(const PromptArgs& p, const Work& w, int 
   }
 }
 
+// q to shared memory by warps 0-7: rotated as the keys are, scaled by a power of two per row, in the swizzle; four
+// pieces' loads go out together.  Rows past the last are zeros (a NaN there would have its warp look for maxima).
+template <int D>
+__device__ __forceinline__ void load_q(const PromptArgs& p, const Work& w, int qtiles, uint8_t* smem, float* row_factor) {
+  using C = Shape<D>;
+  const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
+  constexpr int kOnce = 4, kTogether = D < 256 ? 256 / D : 1;  // rows of a warp's pass
+  const int pieces = (w.rows + kTogether - 1) / kTogether * kTogether * (D / 8);
+  const auto place = [&](int row, int cc) {
+    return reinterpret_cast<uint4*>(smem + C::kQ + (row >> 7) * 128 * D * 2 + (cc >> 3) * C::kPanel + (row & 127) * 128 + (((cc & 7) ^ (row & 7)) << 4));
+  };
+  for (int ch = pieces + threadIdx.x; ch < qtiles * 128 * (D / 8); ch += 256) *place(ch / (D / 8), ch % (D / 8)) = make_uint4(0, 0, 0, 0);
+  for (int row = pieces / (D / 8) + threadIdx.x; row < qtiles * 128; row += 256) row_factor[row] = 0.0f;
+  for (int ch0 = threadIdx.x; ch0 < pieces; ch0 += 256 * kOnce) {
+    Chunk<float> raw[kOnce];
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i) {
+      const int ch = ch0 + 256 * i, row = ch / (D / 8), g = w.row0 + row;
+      if (row < w.rows) {
+        const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldq + (w.head * p.group + g % p.group) * p.a.ldqh + 8 * (ch % (D / 8));
+        if (p.a.q_bf16) reinterpret_cast<Chunk<__nv_bfloat16>&>(raw[i]).load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
+        else raw[i].load(static_cast<const float*>(p.a.q) + at, false);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i) {
+      const int ch = ch0 + 256 * i, row = ch / (D / 8), cc = ch % (D / 8);
+      if (ch >= pieces) break;  // the same for a warp: its pieces fill whole rows
+      float v[8] = {};
+      if (row < w.rows) {
+        if (p.a.q_bf16) reinterpret_cast<const Chunk<__nv_bfloat16>&>(raw[i]).get(v);
+        else raw[i].get(v);
+      }
+      if (p.c.rotated) quad_rotate(v, threadIdx.x & 3);
+      float amax = lane_amax(v);
+#pragma unroll
+      for (int d = 1; d < D / 8; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
+      const int e = row_exponent(amax);
+      const float f = sign * pow2i(-e);  // the scale's sign goes to q: the scores' factors are positive
+      *place(row, cc) = make_uint4(pack_half(v[0] * f, v[1] * f), pack_half(v[2] * f, v[3] * f), pack_half(v[4] * f, v[5] * f), pack_half(v[6] * f, v[7] * f));
+      if (cc == 0) row_factor[row] = fabsf(p.a.scale) * 1.4426950408889634f * pow2i(e);
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_constant__ PromptArgs p) {
   using C = Shape<D>;
@@ -312,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   __shared__ float sm_f[C::kRows];
   // per tile of keys: K scales, V exponents, 2^-exponent
   __shared__ __align__(16) float sm_sc[4][3][kBlocks];
-  __shared__ int sm_carry[32];
+  __shared__ int64_t sm_carry[32];
+  __shared__ Work sm_work;
   uint8_t* const smem = raw_smem + ((1024u - (su32(raw_smem) & 1023u)) & 1023u);
   const uint32_t sbase = su32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
@@ -330,6 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       mbar_init(&S.o_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], kBlocks);
+    mbar_init(&S.q_full, 8);
+
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -343,9 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = S.tmem;
   grid_dep_wait();
-  Work w;
-  const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), w);
-  if (!some) {
+  // Of up to 32 sequences warp 0 finds the CTA's work; all warps read it from shared memory, from where the compiler
+  // takes it for the same in every lane (straight from the shuffles the loops cost 11% more).
+  if (p.s.batch > 32 || warp == 0) {
+    Work w;
+    const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), w);
+    if (tid == 0) {
+      if (!some) w.rows = 0;
+      sm_work = w;
+    }
+  }
+  __syncthreads();
+  const Work w = sm_work;
+  if (w.rows == 0) {
     __syncthreads();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     return;
@@ -353,37 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   const int n = w.t1 - w.t0;
   const int key0 = w.key0 + w.t0 * kBK;
   const int qtiles = C::kTiles == 2 && w.rows > 128 ? 2 : 1;
-
-  // q: rotated as the keys are, scaled by a power of two per row, in the swizzle
-  const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
-  for (int ch = tid; ch < qtiles * 128 * (D / 8); ch += kThreads) {
-    const int row = ch / (D / 8), cc = ch % (D / 8);
-    float v[8] = {};
-    if (row < w.rows) {
-      const int g = w.row0 + row;
-      const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldq + (w.head * p.group + g % p.group) * p.a.ldqh + 8 * cc;
-      if (p.a.q_bf16) {
-        Chunk<__nv_bfloat16> x;
-        x.load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
-        x.get(v);
-      } else {
-        Chunk<float> x;
-        x.load(static_cast<const float*>(p.a.q) + at, false);
-        x.get(v);
-      }
-    }
-    if (p.c.rotated) quad_rotate(v, lane & 3);
-    float amax = lane_amax(v);
-#pragma unroll
-    for (int d = 1; d < D / 8; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
-    const int e = row_exponent(amax);
-    const float f = sign * pow2i(-e);  // the scale's sign goes to q: the scores' factors are positive
-    *reinterpret_cast<uint4*>(smem + C::kQ + (row >> 7) * 128 * D * 2 + (cc >> 3) * C::kPanel + (row & 127) * 128 + (((cc & 7) ^ (row & 7)) << 4)) =
-        make_uint4(pack_half(v[0] * f, v[1] * f), pack_half(v[2] * f, v[3] * f), pack_half(v[4] * f, v[5] * f), pack_half(v[6] * f, v[7] * f));
-    if (cc == 0) sm_f[row] = fabsf(p.a.scale) * 1.4426950408889634f * pow2i(e);
-  }
-  fence_async_smem();
-  __syncthreads();
 
   if (warp >= 8) {
     if constexpr (C::kRegs2 < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegs2));
@@ -395,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
     }
     if (warp > 8) {
       convert<D>(p, w, key0, n, warp - 9, smem, S, sm_sc);
-    } else {
+    } else if (__all_sync(0xFFFFFFFFu, wait_bar(S, &S.q_full, 0, p))) {
       const auto qk = [&](int t, int s, int j) {  // row tile t, into S number s
         const uint32_t q = sbase + C::kQ + t * 128 * D * 2, k = sbase + C::kK + (j % C::kBufs) * C::kTile;
         if (elect_one()) {
@@ -465,6 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         }
       }
     }
+  } else {
+    load_q<D>(p, w, qtiles, smem, sm_f);
+    fence_async_smem();
+    asm volatile("bar.sync 1, 256;" ::: "memory");  // the rows' factors
+    if (lane == 0) mbar_arrive(&S.q_full);
+  }
+  if (warp >= 8) {
   } else if ((warp >> 2) < qtiles) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs0));
     const int t = warp >> 2, row = tid & (C::kRows - 1);
@@ -589,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       const int g = w.row0 + row;
       const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldo + (w.head * p.group + g % p.group) * p.a.ldoh;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      float* const part = w.parts > 1 ? p.parts + static_cast<int64_t>(blockIdx.x) * C::kPart : nullptr;
+      float* const part = w.parts > 1 ? p.parts + static_cast<int64_t>(w.slot0 + w.part) * C::kPart : nullptr;
       if (part) {
         part[C::kRows * D + row] = m;
         part[C::kRows * (D + 1) + row] = l;
@@ -601,9 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         tmem_wait32(o);
         float (&v)[32] = *reinterpret_cast<float(*)[32]>(&o);
         if (part) {
-          float4* const to = reinterpret_cast<float4*>(part + row * D + d);
+          // four elements of every row together: a warp's rows side by side
+          float4* const to = reinterpret_cast<float4*>(part) + (d >> 2) * C::kRows + row;
+          if (row < w.rows)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) to[i * C::kRows] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           continue;
         }
 #pragma unroll
@@ -633,24 +737,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The parts of cut tiles together, in the order of their keys.  grid (tiles x parts at most, shares of a
-// tile's rows): CTA (x, y) takes share y of the tile whose first part CTA x was.
+// The parts of cut tiles together, in the order of their keys.  grid (SMs, shares of a tile's rows): CTA (x, y)
+// takes share y of the tile whose first part CTA x of the attention was.
 constexpr int kJoinThreads = 256, kJoinShares = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
   using C = Shape<D>;
-  __shared__ int prefix[kKvMaxBatch + 1], carry[32];
+  __shared__ int prefix[kKvMaxBatch];
+  __shared__ int64_t carry[32];
   grid_dep_launch();
   grid_dep_wait();
   Work w;
   if (!find_work<D>(p, prefix, carry, kJoinThreads, static_cast<int>(blockIdx.x), w) || w.part > 0 || w.parts == 1) return;
-  const int total = prefix[p.s.batch];  // part i is CTA blockIdx.x + i * total's
   constexpr int kShare = C::kRows / kJoinShares;
   for (int ch = threadIdx.x; ch < kShare * D / 8; ch += kJoinThreads) {
     const int row = blockIdx.y * kShare + ch / (D / 8), cc = ch % (D / 8);
     if (blockIdx.y * kShare >= w.rows) return;
     float top = kNegInf, l = 0.0f, v[8] = {};
-    const auto part = [&](int i) { return p.parts + (static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(i) * total) * C::kPart; };
+    const auto part = [&](int i) { return p.parts + static_cast<int64_t>(w.slot0 + i) * C::kPart; };
     const bool in = row < w.rows;
     if (in) {
       for (int i = 0; i < w.parts; ++i) top = fmaxf(top, part(i)[C::kRows * D + row]);
@@ -658,7 +762,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
       for (int i = 0; i < w.parts; ++i) {
         const float* const s = part(i);
         const float m = s[C::kRows * D + row], x = s[C::kRows * (D + 1) + row];
-        const float4 y = *reinterpret_cast<const float4*>(s + row * D + 8 * cc), z = *reinterpret_cast<const float4*>(s + row * D + 8 * cc + 4);
+        const float4* const t = reinterpret_cast<const float4*>(s) + 2 * cc * C::kRows + row;
+        const float4 y = t[0], z = t[C::kRows];
         const float f = m == kNegInf ? (x == x ? 0.0f : 1.0f) : ex2(m - top);
         l += x * f;
         v[0] += y.x * f; v[1] += y.y * f; v[2] += y.z * f; v[3] += y.w * f;
@@ -708,8 +813,7 @@ cudaError_t launch_prompt(const PromptArgs& p, int64_t most_tiles, cudaStream_t 
   const int64_t grid = most_tiles > p.sms ? most_tiles : p.sms;
   e = launch(kv8_prompt_kernel<D>, dim3(static_cast<unsigned>(p.parts ? grid : most_tiles)), kThreads, C::kSmem, p, st);
   if (e != cudaSuccess || !p.parts) return e;
-  // cut tiles are at most half as many as the SMs
-  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(p.sms / 2 < grid ? p.sms / 2 : grid), kJoinShares), kJoinThreads, 0, p, st);
+  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(p.sms), kJoinShares), kJoinThreads, 0, p, st);
 }
 
 int64_t g_wait = kWaitCycles, g_delay = 0;
