@@ -77,36 +77,67 @@ __device__ __forceinline__ Found find_block(const KvSeqs& s, int page, int x, in
   return f;
 }
 
-// A row of D values over D / 8 lanes, 8 each: 32 / (D / 8) rows a warp at a time.
+// A row of D values over D / 16 lanes, lane k of them with the chunks of 8 elements k and k + D / 16: the pairs
+// (i, i + D / 2) of a full rotary rotation lie in one lane, and the 32-blocks in four neighbours either way.
 template <int D>
 struct Lanes {
-  static constexpr int kPerRow = D / 8, kRows = 32 / kPerRow, kSteps = kKvTokens / kRows;
+  static constexpr int kPerRow = D / 16, kRows = 32 / kPerRow, kSteps = kKvTokens / kRows;
 };
 
-// The rotation by position of this lane's eight values (elements 8 cc ..), angles of nf pairs.
+// How the pairs lie: none, (2i, 2i + 1), (i, i + D / 2), (i, i + nf).
+enum Pairs : int { kNoPairs, kNeighbours, kHalves, kApart };
+
+__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+  o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+}
+
+// The rotation by position of a lane's two chunks of a row, cs and sn the cosines and sines of the row's angles.
 template <int D>
-__device__ __forceinline__ void rope(float (&v)[8], const float2* trig, int cc, int nf, int interleaved) {
-  if (interleaved) {  // pairs (2i, 2i + 1)
+__device__ __forceinline__ void rope(float (&v)[2][8], const float* cs, const float* sn, int k, int nf, Pairs pairs) {
+  constexpr int kPerRow = Lanes<D>::kPerRow;
+  if (pairs == kHalves) {
+    float c[8], s[8];
+    load8(cs + 8 * k, c);
+    load8(sn + 8 * k, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * cc + i < nf) {
-        const float2 t = trig[4 * cc + i];
-        const float a = v[2 * i], b = v[2 * i + 1];
-        v[2 * i] = a * t.x - b * t.y;
-        v[2 * i + 1] = b * t.x + a * t.y;
+    for (int i = 0; i < 8; ++i) {
+      const float a = v[0][i], b = v[1][i];
+      v[0][i] = a * c[i] - b * s[i];
+      v[1][i] = b * c[i] + a * s[i];
+    }
+  } else if (pairs == kNeighbours) {  // angles past nf are zero
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 c4 = *reinterpret_cast<const float4*>(cs + 4 * (k + h * kPerRow)), s4 = *reinterpret_cast<const float4*>(sn + 4 * (k + h * kPerRow));
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = v[h][2 * i], b = v[h][2 * i + 1];
+        v[h][2 * i] = a * c[i] - b * s[i];
+        v[h][2 * i + 1] = b * c[i] + a * s[i];
       }
-    return;
-  }
-  // pairs (i, i + nf), nf a multiple of 8: eight of them between two lanes of the row
-  const int nl = nf >> 3, lane = threadIdx.x & 31;
-  const bool lo = cc < nl, in = cc < 2 * nl;
-  const int src = lane + (!in ? 0 : lo ? nl : -nl);
+    }
+  } else {  // nf a multiple of 8: eight pairs between two chunks, of whichever lanes
+    const int nl = nf >> 3, base = (threadIdx.x & 31) - k;
+    float old[2][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float o = __shfl_sync(0xFFFFFFFFu, v[i], src);
-    if (in) {
-      const float2 t = trig[8 * (lo ? cc : cc - nl) + i];
-      v[i] = lo ? v[i] * t.x - o * t.y : v[i] * t.x + o * t.y;
+    for (int i = 0; i < 8; ++i) old[0][i] = v[0][i], old[1][i] = v[1][i];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int ch = k + h * kPerRow;
+      const bool lo = ch < nl, in = ch < 2 * nl;
+      const int other = !in ? ch : lo ? ch + nl : ch - nl;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = __shfl_sync(0xFFFFFFFFu, old[0][i], base + other % kPerRow), y = __shfl_sync(0xFFFFFFFFu, old[1][i], base + other % kPerRow);
+        const float o = other < kPerRow ? x : y;
+        if (in) {
+          const float c = cs[8 * (lo ? ch : other) + i], s = sn[8 * (lo ? ch : other) + i];
+          v[h][i] = lo ? old[h][i] * c - o * s : old[h][i] * c + o * s;
+        }
+      }
     }
   }
 }
@@ -115,7 +146,7 @@ __device__ __forceinline__ void rope(float (&v)[8], const float2* trig, int cc, 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvCache c, const KvSeqs s, const KvNew a, int* err) {
   using L = Lanes<D>;
-  __shared__ float2 trig[kKvTokens][D / 2];
+  __shared__ __align__(16) float cs[kKvTokens][D / 2], sn[kKvTokens][D / 2];
   __shared__ int at[6];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
@@ -138,62 +169,78 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvCache c, c
   __syncthreads();
   if (at[0] < 0) return;
   const int lo = at[1], hi = at[2], p0 = at[3], tok0 = at[4], page = at[5];
-  if (a.nf > 0) {
-    for (int i = threadIdx.x; i < (hi - lo) * a.nf; i += kThreads) {
-      const int r = lo + i / a.nf, j = i % a.nf;
-      const double turn = static_cast<double>(p0 + r) * (a.freqs[j] * 0.15915494309189533577);  // 1 / (2 pi)
-      const float x = static_cast<float>(turn - rint(turn));
-      float2 t;
-      sincospif(2.0f * x, &t.y, &t.x);
-      trig[r][j] = t;
+  const Pairs pairs = a.nf == 0 ? kNoPairs : a.interleaved ? kNeighbours : 2 * a.nf == D ? kHalves : kApart;
+  if (pairs != kNoPairs) {
+    // angle j of every row by the same threads, so that its share of a turn is taken once
+    for (int j = threadIdx.x % (D / 2); j < (pairs == kNeighbours ? D / 2 : a.nf); j += D / 2) {
+      const double turns = j < a.nf ? a.freqs[j] * 0.15915494309189533577 : 0.0;  // 1 / (2 pi)
+      for (int r = lo + threadIdx.x / (D / 2); r < hi; r += kThreads / (D / 2)) {
+        const double turn = static_cast<double>(p0 + r) * turns;
+        float sine, cosine;
+        sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sine, &cosine);
+        cs[r][j] = cosine;
+        sn[r][j] = sine;
+      }
     }
     __syncthreads();
   }
-  const int rr = lane / L::kPerRow, cc = lane % L::kPerRow;
+  const int rr = lane / L::kPerRow, k = lane % L::kPerRow;
   const int kv_tasks = page >= 0 ? 2 * c.heads : 0, tasks = kv_tasks + a.q_heads;
   for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {
     const bool is_q = task >= kv_tasks;
     const int h = is_q ? task - kv_tasks : task >> 1, is_v = is_q ? 0 : task & 1;
-    const T* x = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + h * (is_q ? a.ldqh : is_v ? a.ldvh : a.ldkh) + 8 * cc;
     const int64_t ld = is_q ? a.ldq : is_v ? a.ldv : a.ldk;
-    Chunk<T> raw[L::kSteps];
+    const T* x = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + h * (is_q ? a.ldqh : is_v ? a.ldvh : a.ldkh) + (tok0 + rr) * ld + 8 * k;
+    Chunk<T> raw[L::kSteps][2];
 #pragma unroll
     for (int i = 0; i < L::kSteps; ++i) {
       const int r = i * L::kRows + rr;
-      if (r >= lo && r < hi) raw[i].load(x + (tok0 + r) * ld, false);
-      else raw[i] = Chunk<T>{};
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        raw[i][g] = Chunk<T>{};
+        if (r >= lo && r < hi) raw[i][g].load(x + i * L::kRows * ld + g * (D / 2), false);
+      }
     }
+    const bool turn = pairs != kNoPairs && !is_v;
     if (is_q) {
+      const int64_t o = (tok0 + rr) * a.ldo + h * a.ldoh + 8 * k;
 #pragma unroll
       for (int i = 0; i < L::kSteps; ++i) {
         const int r = i * L::kRows + rr;
         if (i * L::kRows >= hi || (i + 1) * L::kRows <= lo) continue;
-        float v[8];
-        raw[i].get(v);
-        if (a.nf > 0) rope<D>(v, trig[r], cc, a.nf, a.interleaved);
-        if (r >= lo && r < hi) {
-          const int64_t o = (tok0 + r) * a.ldo + h * a.ldoh + 8 * cc;
-          if (a.o_bf16) store8(static_cast<__nv_bfloat16*>(a.q_out) + o, v, false);
-          else store8(static_cast<float*>(a.q_out) + o, v, false);
-        }
+        float v[2][8];
+        raw[i][0].get(v[0]);
+        raw[i][1].get(v[1]);
+        if (turn) rope<D>(v, cs[r], sn[r], k, a.nf, pairs);
+        if (r >= lo && r < hi)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int64_t to = o + i * L::kRows * a.ldo + g * (D / 2);
+            if (a.o_bf16) store8(static_cast<__nv_bfloat16*>(a.q_out) + to, v[g], false);
+            else store8(static_cast<float*>(a.q_out) + to, v[g], false);
+          }
       }
       continue;
     }
-    float v[L::kSteps][8];
+    float v[L::kSteps][2][8];
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < L::kSteps; ++i) {
-      raw[i].get(v[i]);
+      raw[i][0].get(v[i][0]);
+      raw[i][1].get(v[i][1]);
       if (i * L::kRows >= hi || (i + 1) * L::kRows <= lo) continue;  // no new row: zeros
-      if (!is_v && a.nf > 0) {
-        const int r = i * L::kRows + rr;
-        rope<D>(v[i], trig[r], cc, a.nf, a.interleaved);
+      const int r = i * L::kRows + rr;
+      if (turn) {
+        rope<D>(v[i], cs[r], sn[r], k, a.nf, pairs);
         if (r < lo || r >= hi)  // it has no angles, and whatever stands in their place may be a NaN
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+          for (int j = 0; j < 8; ++j) v[i][0][j] = v[i][1][j] = 0.0f;
       }
-      if (c.rotated) quad_rotate(v[i], lane & 3);
-      amax = max3_abs(amax, lane_amax(v[i]), 0.0f);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (c.rotated) quad_rotate(v[i][g], lane & 3);
+        amax = max3_abs(amax, lane_amax(v[i][g]), 0.0f);
+      }
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
@@ -201,41 +248,62 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvCache c, c
     // 127 = 1.984375 * 2^6
     const uint32_t bits = __float_as_uint(amax);
     int E = static_cast<int>(bits >> 23) - 127 - 6 + ((bits & 0x7FFFFFu) > 0x7E0000u);
-    E = min(max(E, kKvLow), kKvHigh);
-    uint8_t* const scale = c.scales + kv_scale_at(c, page, h, is_v) + p0 % c.page / kKvTokens;
-    int8_t* const codes = c.codes + kv_at(c, page, h, is_v) + static_cast<int64_t>(p0 % c.page) * D + 8 * cc;
+    E = max(E, kKvLow);
+    const bool clip = E > kKvHigh;  // past the largest scale: the codes saturate
+    E = min(E, kKvHigh);
+    const int in_page = p0 & (c.page - 1);
+    uint8_t* const scale = c.scales + kv_scale_at(c, page, h, is_v) + in_page / kKvTokens;
+    int8_t* const codes = c.codes + kv_at(c, page, h, is_v) + static_cast<int64_t>(in_page) * D + 8 * k;
     if (lo > 0) {
       const int was = *scale;
       bad = bad || was == 255;
       const int old = min(max(was - 127, kKvLow), kKvHigh);
       if (!bad && E > old) {  // the rows before: their codes, at the larger scale
         const float f = pow2i(old - E);
-        for (int r = rr; r < lo; r += L::kRows) {
-          uint2* const p = reinterpret_cast<uint2*>(codes + r * D);
-          const uint2 w = *p;
-          uint32_t o[2] = {0, 0};
+        for (int r = rr; r < lo; r += L::kRows)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int q = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
-            o[i >> 2] |= (static_cast<uint32_t>(__float2int_rn(static_cast<float>(q) * f)) & 0xFFu) << (8 * (i & 3));
+          for (int g = 0; g < 2; ++g) {
+            uint2* const p = reinterpret_cast<uint2*>(codes + r * D + g * (D / 2));
+            const uint2 w = *p;
+            uint32_t o[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int q = static_cast<int8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+              o[i >> 2] |= (static_cast<uint32_t>(__float2int_rn(static_cast<float>(q) * f)) & 0xFFu) << (8 * (i & 3));
+            }
+            *p = make_uint2(o[0], o[1]);
           }
-          *p = make_uint2(o[0], o[1]);
-        }
       }
       E = max(E, old);
     }
     const float inv = bad ? 0.0f : pow2i(-E);
+    if (bad || clip)
+#pragma unroll
+      for (int i = 0; i < L::kSteps; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) v[i][g][j] = bad ? 0.0f : fminf(fmaxf(v[i][g][j], -127.0f * pow2i(kKvHigh)), 127.0f * pow2i(kKvHigh));
+    // |v| / 2^E is at most 127: plus 1.5 * 2^23 it is that and the nearest integer (ties to even), whose low byte is
+    // the code in two's complement
+    constexpr float kMagic = 12582912.0f;
 #pragma unroll
     for (int i = 0; i < L::kSteps; ++i) {
       const int r = i * L::kRows + rr;
       if (r < lo || r >= hi) continue;
-      uint32_t o[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = bad ? 0 : min(max(__float2int_rn(v[i][j] * inv), -127), 127);
-        o[j >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (j & 3));
+      for (int g = 0; g < 2; ++g) {
+        uint32_t t[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 y = __ffma2_rn(make_float2(v[i][g][j], v[i][g][j + 1]), make_float2(inv, inv), make_float2(kMagic, kMagic));
+          t[j] = __float_as_uint(y.x);
+          t[j + 1] = __float_as_uint(y.y);
+        }
+        *reinterpret_cast<uint2*>(codes + r * D + g * (D / 2)) =
+            make_uint2(prmt(prmt(t[0], t[1], 0x0040u), prmt(t[2], t[3], 0x0040u), 0x5410u),
+                       prmt(prmt(t[4], t[5], 0x0040u), prmt(t[6], t[7], 0x0040u), 0x5410u));
       }
-      *reinterpret_cast<uint2*>(codes + r * D) = make_uint2(o[0], o[1]);
     }
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = static_cast<uint8_t>(bad ? 255 : E + 127);
