@@ -376,8 +376,8 @@ cudaError_t launch_kv8_append(const KvCache& c, const KvSeqs& s, const KvNew& a,
   const int64_t few = s.batch < s.tokens ? s.batch : s.tokens;
   const int64_t blocks = s.cu ? s.tokens / kKvTokens + 2 * few : static_cast<int64_t>(s.batch) * ((s.each + kKvTokens - 2) / kKvTokens + 1);
   const int64_t shares = (2 * c.heads + a.q_heads + kWarps - 1) / kWarps;
-  // heads over several CTAs while there are fewer than four CTAs an SM
-  int64_t y = (4 * static_cast<int64_t>(num_sms()) + blocks - 1) / blocks;
+  // heads over several CTAs while there are fewer than two CTAs an SM
+  int64_t y = (2 * static_cast<int64_t>(num_sms()) + blocks - 1) / blocks;
   y = y < shares ? y : shares;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y));
   int* err = device_error_word();
