@@ -246,46 +246,102 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, in
 
 // ---------------------------------------------------------------- bias, activation, residual
 // act(r + bias) + residual on tokens m0 .. m0 + lim - 1 of this lane's weight row n, in place
-// in the accumulators (r[i] = token i): nothing but the residual is read, a warp's lanes 32
-// consecutive values of a token.  SiLU and the tanh form of GELU are both x / (1 + exp(-z)),
-// z = x (c1 + c3 x^2), since (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)): one code for both.
+// in the accumulators (r[i] = token i), two tokens an instruction.
+//   SiLU and the tanh form of GELU: x / (1 + exp(-z)), z = x or 2 sqrt(2/pi) (x + 0.044715 x^3), since
+//     (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)).
+//   GELU: max(x, 0) - |x| q / 2, q = erfc(|x| / sqrt 2) by Abramowitz and Stegun, "Handbook of Mathematical
+//     Functions", 7.1.26 (off by 1.5e-7 at most): no branches, a quarter of erff's instructions (M333 N4600 K1184
+//     11.9 us with that).
+// The residual is all that is read: 32 tokens' loads of a warp's 32 neighbours go out together (one after the other,
+// each behind the sum before it, M4096 K5120 N17408 took 293 us), the first before the sums are there, the next
+// before these are stored; and its lines are asked into L2 while the products run.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 pair_of(float a) { return make_float2(a, a); }
+template <int ACT>
+__device__ __forceinline__ float2 activate(float2 x) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  if constexpr (ACT == kActRelu) {
+    return make_float2(x.x <= 0.0f ? 0.0f : x.x, x.y <= 0.0f ? 0.0f : x.y);
+  } else if constexpr (ACT == kActGelu) {
+    const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
+    const float2 d = __ffma2_rn(a, pair_of(0.3275911f * 0.70710678118654752f), pair_of(1.0f));
+    const float2 t = make_float2(rcp(d.x), rcp(d.y));
+    float2 q = __ffma2_rn(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));
+    q = __ffma2_rn(q, t, pair_of(0.5f * 1.421413741f));
+    q = __ffma2_rn(q, t, pair_of(0.5f * -0.284496736f));
+    q = __ffma2_rn(q, t, pair_of(0.5f * 0.254829592f));
+    q = __fmul2_rn(q, t);
+    const float2 u = __fmul2_rn(__fmul2_rn(x, x), pair_of(-0.5f * kLog2e));
+    q = __fmul2_rn(q, make_float2(ex2(u.x), ex2(u.y)));
+    return __ffma2_rn(make_float2(-a.x, -a.y), q, make_float2(x.x > 0.0f ? x.x : 0.0f, x.y > 0.0f ? x.y : 0.0f));
+  } else {
+    float2 u = pair_of(-kLog2e);
+    if constexpr (ACT == kActGeluTanh) u = __ffma2_rn(__fmul2_rn(x, x), pair_of(-kLog2e * 0.07135481282553567f), pair_of(-kLog2e * 1.5957691216057308f));
+    u = __fmul2_rn(u, x);
+    const float2 d = __fadd2_rn(make_float2(ex2(u.x), ex2(u.y)), pair_of(1.0f));
+    return __fmul2_rn(x, make_float2(rcp(d.x), rcp(d.y)));
+  }
+}
+template <int ACT, int NC>
+__device__ __forceinline__ void activate_all(uint32_t (&r)[NC]) {
+#pragma unroll
+  for (int i = 0; i < NC; i += 2) {
+    const float2 y = activate<ACT>(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+    r[i] = __float_as_uint(y.x);
+    r[i + 1] = __float_as_uint(y.y);
+  }
+}
+// Lines of the residual that this warp's epilogue will read, tokens m0 .. m0 + lim - 1 of weight rows n0 .. n0 + 31.
+__device__ __forceinline__ void ask_residual(const MxEpilogue& e, int64_t n0, int64_t N, int64_t m0, int lim) {
+  if (!e.residual || n0 >= N) return;
+  for (int i = threadIdx.x & 31; i < lim; i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(e.residual) + ((m0 + i) * e.ldr + n0) * (e.r_bf16 ? 2 : 4)));
+}
+// Residual of tokens m0 .. m0 + NC - 1 of weight row n; lanes and tokens past the last read the last.
 template <int NC>
-__device__ __forceinline__ void epilogue(uint32_t (&r)[NC], const MxEpilogue& e, int64_t n, int64_t N, int64_t m0, int lim) {
+__device__ __forceinline__ void load_residual(float (&v)[NC], const MxEpilogue& e, int64_t n, int64_t N, int64_t m0, int lim) {
+  if (!e.residual || lim <= 0) return;
+  const int64_t at = m0 * e.ldr + min(n, N - 1);
+  if (e.r_bf16) {
+    const __nv_bfloat16* const p = static_cast<const __nv_bfloat16*>(e.residual) + at;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] = __bfloat162float(p[min(i, lim - 1) * e.ldr]);
+  } else {
+    const float* const p = static_cast<const float*>(e.residual) + at;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] = p[min(i, lim - 1) * e.ldr];
+  }
+}
+template <int NC>
+__device__ __forceinline__ void add_residual(uint32_t (&r)[NC], const float (&v)[NC], const MxEpilogue& e) {
+  if (!e.residual) return;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + v[i]);
+}
+template <int NC>
+__device__ __forceinline__ void bias_act(uint32_t (&r)[NC], const MxEpilogue& e, int64_t n, int64_t N) {
   if (e.bias) {
-    const float b = n < N ? e.bias[n] : 0.0f;
+    const float2 b = pair_of(e.bias[min(n, N - 1)]);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + b);
-  }
-  if (e.act == kActRelu) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) <= 0.0f ? 0.0f : __uint_as_float(r[i]));
-  } else if (e.act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const float x = __uint_as_float(r[i]);
-      r[i] = __float_as_uint(0.5f * x * (1.0f + erff(x * 0.70710678118654752f)));
-    }
-  } else if (e.act != kActNone) {
-    const float c1 = e.act == kActSilu ? 1.0f : 1.5957691216057308f, c3 = e.act == kActSilu ? 0.0f : 0.07135481282553567f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const float x = __uint_as_float(r[i]);
-      r[i] = __float_as_uint(__fdividef(x, 1.0f + __expf(-x * fmaf(c3 * x, x, c1))));
+    for (int i = 0; i < NC; i += 2) {
+      const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), b);
+      r[i] = __float_as_uint(y.x);
+      r[i + 1] = __float_as_uint(y.y);
     }
   }
-  if (e.residual && n < N) {
-    if (e.r_bf16) {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.residual) + m0 * e.ldr + n;
-#pragma unroll
-      for (int i = 0; i < NC; ++i, p += e.ldr)
-        if (i < lim) r[i] = __float_as_uint(__uint_as_float(r[i]) + __bfloat162float(*p));
-    } else {
-      const float* p = static_cast<const float*>(e.residual) + m0 * e.ldr + n;
-#pragma unroll
-      for (int i = 0; i < NC; ++i, p += e.ldr)
-        if (i < lim) r[i] = __float_as_uint(__uint_as_float(r[i]) + *p);
-    }
-  }
+  if (e.act == kActRelu) activate_all<kActRelu>(r);
+  else if (e.act == kActSilu) activate_all<kActSilu>(r);
+  else if (e.act == kActGelu) activate_all<kActGelu>(r);
+  else if (e.act == kActGeluTanh) activate_all<kActGeluTanh>(r);
 }
 
 // ---------------------------------------------------------------- stores of Y
@@ -440,25 +496,35 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   }
 
   __syncwarp();
-  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p) && !S.abort);
-  tc_fence_after();
+  if (EPI && warp < 4) {
+    grid_dep_wait();  // the residual and the bias may be what the kernel in front of this one writes
+    ask_residual(p.ep, n0 + 32 * warp, p.N, m0, static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0)));
+  }
   const int64_t n = n0 + 32 * (warp & 3) + lane;
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   const int tok = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
   constexpr int NC = NT < 32 ? NT : 32;  // columns per pass
+  float res[NC];
+  if (EPI && warp < 4 && split == 1) load_residual(res, p.ep, n, p.N, m0, tok);
+  const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p) && !S.abort);
+  tc_fence_after();
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   constexpr int kEsz = BF16 ? 2 : 4;
   uint8_t* const y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * kEsz;
-  if (EPI) grid_dep_wait();  // the residual and the bias may be what is in front of this kernel's
   if (split == 1) {
+    constexpr int kUnroll = EPI ? 1 : NT / NC;  // the epilogue's code once: its first fetch is a part of such a call's time
     if (whole)
-#pragma unroll
+#pragma unroll kUnroll
       for (int c = 0; c < NT; c += NC) {
         uint32_t r[NC];
 #pragma unroll
         for (int i = 0; i < NC; i += 16) tmem_ld16(lanes + c + i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
 #pragma unroll
         for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
-        if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0 + c, tok - c);
+        if constexpr (EPI) {
+          bias_act(r, p.ep, n, p.N);
+          add_residual(r, res, p.ep);
+          if (c + NC < NT) load_residual(res, p.ep, n, p.N, m0 + c + NC, tok - c - NC);
+        }
         store_cols<BF16>(r, y + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
   } else {
@@ -498,7 +564,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         }
         uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
         const int64_t m = static_cast<int64_t>(rank) * share + i;
-        if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0 + m, static_cast<int>(tok - m));
+        if constexpr (EPI) {
+          float v4[4];
+          load_residual(v4, p.ep, n, p.N, m0 + m, static_cast<int>(tok - m));
+          bias_act(r, p.ep, n, p.N);
+          add_residual(r, v4, p.ep);
+        }
         store_cols<BF16>(r, y + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
       }
     }
@@ -672,6 +743,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t seg = 0;
     bool live = true;  // cleared when a wait gave up; the barrier below still counts this warp
     for (; more; more = work.next(p)) {
+      if (EPI && work.s0 == 0) {
+        const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * kMaxTok + 128 * (warp >> 2);
+        ask_residual(p.ep, static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3), p.N, m0,
+                     static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
+      }
       live = live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, seg & 1, p));
       ++seg;
       uint32_t r[128];
@@ -731,8 +807,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t n = static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3) + lane;
       const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * kMaxTok + 128 * (warp >> 2);
       const int lim = static_cast<int>(min(static_cast<int64_t>(128), p.M - m0));
-      if constexpr (EPI) epilogue(r, p.ep, n, p.N, m0, lim);
-      store_cols<BF16>(r, static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N, lim);
+      uint8_t* const y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4);
+      if constexpr (EPI) {
+        // 16 tokens at a time: beside the 128 accumulators no more fit the 168 registers that ten warps leave
+        float res[16];
+        load_residual(res, p.ep, n, p.N, m0, lim);
+        bias_act(r, p.ep, n, p.N);
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          uint32_t (&part)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c);
+          add_residual(part, res, p.ep);
+          if (c < 112) load_residual(res, p.ep, n, p.N, m0 + c + 16, lim - c - 16);
+          store_cols<BF16>(part, y + c * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N, lim - c);
+        }
+      } else {
+        store_cols<BF16>(r, y, p.ldy, n, p.N, lim);
+      }
     }
   }
   tc_fence_before();
