@@ -32,6 +32,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -140,6 +141,13 @@ class _Kv8Attn(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("ldqh", ctypes.c_int64),
                 ("ldo", ctypes.c_int64), ("ldoh", ctypes.c_int64), ("q_heads", ctypes.c_int), ("q_dtype", ctypes.c_int),
                 ("o_dtype", ctypes.c_int), ("causal", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+# The same laid out by struct, which takes a third of the time of a ctypes structure: what the calls pass.
+_pack_epilogue = struct.Struct("2Pq2i").pack
+_pack_kv8_seqs = struct.Struct("3P4q").pack
+_pack_kv8_new = struct.Struct("5P8q5i").pack
+_pack_kv8_attn = struct.Struct("2P4q5if").pack
 
 
 _LIB = None
@@ -1081,35 +1089,31 @@ def mxfp4_gemm_epilogue(w: MxFp4, a: MxFp4, bias: torch.Tensor | None = None, ac
         raise ValueError("w and a must be MxFp4 operands on the GPU")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None")
-    M, N = a._rows, w._rows
-    device = w._buf.device
-    b = r = None
-    ldr = r_dtype = 0
+    M, N, at = a._rows, w._rows, w._buf.get_device()
+    b = r = ldr = r_dtype = 0
     if bias is not None:
-        if not bias.is_cuda or bias.dtype != torch.float32 or bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
+        if bias.get_device() != at or bias.dtype != torch.float32 or bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
             _cuda(bias, "bias")
-            raise ValueError("bias must be a contiguous fp32 tensor of N values")
+            raise ValueError("bias must be a contiguous fp32 tensor of N values on w's device")
         b = bias.data_ptr()
     if residual is not None:
         ldr = _rows(residual, "residual", (M, N))
         r, r_dtype = residual.data_ptr(), _DTYPE[residual.dtype]
-    for t, name in ((a._buf, "a"), (bias, "bias"), (residual, "residual"), (y, "y")):
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, w on {device}")
+    if a._buf.get_device() != at or (residual is not None and residual.get_device() != at) or (y is not None and y.get_device() != at):
+        raise ValueError(f"a, residual and y must be on w's device, cuda:{at}")
     if y is None:
-        ldy = N
+        ldy, device = N, w._buf.device
         y = (torch.empty(M, N, dtype=dtype, device=device) if stream is None
              else _made(stream, torch.empty, M, N, dtype=dtype, device=device))
     else:
-        ldy = _rows(y, "y", (M, N))
-    e = _Epilogue(b, r, ldr, r_dtype, ACTIVATIONS[activation])
+        ldy, dtype = _rows(y, "y", (M, N)), y.dtype
     lib, st = load_library(), _stream(stream)
     if ws is True:  # batches of up to 128 tokens never use one
         need = lib.mxfp4_gemm_workspace_bytes(M, N, w._K) if M > 128 else 0
         ws = gemm_workspace(M, N, w._K, y.device, st, need) if need else None
     ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
-    _check(lib.mxfp4_gemm_epilogue(w._at, a._at, ctypes.addressof(e), y.data_ptr(), _DTYPE.get(y.dtype, -1), ldy, ws_ptr,
-                                   ws_bytes, st))
+    _check(lib.mxfp4_gemm_epilogue(w._at, a._at, _pack_epilogue(b, r, ldr, r_dtype, ACTIVATIONS[activation]), y.data_ptr(),
+                                   _DTYPE.get(dtype, -1), ldy, ws_ptr, ws_bytes, st))
     return y
 
 
@@ -1213,7 +1217,7 @@ class KvCache8:
     descriptor is kept.  rotated: keys and values carry the H32 rotation.
     """
 
-    __slots__ = ("_codes", "_scales", "_rotated", "_desc", "_at", "_index")
+    __slots__ = ("_codes", "_scales", "_rotated", "_desc", "_at", "_index", "_heads", "_dim")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rotated: bool = True):
         if codes.dtype != torch.int8 or codes.dim() != 5 or codes.shape[2] != 2 or not codes.is_contiguous():
@@ -1228,7 +1232,7 @@ class KvCache8:
         if scales.device != codes.device:
             raise ValueError(f"scales are on {scales.device}, codes on {codes.device}")
         self._codes, self._scales, self._rotated = codes, scales, bool(rotated)
-        self._index = codes.get_device()
+        self._index, self._heads, self._dim = codes.get_device(), heads, dim
         self._desc = _Kv8Desc(codes.data_ptr(), scales.data_ptr(), pages, heads, page, dim,
                               TAG_KV8 | TAG_ROTATED if rotated else TAG_KV8)
         self._at = ctypes.addressof(self._desc)
@@ -1287,33 +1291,41 @@ def rope_freqs(dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     return base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
 
 
-def _kv8_seqs(cache, table, lens, cu, tokens: int) -> _Kv8Seqs:
+def _kv8_seqs(cache, table, lens, cu, tokens: int) -> bytes:
+    """The sequences of a call, checked, as the C struct."""
     if not isinstance(cache, KvCache8):
         raise ValueError(f"cache must be KvCache8, not {type(cache).__name__}")
     at = cache._index
     if at < 0:
         raise ValueError("the cache must be on the GPU (there is no CPU path)")
-    if at != torch.cuda.current_device():
+    if at != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on cuda:{at}, the current device is cuda:{torch.cuda.current_device()}")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.get_device() != at or (table.stride(1) != 1 and table.shape[1] > 1):
+    shape, st = table.shape, table.stride()
+    if len(shape) != 2 or table.dtype != torch.int32 or table.get_device() != at or (st[1] != 1 and shape[1] > 1):
         raise ValueError("table must be a 2-D int32 tensor with unit stride along its rows, on the cache's device")
-    batch, width = table.shape
+    batch, width = shape
     if lens.dtype != torch.int32 or lens.shape != (batch,) or lens.get_device() != at or (batch > 1 and lens.stride(0) != 1):
         raise ValueError("lens must be a contiguous int32 tensor of one length per row of table, on the cache's device")
     if cu is not None and (cu.dtype != torch.int32 or cu.shape != (batch + 1,) or cu.get_device() != at or (batch and cu.stride(0) != 1)):
         raise ValueError("cu must be a contiguous int32 tensor of batch + 1 offsets, on the cache's device")
-    return _Kv8Seqs(table.data_ptr(), lens.data_ptr(), None if cu is None else cu.data_ptr(), batch, width,
-                    table.stride(0) if batch > 1 else width, tokens)
+    return _pack_kv8_seqs(table.data_ptr(), lens.data_ptr(), 0 if cu is None else cu.data_ptr(), batch, width,
+                          st[0] if batch > 1 else width, tokens)
 
 
-def _heads(t: torch.Tensor, name: str, cache: KvCache8, heads: int, tokens: int | None = None, dtype=None):
-    """Checks [tokens][heads][dim] rows (bf16 or fp32, unit stride along dim); strides of tokens and of heads."""
-    if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache._desc.dim or (tokens is not None and t.shape[0] != tokens)
-            or t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype) or t.stride(2) != 1 or t.get_device() != cache._index):
+def _kv8_stream(cache: KvCache8, stream) -> int:  # as _stream, on a device that is known to be the current one
+    return torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _stream(stream)
+
+
+def _kv8_rows(t: torch.Tensor, name: str, cache: KvCache8, heads: int, tokens: int, dtype=None):
+    """Checks [tokens][heads][dim] rows (bf16 or fp32, unit stride along dim); strides of tokens and of heads, and type."""
+    st, own = t.stride(), t.dtype
+    code = _DTYPE.get(own)
+    if (code is None or t.shape != (tokens, heads, cache._dim) or st[2] != 1 or t.get_device() != cache._index
+            or (dtype is not None and own != dtype)):
         _cuda(t, name)
-        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}][{heads}][{cache.dim}] "
-                         f"{dtype or 'bf16 or fp32'} with unit stride along dim, on the cache's device")
-    return t.stride(0), t.stride(1)
+        raise ValueError(f"{name} must be [{tokens}][{heads}][{cache.dim}] {dtype or 'bf16 or fp32'} with unit stride along dim, "
+                         "on the cache's device")
+    return st[0], st[1], code
 
 
 def kv8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -1327,29 +1339,28 @@ def kv8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, table: torch.T
     interleaved (2i, 2i + 1).  q [tokens][q_heads][dim] is rotated into q_out (None: in place), which is returned.
     A page, length or offset out of range is skipped, and reported by w4a4_check.
     """
-    T = k.shape[0]
+    T = k.shape[0] if k.dim() == 3 else -1
     s = _kv8_seqs(cache, table, lens, cu, T)
-    H = cache._desc.heads
-    ldk, ldkh = _heads(k, "k", cache, H)
-    ldv, ldvh = _heads(v, "v", cache, H, T, k.dtype)
-    qp = op = fp = None
-    ldq = ldqh = ldo = ldoh = q_heads = nf = o_dtype = 0
+    H, dtype = cache._heads, k.dtype
+    ldk, ldkh, x_dtype = _kv8_rows(k, "k", cache, H, T)
+    ldv, ldvh, _ = _kv8_rows(v, "v", cache, H, T, dtype)
+    qp = op = fp = ldq = ldqh = ldo = ldoh = q_heads = nf = o_dtype = 0
     if q is not None:
-        q_heads = q.shape[1]
-        ldq, ldqh = _heads(q, "q", cache, q_heads, T, k.dtype)
+        q_heads = q.shape[1] if q.dim() == 3 else -1
+        ldq, ldqh, _ = _kv8_rows(q, "q", cache, q_heads, T, dtype)
         if q_out is None:
             q_out = q
-        ldo, ldoh = _heads(q_out, "q_out", cache, q_heads, T)
-        qp, op, o_dtype = q.data_ptr(), q_out.data_ptr(), _DTYPE[q_out.dtype]
+        ldo, ldoh, o_dtype = _kv8_rows(q_out, "q_out", cache, q_heads, T)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if freqs is not None:
         if freqs.dtype != torch.float64 or freqs.dim() != 1 or freqs.get_device() != cache._index or not freqs.is_contiguous():
             raise ValueError("freqs must be a contiguous 1-D fp64 tensor on the cache's device")
         fp, nf = freqs.data_ptr(), freqs.shape[0]
-    n = _Kv8New(k.data_ptr(), v.data_ptr(), qp, op, fp, ldk, ldkh, ldv, ldvh, ldq, ldqh, ldo, ldoh, q_heads, nf,
-                interleaved, _DTYPE[k.dtype], o_dtype)
-    _check(load_library().kv8_append(cache._at, ctypes.addressof(s), ctypes.addressof(n), _stream(stream)))
+    n = _pack_kv8_new(k.data_ptr(), v.data_ptr(), qp, op, fp, ldk, ldkh, ldv, ldvh, ldq, ldqh, ldo, ldoh, q_heads, nf,
+                      interleaved, x_dtype, o_dtype)
+    _check(load_library().kv8_append(cache._at, s, n, _kv8_stream(cache, stream)))
     return q_out
 
 
@@ -1359,18 +1370,15 @@ def kv8_read(cache: KvCache8, table: torch.Tensor, lens: torch.Tensor, tokens: i
     """The values (k, v) [tokens][heads][dim] of each sequence's last tokens, as kv8_append takes them (a rotation by
     H32 is not undone); rows past cu[-1] are left as they are."""
     s = _kv8_seqs(cache, table, lens, cu, tokens)
-    H, D = cache._desc.heads, cache._desc.dim
-    made = []
-    for t in (k, v):
-        if t is None:
-            t = (torch.empty(tokens, H, D, dtype=dtype, device=cache.device) if stream is None
-                 else _made(stream, torch.empty, tokens, H, D, dtype=dtype, device=cache.device))
-        made.append(t)
-    k, v = made
-    ldk, ldkh = _heads(k, "k", cache, H, tokens)
-    ldv, ldvh = _heads(v, "v", cache, H, tokens, k.dtype)
-    _check(load_library().kv8_read(cache._at, ctypes.addressof(s), k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], ldk, ldkh,
-                                   ldv, ldvh, _stream(stream)))
+    H, D = cache._heads, cache._dim
+    if (k is None) != (v is None):
+        raise ValueError("k and v: both or neither")
+    if k is None:
+        k, v = (torch.empty(2, tokens, H, D, dtype=dtype, device=cache._codes.device) if stream is None
+                else _made(stream, torch.empty, 2, tokens, H, D, dtype=dtype, device=cache._codes.device))
+    ldk, ldkh, code = _kv8_rows(k, "k", cache, H, tokens)
+    ldv, ldvh, _ = _kv8_rows(v, "v", cache, H, tokens, k.dtype)
+    _check(load_library().kv8_read(cache._at, s, k.data_ptr(), v.data_ptr(), code, ldk, ldkh, ldv, ldvh, _kv8_stream(cache, stream)))
     return k, v
 
 
@@ -1389,22 +1397,25 @@ def kv8_attention(q: torch.Tensor, cache: KvCache8, table: torch.Tensor, lens: t
     ws: True = the cached per-stream workspace (in a capture one of the graph's own), a tensor = that workspace (its
     first MiB zero before its first use), None/False = a sequence is not cut over the SMs.
     """
-    T, Hq = q.shape[0], q.shape[1]
+    T, Hq = q.shape[:2] if q.dim() == 3 else (-1, -1)
     s = _kv8_seqs(cache, table, lens, cu, T)
-    ldq, ldqh = _heads(q, "q", cache, Hq)
+    D, at = cache._dim, cache._index
+    ldq, ldqh, q_dtype = _kv8_rows(q, "q", cache, Hq, T)
     if out is None:
-        out = (torch.empty(T, Hq, cache._desc.dim, dtype=dtype, device=q.device) if stream is None
-               else _made(stream, torch.empty, T, Hq, cache._desc.dim, dtype=dtype, device=q.device))
-    ldo, ldoh = _heads(out, "out", cache, Hq, T)
-    D = cache._desc.dim
-    a = _Kv8Attn(q.data_ptr(), out.data_ptr(), ldq, ldqh, ldo, ldoh, Hq, _DTYPE[q.dtype], _DTYPE[out.dtype], causal, window,
-                 D ** -0.5 if scale is None else scale)
-    lib, st = load_library(), _stream(stream)
+        out = q.new_empty((T, Hq, D), dtype=dtype) if stream is None else _made(stream, q.new_empty, (T, Hq, D), dtype=dtype)
+    ldo, ldoh, o_dtype = _kv8_rows(out, "out", cache, Hq, T)
+    a = _pack_kv8_attn(q.data_ptr(), out.data_ptr(), ldq, ldqh, ldo, ldoh, Hq, q_dtype, o_dtype, causal, window,
+                       D ** -0.5 if scale is None else scale)
+    lib, st = load_library(), _kv8_stream(cache, stream)
     if ws is True:
         need = lib.kv8_attention_workspace_bytes(D)
         # two graphs of one stream may be replayed side by side: each has its own
-        ws = (_made(st, _graph_workspace, need, q.device) if _capturing(stream)
-              else gemm_workspace(0, 0, 0, q.device, st, need))
+        if torch._C._cuda_isCurrentStreamCapturing() if stream is None else _capturing(stream):
+            ws = _made(st, _graph_workspace, need, q.device)
+        else:
+            ws = _GEMM_WS.get((at, st))
+            if ws is None or ws.numel() < need:
+                ws = gemm_workspace(0, 0, 0, q.device, st, need)
     ws_ptr, ws_bytes = (None, 0) if ws is None or ws is False else (ws.data_ptr(), ws.numel() * ws.element_size())
-    _check(lib.kv8_attention(cache._at, ctypes.addressof(s), ctypes.addressof(a), ws_ptr, ws_bytes, st))
+    _check(lib.kv8_attention(cache._at, s, a, ws_ptr, ws_bytes, st))
     return out

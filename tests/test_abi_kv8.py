@@ -164,3 +164,22 @@ def test_host_tensors_are_refused():
 def test_rope_freqs():
     f = w4.rope_freqs(64, 1e4, device="cpu")
     assert f.dtype == torch.float64 and f.shape == (32,) and f[0] == 1 and abs(float(f[16]) - 1e-2) < 1e-15
+
+
+def test_packed_structures_are_the_c_ones():
+    """The bytes that the binding passes, against ctypes' layout of the same fields."""
+    for pack, kind, values in ((w4._pack_epilogue, _Epilogue, (1, 2, 3, 4, 5)), (w4._pack_kv8_seqs, _Kv8Seqs, range(1, 8)),
+                               (w4._pack_kv8_new, _Kv8New, range(1, 19)), (w4._pack_kv8_attn, _Kv8Attn, (*range(1, 12), 0.5))):
+        c = kind(*values)
+        b = pack(*values)
+        assert b == bytes(c)[: len(b)]
+        assert len(b) >= max(getattr(kind, n).offset + getattr(kind, n).size for n, _ in kind._fields_)
+
+
+def test_host_shapes_are_refused():
+    c, i = host_cache(), torch.zeros(1, 2, dtype=torch.int32)
+    for bad in (torch.zeros(64), torch.zeros(1, 64), torch.zeros(1, 2, 2, 64)):
+        with pytest.raises(ValueError):
+            w4.kv8_attention(bad, c, i, i[0, :1])
+        with pytest.raises(ValueError):
+            w4.kv8_append(c, bad, bad, i, i[0, :1])
