@@ -8,11 +8,12 @@
 // one a row and key; and the way from codes to fp16.
 //
 // Warps: 0-3 and 4-7 the softmax of 128 rows each, a row a thread, so that no maximum crosses
-// lanes; 8 issues the MMAs; 9-15 take blocks of 16 keys or values in turn, load their codes ahead
-// into registers and write them as the products' B operands: keys are rows of 128 bytes in the
-// 128-byte swizzle either way, K read along d (K-major), V along the keys (MN-major).  The two
-// row tiles take turns: while one's weights are computed the other's products run.  With heads
-// of 256 TMEM has room for one row tile with two S, and the next tile's S runs beside the softmax.
+// lanes; 8 issues the MMAs; 9 looks up pages and scales and copies blocks of 16 keys' codes and
+// values' codes (cp.async.bulk) to their rings; 10-15 take these blocks in turn and write them as the
+// products' B operands: keys are rows of 128 bytes in the 128-byte swizzle either way, K read along
+// d (K-major), V along the keys (MN-major).  The two row tiles take turns: while one's weights are
+// computed the other's products run.  With heads of 256 TMEM has room for one row tile with two S,
+// and the next tile's S runs beside the softmax.
 //
 // The running maximum is looked for, and O rescaled, only where a weight might not fit fp16.
 #include <cuda_bf16.h>
@@ -29,6 +30,7 @@ constexpr int kBK = 128;                         // keys of a tile
 constexpr int kBlocks = kBK / kKvTokens;         // blocks of 16 keys, each with its scales
 constexpr int64_t kWaitCycles = int64_t(1) << 31;  // 1.04 s at the top clock, longer below it
 constexpr size_t kWsCounters = size_t(1) << 20;
+constexpr int kConvertWarps = 6;
 constexpr float kMost = 32768.0f;  // of 16 weights together, below fp16's largest
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -44,13 +46,15 @@ struct Shape {
   static constexpr int kBufs = D == 256 ? 1 : 2;    // converted tiles of K, and of V
   static constexpr int kTile = kBK * D * 2;         // bytes of one
   static constexpr int kPanel = 128 * 128;          // bytes of 64 elements of 128 rows
-  static constexpr int kQ = 0, kK = kQ + kRows * D * 2, kV = kK + kBufs * kTile;
+  static constexpr int kQ = 0, kK = kQ + kRows * D * 2, kV = kK + kBufs * kTile, kRaw = kV + kBufs * kTile;
+  static constexpr int kBlock = kKvTokens * D;      // bytes of a block's codes
+  static constexpr int kDepth = D == 256 ? 1 : 2, kSlots = kConvertWarps * kDepth;  // of them in a warp's ring, in all rings
   static constexpr int kPieces = D / 32;              // 16-code pieces of a lane in a block of 16 keys
   static constexpr int kPrefix = kK;  // find_work's sums, before the first tile of K
-  static constexpr int kSmem = 1024 + kV + kBufs * kTile;
+  static constexpr int kSmem = 1024 + kRaw + kSlots * kBlock;
   // registers a thread: warps 0-3, 4-7 (which heads of 256 leave idle), 8-11 and 12-15;
   // together no more than the launch's 4 x 128
-  static constexpr int kRegs0 = 176, kRegs1 = D == 256 ? 24 : 176, kRegs2 = D == 256 ? 152 : 80;
+  static constexpr int kRegs0 = 176, kRegs1 = D == 256 ? 24 : 176, kRegs2 = D == 256 ? 128 : 80;
   static_assert(kRegs0 + kRegs1 + 2 * kRegs2 <= 4 * 128);
   static constexpr int kS = 0, kO = 256;            // TMEM columns
   static constexpr int kPart = kRows * (D + 2);     // floats of a cut tile's part
@@ -70,11 +74,13 @@ struct PromptArgs {
 };
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], sc_full[4];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], sc_full[4], sc_empty[4];
   uint64_t p_ready[2][2];  // [S][half of the keys]
   uint64_t pv_done[2][2];  // [row tile][half]
   uint64_t o_done[2];      // once, at the end
   uint64_t q_full;         // once
+  uint64_t raw_full[12], raw_empty[12];  // [warp][its ring]
+  int raw_none[12];        // no page: nothing was copied
   uint32_t tmem;
   volatile int abort;
 };
@@ -290,56 +296,87 @@ __device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int6
   return w.part < w.parts;
 }
 
-// Blocks of 16 keys of tiles 0 .. n - 1, in the order of the tiles, K's eight and then V's, of which warp `first` of
-// `kWarps` takes every kWarps-th: codes to fp16 in the swizzled rows of the tile's buffer, and with K's the block's
-// scales.  A lane takes 16 codes of rows lane / 4 and lane / 4 + 8 in every panel of 64: eight neighbours read 64 bytes
-// of two rows each, write on different banks, and find the swizzle's share of an address in a register.
-constexpr int kConvertWarps = 7;
+// Blocks of 16 keys of tiles 0 .. n - 1 in the order of the tiles, K's eight and then V's: their codes to the rings
+// of the warps that take them, by one warp, and each tile's scales.
 template <int D>
-__device__ __forceinline__ void convert(const PromptArgs& p, const Work& w, int key0, int n, int first, uint8_t* smem, Bars& S,
-                                        float (&sc)[4][3][kBlocks]) {
+__device__ __forceinline__ void copy_codes(const PromptArgs& p, const Work& w, int key0, int n, uint8_t* smem, Bars& S, float (&sc)[4][3][kBlocks]) {
+  using C = Shape<D>;
+  const int lane = threadIdx.x & 31, v = (lane >> 3) & 1, b = lane & 7;  // lanes 0-15: the tile's blocks
+  const auto page_of = [&](int j) {  // of tile j's block, -1: none
+    const int t = key0 + j * kBK + b * kKvTokens;
+    return lane < 16 && j < n && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
+  };
+  int next = page_of(0);
+  for (int j = 0; j < n; ++j) {
+    const int page = next, t = key0 + j * kBK + b * kKvTokens, in_page = t & (p.c.page - 1);
+    next = page_of(j + 1);
+    bool ok = true;
+    // as many lanes at a time as there are places: a later one may wait for an earlier one's block to be taken
+#pragma unroll 1
+    for (int from = 0; from < 16; from += C::kSlots, __syncwarp()) {
+      if (lane < from || lane >= min(16, from + C::kSlots)) continue;
+      const int u = 16 * j + lane, turn = u / kConvertWarps, slot = u % kConvertWarps * C::kDepth + turn % C::kDepth, round = turn / C::kDepth;
+      if (round > 0) ok = wait_bar(S, &S.raw_empty[slot], (round - 1) & 1, p);
+      if (ok) {
+        S.raw_none[slot] = page < 0;
+        if (page < 0) {
+          mbar_arrive(&S.raw_full[slot]);
+        } else {
+          mbar_expect_tx(&S.raw_full[slot], C::kBlock);
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           su32(smem + C::kRaw + slot * C::kBlock)),
+                       "l"(p.c.codes + kv_at(p.c, page, w.head, v) + static_cast<int64_t>(in_page) * D), "r"(C::kBlock), "r"(su32(&S.raw_full[slot]))
+                       : "memory");
+        }
+      }
+    }
+    // a block without a page, or past the sequence: no weight (its codes are zeros)
+    const int byte = page < 0 ? -1 : p.c.scales[kv_scale_at(p.c, page, w.head, v) + in_page / kKvTokens];
+    // not k_empty: this tile's own products may be done by now, and a parity does not tell two phases on
+    if (j >= 4) ok = ok && wait_bar(S, &S.sc_empty[j & 3], (j / 4 - 1) & 1, p);
+    if (!__all_sync(0xFFFFFFFFu, ok)) return;
+    const float f = kv_scale(byte);
+    if (lane < 8) {
+      sc[j & 3][0][b] = byte < 0 ? 0.0f : f;
+    } else if (lane < 16) {
+      sc[j & 3][1][b] = byte < 0 ? kNegInf : byte == 255 ? f : static_cast<float>(byte - 127);
+      sc[j & 3][2][b] = byte < 0 ? 0.0f : byte == 255 ? f : ex2(static_cast<float>(127 - byte));
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.sc_full[j & 3]);
+  }
+}
+
+// The ring's blocks, of which warp `first` of kConvertWarps takes every kConvertWarps-th: to fp16 in the swizzled rows
+// of the tile's buffer.  A lane takes 16 codes of rows lane / 4 and lane / 4 + 8 in every panel of 64: eight
+// neighbours write on different banks, and find the swizzle's share of an address in a register.  (With the codes
+// loaded to registers, the fence before the MMAs waited for the next block's loads as well: 1000 cycles a block.)
+template <int D>
+__device__ __forceinline__ void convert(const PromptArgs& p, int n, int first, uint8_t* smem, Bars& S) {
   using C = Shape<D>;
   const int lane = threadIdx.x & 31, units = n * 2 * kBlocks;
   const uint32_t k0 = su32(smem + C::kK) + (lane >> 2) * 128;
   const uint32_t lo = k0 + (((2 * (lane & 3)) ^ (lane >> 2)) << 4), hi = k0 + (((2 * (lane & 3) + 1) ^ (lane >> 2)) << 4);
-  const int64_t v_off = static_cast<int64_t>(p.c.page) * D;
-  const auto page_of = [&](int u) {  // of unit u, -1: none
-    const int t = key0 + (u >> 4) * kBK + (u & 7) * kKvTokens;
-    return u < units && t < w.q.len ? kv_page(p.s, p.c, w.b, t, p.err) : -1;
-  };
-  struct Unit {
-    uint4 x[C::kPieces];
-    int scale;  // lane 0: K's byte, lane 1: V's; -1: no page
-  };
-  const auto load = [&](int u, int page, Unit& o) {
-    const int t = key0 + (u >> 4) * kBK + (u & 7) * kKvTokens, v = (u >> 3) & 1, at = t & (p.c.page - 1);
-    o.scale = -1;
-    if (page >= 0) {
-      const int8_t* const src = p.c.codes + kv_at(p.c, page, w.head, 0) + (v ? v_off : 0) + static_cast<int64_t>(at + (lane >> 2)) * D + 16 * (lane & 3);
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) o.x[i] = __ldg(reinterpret_cast<const uint4*>(src + (i & 1) * 8 * D + (i >> 1) * 64));
-      if (!v && lane < 2) o.scale = p.c.scales[kv_scale_at(p.c, page, w.head, lane) + at / kKvTokens];
-    } else {
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) o.x[i] = make_uint4(0, 0, 0, 0);
-    }
-  };
-  const auto store = [&](int u, const Unit& o) {
+  // The ring is the warp's own: whoever waits for a round of a place has seen the one before, so that a phase's parity
+  // says which of the two it is.
+  for (int u = first, turn = 0; u < units; u += kConvertWarps, ++turn) {
+    const int slot = first * C::kDepth + turn % C::kDepth, round = turn / C::kDepth;
     const int j = u >> 4, v = (u >> 3) & 1, b = u & 7, buf = j % C::kBufs;
-    if (j >= C::kBufs && !__all_sync(0xFFFFFFFFu, wait_bar(S, v ? &S.v_empty[buf] : &S.k_empty[buf], (j / C::kBufs - 1) & 1, p))) return false;
-    if (!v) {
-      // a block without a page, or past the sequence: no weight (its codes are zeros)
-      const float f = kv_scale(o.scale);
-      if (lane == 0) sc[j & 3][0][b] = o.scale < 0 ? 0.0f : f;
-      if (lane == 1) {
-        sc[j & 3][1][b] = o.scale < 0 ? kNegInf : o.scale == 255 ? f : static_cast<float>(o.scale - 127);
-        sc[j & 3][2][b] = o.scale < 0 ? 0.0f : o.scale == 255 ? f : ex2(static_cast<float>(127 - o.scale));
-      }
-    }
+    if (!__all_sync(0xFFFFFFFFu, wait_bar(S, &S.raw_full[slot], round & 1, p))) return;
+    const bool none = S.raw_none[slot] != 0;
+    const uint8_t* const raw = smem + C::kRaw + slot * C::kBlock + (lane >> 2) * D + 16 * (lane & 3);
+    uint4 x[C::kPieces];
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i)
+      x[i] = none ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(raw + (i & 1) * 8 * D + (i >> 1) * 64);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.raw_empty[slot]);
+    if (j >= C::kBufs && !__all_sync(0xFFFFFFFFu, wait_bar(S, v ? &S.v_empty[buf] : &S.k_empty[buf], (j / C::kBufs - 1) & 1, p))) return;
     const uint32_t at = (v ? C::kV - C::kK : 0) + buf * C::kTile + b * kKvTokens * 128;
 #pragma unroll
     for (int i = 0; i < C::kPieces; ++i) {
-      const uint32_t a = o.x[i].x ^ 0x80808080u, b4 = o.x[i].y ^ 0x80808080u, c = o.x[i].z ^ 0x80808080u, d = o.x[i].w ^ 0x80808080u;
+      const uint32_t a = x[i].x ^ 0x80808080u, b4 = x[i].y ^ 0x80808080u, c = x[i].z ^ 0x80808080u, d = x[i].w ^ 0x80808080u;
       const uint32_t to = at + (i & 1) * 1024 + (i >> 1) * C::kPanel;
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(lo + to), "r"(codes_half2(a, 0x4140u)), "r"(codes_half2(a, 0x4342u)),
                    "r"(codes_half2(b4, 0x4140u)), "r"(codes_half2(b4, 0x4342u))
@@ -350,25 +387,7 @@ __device__ __forceinline__ void convert(const PromptArgs& p, const Work& w, int 
     }
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(v ? &S.v_full[buf] : &S.k_full[buf]);
-      if (!v) mbar_arrive(&S.sc_full[j & 3]);
-    }
-    return true;
-  };
-  Unit a, b;
-  int u = first, page = page_of(u + kConvertWarps);
-  load(u, page_of(u), a);
-  while (u < units) {
-    load(u + kConvertWarps, page, b);
-    page = page_of(u + 2 * kConvertWarps);
-    if (!store(u, a)) return;
-    u += kConvertWarps;
-    if (u >= units) return;
-    load(u + kConvertWarps, page, a);
-    page = page_of(u + 2 * kConvertWarps);
-    if (!store(u, b)) return;
-    u += kConvertWarps;
+    if (lane == 0) mbar_arrive(v ? &S.v_full[buf] : &S.k_full[buf]);
   }
 }
 
@@ -443,8 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       mbar_init(&S.pv_done[i][1], 1);
       mbar_init(&S.o_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], kBlocks);
+    for (int i = 0; i < 4; ++i) mbar_init(&S.sc_full[i], 1);
     mbar_init(&S.q_full, 8);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&S.raw_full[i], 1);
+      mbar_init(&S.raw_empty[i], 1);
+    }
 
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -467,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
     if (tid == 0) {
       if (!some) w.rows = 0;
       sm_work = w;
+      for (int i = 0; i < 4; ++i) mbar_init(&S.sc_empty[i], C::kTiles == 2 && w.rows > 128 ? 8 : 4);  // the softmax's warps
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   }
   __syncthreads();
@@ -482,14 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
 
   if (warp >= 8) {
     if constexpr (C::kRegs2 < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegs2));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs2));
-    if (p.delay > 0 && warp != 8) {
+    if (p.delay > 0 && warp == 9) {
       const int64_t t0 = clock64();
       while (clock64() - t0 < p.delay) {
       }
     }
-    if (warp > 8) {
-      convert<D>(p, w, key0, n, warp - 9, smem, S, sm_sc);
+    if (warp > 9) {
+      convert<D>(p, n, warp - 10, smem, S);
+    } else if (warp == 9) {
+      copy_codes<D>(p, w, key0, n, smem, S, sm_sc);
     } else if (__all_sync(0xFFFFFFFFu, wait_bar(S, &S.q_full, 0, p))) {
       const auto qk = [&](int t, int s, int j) {  // row tile t, into S number s
         const uint32_t q = sbase + C::kQ + t * 128 * D * 2, k = sbase + C::kK + (j % C::kBufs) * C::kTile;
@@ -582,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
     }
     constexpr int kHalf = kBK / 2, kHB = kBlocks / 2;
     // scores to the exponents of their weights, -infinity where the row does not see the key
-    const auto mask = [&](float (&x)[kHalf], const float* sc, int key) {
+    const auto mask = [&](float (&x)[kHalf], const float (&kscale)[kHB], const float (&vexp)[kHB], int key) {
 #pragma unroll
       for (int c = 0; c < kHalf; ++c) {
-        const float y = fmaf(x[c], sc[c >> 4] * f, sc[kBlocks + (c >> 4)]);
+        const float y = fmaf(x[c], kscale[c >> 4] * f, vexp[c >> 4]);
         x[c] = key + c >= lo && key + c < hi ? y : kNegInf;
       }
     };
@@ -622,8 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         // Weights against the maximum so far.  None is negative, so that sums of 16 of at most kMost say that each fits
         // fp16: the maximum itself is looked for, and O and the sums rescaled, only where a sum does not.
         float (&x)[kHalf] = *reinterpret_cast<float(*)[kHalf]>(&r);
-        const float* const sc = &sm_sc[j & 3][0][h * kHB];  // scales of K; exponents and back factors of V behind them
-        if (masked) mask(x, sc, k0 + h * kHalf);
+        const float* const at = &sm_sc[j & 3][0][h * kHB];
+        const float4 g4 = *reinterpret_cast<const float4*>(at), e4 = *reinterpret_cast<const float4*>(at + kBlocks), b4 = *reinterpret_cast<const float4*>(at + 2 * kBlocks);
+        const float kscale[4] = {g4.x, g4.y, g4.z, g4.w}, vexp[4] = {e4.x, e4.y, e4.z, e4.w}, vback[4] = {b4.x, b4.y, b4.z, b4.w};
+        if (masked) mask(x, kscale, vexp, k0 + h * kHalf);
         bool sure = false;
         while (true) {
           const float z = m == kNegInf ? 0.0f : m;
@@ -632,16 +660,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
           if (!masked) {
 #pragma unroll
             for (int b = 0; b < kHB; ++b) {
-              const float all = weights(x + 16 * b, sc[b] * f, sc[kBlocks + b] - z, w2 + 8 * b);
+              const float all = weights(x + 16 * b, kscale[b] * f, vexp[b] - z, w2 + 8 * b);
               most = max_nan(most, all);
-              sum = fmaf(all, sc[2 * kBlocks + b], sum);
+              sum = fmaf(all, vback[b], sum);
             }
           } else {
 #pragma unroll
             for (int b = 0; b < kHB; ++b) {
               const float all = weights(x + 16 * b, 1.0f, -z, w2 + 8 * b);
               most = max_nan(most, all);
-              if (all != 0.0f) sum = fmaf(all, sc[2 * kBlocks + b], sum);  // a NaN scale that the row does not see counts for nothing
+              if (all != 0.0f) sum = fmaf(all, vback[b], sum);  // a NaN scale that the row does not see counts for nothing
             }
           }
           if (sure || !__any_sync(0xFFFFFFFFu, !(most <= kMost) || m == kNegInf)) {
@@ -656,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
             float y = fmaxf(x[16 * b], x[16 * b + 1]);
 #pragma unroll
             for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
-            top = fmaxf(top, masked ? y : fmaf(y, sc[b] * f, sc[kBlocks + b]));
+            top = fmaxf(top, masked ? y : fmaf(y, kscale[b] * f, vexp[b]));
           }
           const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
           m = next;
@@ -685,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_ready[s][h]);
       }
+      if (lane == 0) mbar_arrive(&S.sc_empty[j & 3]);
     }
     if (live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.o_done[t], 0, p))) {
       tc_fence_after();

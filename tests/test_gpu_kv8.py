@@ -226,6 +226,44 @@ def test_attention(dev, dim, heads, group, page, lens, counts, rotated):
     w4.w4a4_check()
 
 
+@pytest.mark.parametrize("dim,heads,group,page,lens,counts,window", [
+    (256, 2, 5, 32, [2500, 700, 130], [8, 8, 8], 0), (128, 2, 4, 64, [3000, 1], [100, 1], 0), (64, 1, 8, 16, [2100, 40, 900], [60, 30, 3], 0),
+    (128, 1, 17, 128, [5000], [1], 0), (64, 2, 3, 64, [1800], [700], 300), (256, 1, 20, 16, [1700, 1600], [1, 30], 0)])
+def test_attention_of_many_rows_over_many_keys(dev, dim, heads, group, page, lens, counts, window):
+    """More key tiles than any ring of the kernel holds, whole and in parts."""
+    rng = np.random.default_rng(dim + len(lens))
+    pages = sum((L + page - 1) // page for L in lens)
+    cache, codes, scales = make_cache(rng, dev, pages, heads, page, dim)
+    table, t = make_table(rng, dev, pages, lens, page)
+    q = rows(rng, sum(counts), heads * group, dim, torch.bfloat16, dev) * 0.3
+    cu = None if len(set(counts)) == 1 else ints(offsets(counts), dev)
+    for ws in (True, None):
+        got = w4.kv8_attention(q, cache, t, ints(lens, dev), cu=cu, window=window, dtype=torch.float32, ws=ws)
+        check_attention(got, q, codes, scales, table, lens, counts, window=window)
+        assert torch.equal(got, w4.kv8_attention(q, cache, t, ints(lens, dev), cu=cu, window=window, dtype=torch.float32, ws=ws))
+    w4.w4a4_check()
+
+
+def test_attention_gives_up_on_a_bounded_wait(dev):
+    """A loader held back longer than the waits' limit: the kernel returns by itself, the check says so, the next call is right."""
+    rng = np.random.default_rng(13)
+    for dim in (128, 256):
+        cache, codes, scales = make_cache(rng, dev, 8, 1, 64, dim)
+        table, t = make_table(rng, dev, 8, [400], 64)
+        q = rows(rng, 50, 2, dim, torch.bfloat16, dev)
+        w4.w4a4_debug_set_wait_limit(2_000_000, 20_000_000)
+        try:
+            w4.kv8_attention(q, cache, t, ints([400], dev))
+            with pytest.raises(w4.W4A4Error) as e:
+                w4.w4a4_check()
+            assert e.value.status_name == "W4A4_ERR_TIMEOUT"
+        finally:
+            w4.w4a4_debug_set_wait_limit()
+        got = w4.kv8_attention(q, cache, t, ints([400], dev))
+        w4.w4a4_check()
+        check_attention(got, q, codes, scales, table, [400], [50])
+
+
 def test_attention_types_strides_scale(dev):
     rng = np.random.default_rng(5)
     lens, counts, page, H, g, D = [90, 40], [30, 2], 32, 2, 3, 128
