@@ -208,12 +208,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* carry, int thr
   return total;
 }
 // By whole CTAs; prefix: shared, of batch entries, not used for up to 32 sequences: then each warp finds it by itself,
-// without a barrier.  False: nothing to do.
+// without a barrier.  join: of the join's CTAs, one a cut tile: its work is that of the tile's first part.  False:
+// nothing to do.
 // With fewer row tiles than SMs and a workspace, a sequence's tiles have their keys cut into parts, each of as
 // many key tiles at most as let all parts have an SM; two at least, since a part costs its q, its first copies
 // and its write of O.  Tiles in descending order: with a causal mask a sequence's later rows see more keys.
 template <int D>
-__device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int64_t* carry, int threads, int cta, Work& w) {
+__device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int64_t* carry, int threads, int cta, bool join, Work& w) {
   const int tid = threadIdx.x, lane = tid & 31;
   const bool small = p.s.batch <= 32;
   int64_t tiles = 0, keys = 0, total = 0, before = 0;
@@ -243,18 +244,24 @@ __device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int6
   // ceil(n / most) a tile, at most n / most + 1: keys / most + tiles parts
   int most = 0;
   if (p.parts && 2 * tiles <= p.sms) most = static_cast<int>(max(int64_t(2), (keys + p.sms - tiles - 1) / (p.sms - tiles)));
-  const auto ctas = [&](const Plan& o) { return most ? static_cast<int64_t>(o.tiles) * ((o.keys + most - 1) / most) : o.tiles; };
-  int at, b = 0, in;
+  if (join && !most) return false;
+  const auto parts_of = [&](const Plan& o) { return most ? (o.keys + most - 1) / most : 1; };
+  // The CTA's tile is `in` of sequence b, whose parts begin at slot `first` of all.  The join counts tiles, and the
+  // slots before them beside.
+  const auto count = [&](const Plan& o) { return static_cast<int64_t>(o.tiles) * (join ? 1 : parts_of(o)); };
+  int at, b = 0, in, first;
   if (small) {
-    int64_t sum = ctas(o);
+    const int64_t sum = count(o), slots = static_cast<int64_t>(o.tiles) * parts_of(o);
     before = sum;
+    int64_t slots_before = slots;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
-      if (lane >= d) before += x;
+      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, before, d), y = __shfl_up_sync(0xFFFFFFFFu, slots_before, d);
+      if (lane >= d) before += x, slots_before += y;
     }
     total = __shfl_sync(0xFFFFFFFFu, before, 31);
     before -= sum;
+    slots_before -= slots;
     if (cta >= total) return false;
     at = static_cast<int>(total) - 1 - cta;
     b = 31 - __clz(__ballot_sync(0xFFFFFFFFu, lane < p.s.batch && before <= at));
@@ -262,13 +269,22 @@ __device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int6
     w.q.n = __shfl_sync(0xFFFFFFFFu, seq.n, b);
     w.q.len = __shfl_sync(0xFFFFFFFFu, seq.len, b);
     in = at - static_cast<int>(__shfl_sync(0xFFFFFFFFu, before, b));
+    first = static_cast<int>(__shfl_sync(0xFFFFFFFFu, slots_before, b));
   } else {
+    int64_t slots = 0;
+    first = 0;
     for (int b0 = 0; b0 < p.s.batch; b0 += threads) {
       o = Plan{0, 0};
       if (b0 + tid < p.s.batch) o = plan_of<D>(p, kv_seq(p.s, b0 + tid, p.c.page, nullptr));
-      const int64_t sum = block_scan(ctas(o), carry, threads, before);
+      const int64_t sum = block_scan(count(o), carry, threads, before);
       if (b0 + tid < p.s.batch) prefix[b0 + tid] = static_cast<int>(total + before);
       total += sum;
+      if (join) {
+        int64_t mine;
+        const int64_t all = block_scan(static_cast<int64_t>(o.tiles) * parts_of(o), carry, threads, mine);
+        if (b0 + tid < p.s.batch) prefix[p.s.batch + b0 + tid] = static_cast<int>(slots + mine);
+        slots += all;
+      }
     }
     __syncthreads();
     if (cta >= total) return false;
@@ -280,12 +296,13 @@ __device__ __forceinline__ bool find_work(const PromptArgs& p, int* prefix, int6
     }
     w.q = kv_seq(p.s, b, p.c.page, nullptr);
     in = at - prefix[b];
+    first = join ? prefix[p.s.batch + b] : prefix[b];
   }
   w.b = b;
-  const int parts = most ? (plan_of<D>(p, w.q).keys + most - 1) / most : 1;
-  w.part = in % parts;
-  in /= parts;
-  w.slot0 = at - w.part;
+  const int parts = most ? parts_of(plan_of<D>(p, w.q)) : 1;
+  w.part = join ? 0 : in % parts;
+  if (!join) in /= parts;
+  w.slot0 = first + in * parts;
   w.head = in % p.c.heads;
   w.row0 = in / p.c.heads * Shape<D>::kRows;
   w.rows = min(Shape<D>::kRows, w.q.n * p.group - w.row0);
@@ -486,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   // takes it for the same in every lane (straight from the shuffles the loops cost 11% more).
   if (p.s.batch > 32 || warp == 0) {
     Work w;
-    const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), w);
+    const bool some = find_work<D>(p, reinterpret_cast<int*>(smem + C::kPrefix), sm_carry, kThreads, static_cast<int>(blockIdx.x), false, w);
     if (tid == 0) {
       if (!some) w.rows = 0;
       sm_work = w;
@@ -766,18 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The parts of cut tiles together, in the order of their keys.  grid (SMs, shares of a tile's rows): CTA (x, y)
-// takes share y of the tile whose first part CTA x of the attention was.
-constexpr int kJoinThreads = 256, kJoinShares = 8;
+// The parts of cut tiles together, in the order of their keys.  grid (cut tiles at most, shares of a tile's rows).
+constexpr int kJoinThreads = 256, kJoinShares = 16, kAtOnce = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
   using C = Shape<D>;
-  __shared__ int prefix[kKvMaxBatch];
+  __shared__ int prefix[2 * kKvMaxBatch];
   __shared__ int64_t carry[32];
   grid_dep_launch();
   grid_dep_wait();
   Work w;
-  if (!find_work<D>(p, prefix, carry, kJoinThreads, static_cast<int>(blockIdx.x), w) || w.part > 0 || w.parts == 1) return;
+  if (!find_work<D>(p, prefix, carry, kJoinThreads, static_cast<int>(blockIdx.x), true, w) || w.parts == 1) return;
   constexpr int kShare = C::kRows / kJoinShares;
   for (int ch = threadIdx.x; ch < kShare * D / 8; ch += kJoinThreads) {
     const int row = blockIdx.y * kShare + ch / (D / 8), cc = ch % (D / 8);
@@ -785,20 +801,40 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     float top = kNegInf, l = 0.0f, v[8] = {};
     const auto part = [&](int i) { return p.parts + static_cast<int64_t>(w.slot0 + i) * C::kPart; };
     const bool in = row < w.rows;
-    if (in) {
-      for (int i = 0; i < w.parts; ++i) top = fmaxf(top, part(i)[C::kRows * D + row]);
-#pragma unroll 4
-      for (int i = 0; i < w.parts; ++i) {
-        const float* const s = part(i);
-        const float m = s[C::kRows * D + row], x = s[C::kRows * (D + 1) + row];
-        const float4* const t = reinterpret_cast<const float4*>(s) + 2 * cc * C::kRows + row;
-        const float4 y = t[0], z = t[C::kRows];
-        const float f = m == kNegInf ? (x == x ? 0.0f : 1.0f) : ex2(m - top);
-        l += x * f;
-        v[0] += y.x * f; v[1] += y.y * f; v[2] += y.z * f; v[3] += y.w * f;
-        v[4] += z.x * f; v[5] += z.y * f; v[6] += z.z * f; v[7] += z.w * f;
+    if (in)  // eight parts' loads out together; what is summed so far moves to the new maximum
+      for (int i0 = 0; i0 < w.parts; i0 += kAtOnce) {
+        float m[kAtOnce], x[kAtOnce];
+        float4 y[kAtOnce], z[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          m[i] = kNegInf;
+          x[i] = 0.0f;
+          y[i] = z[i] = make_float4(0, 0, 0, 0);
+          if (i0 + i < w.parts) {
+            const float* const s = part(i0 + i);
+            const float4* const t = reinterpret_cast<const float4*>(s) + 2 * cc * C::kRows + row;
+            m[i] = __ldcg(s + C::kRows * D + row);
+            x[i] = __ldcg(s + C::kRows * (D + 1) + row);
+            y[i] = __ldcg(t);
+            z[i] = __ldcg(t + C::kRows);
+          }
+        }
+        float next = top;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) next = fmaxf(next, m[i]);
+        const float c = next == top ? 1.0f : ex2(top - next);
+        top = next;
+        l *= c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= c;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float f = m[i] == kNegInf ? (x[i] == x[i] ? 0.0f : 1.0f) : ex2(m[i] - top);
+          l += x[i] * f;
+          v[0] += y[i].x * f; v[1] += y[i].y * f; v[2] += y[i].z * f; v[3] += y[i].w * f;
+          v[4] += z[i].x * f; v[5] += z[i].y * f; v[6] += z[i].z * f; v[7] += z[i].w * f;
+        }
       }
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : v[i] / l;
     if (p.c.rotated) quad_rotate(v, threadIdx.x & 3);
@@ -827,7 +863,7 @@ cudaError_t launch(K kernel, dim3 grid, int threads, int smem, const PromptArgs&
 }
 
 template <int D>
-cudaError_t launch_prompt(const PromptArgs& p, int64_t most_tiles, cudaStream_t st) {
+cudaError_t launch_prompt(const PromptArgs& p, int64_t least_tiles, int64_t most_tiles, cudaStream_t st) {
   using C = Shape<D>;
   static bool configured[64] = {};
   int dev = 0;
@@ -841,8 +877,10 @@ cudaError_t launch_prompt(const PromptArgs& p, int64_t most_tiles, cudaStream_t 
   }
   const int64_t grid = most_tiles > p.sms ? most_tiles : p.sms;
   e = launch(kv8_prompt_kernel<D>, dim3(static_cast<unsigned>(p.parts ? grid : most_tiles)), kThreads, C::kSmem, p, st);
-  if (e != cudaSuccess || !p.parts) return e;
-  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(p.sms), kJoinShares), kJoinThreads, 0, p, st);
+  // tiles are cut while there are two SMs each
+  if (e != cudaSuccess || !p.parts || 2 * least_tiles > p.sms) return e;
+  const int64_t cut = most_tiles < p.sms / 2 ? most_tiles : p.sms / 2;
+  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(cut), kJoinShares), kJoinThreads, 0, p, st);
 }
 
 int64_t g_wait = kWaitCycles, g_delay = 0;
@@ -877,10 +915,13 @@ cudaError_t launch_kv8_prompt(const KvCache& c, const KvSeqs& s, const KvAttn& a
   const int64_t few = s.batch < s.tokens ? s.batch : s.tokens;
   const int64_t most = c.heads * (s.cu ? static_cast<int64_t>(s.tokens) * p.group / rows + few
                                        : s.batch * ((static_cast<int64_t>(s.each) * p.group + rows - 1) / rows));
+  // and at least, with all the rows that may be the other kernel's taken off
+  const int64_t mine = static_cast<int64_t>(s.tokens) * p.group - static_cast<int64_t>(least_rows - 1) * s.batch;
+  const int64_t least = s.cu ? c.heads * (mine > 0 ? (mine + rows - 1) / rows : 0) : most;
   switch (c.dim) {
-    case 64: return launch_prompt<64>(p, most, st);
-    case 128: return launch_prompt<128>(p, most, st);
-    default: return launch_prompt<256>(p, most, st);
+    case 64: return launch_prompt<64>(p, least, most, st);
+    case 128: return launch_prompt<128>(p, least, most, st);
+    default: return launch_prompt<256>(p, least, most, st);
   }
 }
 

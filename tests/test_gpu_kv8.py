@@ -244,6 +244,21 @@ def test_attention_of_many_rows_over_many_keys(dev, dim, heads, group, page, len
     w4.w4a4_check()
 
 
+def test_attention_of_many_sequences_of_many_rows(dev):
+    """More sequences than a warp's lanes: whole row tiles, and (with one head) tiles cut into parts."""
+    rng = np.random.default_rng(14)
+    for B, H, g, D, page in ((40, 1, 3, 128, 32), (45, 2, 2, 64, 16)):
+        lens = [int(x) for x in rng.integers(30, 900, B)]
+        counts = [int(x) for x in rng.integers(0, 30, B)]
+        pages = sum((L + page - 1) // page for L in lens)
+        cache, codes, scales = make_cache(rng, dev, pages, H, page, D)
+        table, t = make_table(rng, dev, pages, lens, page)
+        q = rows(rng, sum(counts), H * g, D, torch.bfloat16, dev)
+        got = w4.kv8_attention(q, cache, t, ints(lens, dev), cu=ints(offsets(counts), dev))
+        check_attention(got, q, codes, scales, table, lens, counts)
+    w4.w4a4_check()
+
+
 def test_attention_gives_up_on_a_bounded_wait(dev):
     """A loader held back longer than the waits' limit: the kernel returns by itself, the check says so, the next call is right."""
     rng = np.random.default_rng(13)
