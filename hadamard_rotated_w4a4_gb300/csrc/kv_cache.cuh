@@ -55,9 +55,13 @@ __device__ __forceinline__ int64_t kv_scale_at(const KvCache& c, int page, int h
 
 // 2^e of -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-// The scale that byte s stands for; NaN for 255.
+// The exponent that byte s stands for, as a float: NaN for 255; a byte that no append wrote (of a page of zeros, for
+// instance) counts as the nearest that one would.
+__device__ __forceinline__ float kv_exponent(int s) {
+  return s == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(min(max(s - 127, kKvLow), kKvHigh));
+}
 __device__ __forceinline__ float kv_scale(int s) {
-  return s == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(s) << 23);
+  return s == 255 ? __uint_as_float(0x7FC00000u) : pow2i(min(max(s - 127, kKvLow), kKvHigh));
 }
 
 }  // namespace w4a4

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 2) kv8_decode_kernel(const
         }
         const int sc = __shfl_sync(0xFFFFFFFFu, look_s, i & 31);
         if (lane == 0)  // a block without a page: codes of zero, whose weights are taken out below
-          sm_scale[warp][st] = make_float2(there ? kv_scale(sc & 255) : 0.0f, (sc >> 8) == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>((sc >> 8) - 127));
+          sm_scale[warp][st] = make_float2(there ? kv_scale(sc & 255) : 0.0f, kv_exponent(sc >> 8));
       }
       cp_commit();
     };

@@ -356,8 +356,8 @@ __device__ __forceinline__ void copy_codes(const PromptArgs& p, const Work& w, i
     if (lane < 8) {
       sc[j & 3][0][b] = byte < 0 ? 0.0f : f;
     } else if (lane < 16) {
-      sc[j & 3][1][b] = byte < 0 ? kNegInf : byte == 255 ? f : static_cast<float>(byte - 127);
-      sc[j & 3][2][b] = byte < 0 ? 0.0f : byte == 255 ? f : ex2(static_cast<float>(127 - byte));
+      sc[j & 3][1][b] = byte < 0 ? kNegInf : kv_exponent(byte);
+      sc[j & 3][2][b] = byte < 0 ? 0.0f : ex2(-kv_exponent(byte));
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.sc_full[j & 3]);

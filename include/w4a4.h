@@ -583,7 +583,8 @@ w4a4_status mxfp4_swiglu_quantize(const void* gate, const void* up, int dtype, i
  *   codes : device, [pages][heads][2][page][dim] int8: of each page and head its tokens'
  *           keys, then their values.
  *   scales: device, [pages][heads][2][page / 16]: 16 tokens share a scale per head, for K
- *           and for V, the power of two 2^(s - 127) of byte s, 87 <= s <= 167 (255 = NaN).
+ *           and for V, the power of two 2^(s - 127) of byte s, 87 <= s <= 167 (255 = NaN; another
+ *           byte, of a page that was only zeroed, counts as the nearest of these).
  *   page  : tokens of a page, 16, 32, 64 or 128.   dim: 64, 128 or 256.
  *   tag   : W4A4_TAG_KV8 | (W4A4_TAG_ROTATED if keys and values are rotated by H32 per 32
  *           elements, which spreads loud channels over the codes of their block).

@@ -1,5 +1,9 @@
 """The 8-bit paged keys and values on the GPU: appending against the oracle, bit for bit where no angle is involved,
 else within the fp32 error of the angles; reading back; attention against 64 bits (kv8_testutil)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -200,6 +204,8 @@ CASES = [
     (64, 2, 8, 32, [700, 90], [2, 2]), (256, 2, 5, 16, [260, 8], [3, 3]), (128, 2, 2, 64, [64, 63], [8, 8]),
     (128, 1, 7, 16, [100, 3, 50, 0, 31], [20, 1, 0, 0, 31]), (64, 3, 4, 64, [333], [200]), (256, 1, 2, 128, [300, 290], [100, 1]),
     (128, 2, 1, 32, [513], [513]), (64, 1, 24, 16, [77], [5]), (128, 1, 128, 16, [99, 40], [1, 3]),
+    # more new tokens than there are, and no tokens at all
+    (128, 2, 3, 16, [10, 50], [30, 50]), (64, 1, 2, 32, [0, 3], [40, 9]), (256, 1, 1, 16, [2, 0], [5, 5]),
 ]
 
 
@@ -311,6 +317,23 @@ def test_attention_of_wide_scales_and_loud_queries(dev):
         check_attention(got, q, codes, scales, table, lens, counts, scale=0.1 / size, rotated=False)
 
 
+def test_pages_that_were_only_zeroed_hold_zeros(dev):
+    """Blocks that no append wrote, in the middle of a sequence: keys and values of zero, in every kernel alike."""
+    D = 128
+    cache = w4.alloc_kv8(8, 1, D, 32, dev)
+    t = ints(range(8), dev)[None]
+    rng = np.random.default_rng(17)
+    x = rows(rng, 40, 2, D, torch.bfloat16, dev)
+    w4.kv8_append(cache, x[:, :1], x[:, 1:], t, ints([200], dev))
+    codes, scales = cache.codes.cpu().numpy(), cache.scales.cpu().numpy()
+    table = t.cpu().numpy()
+    k, v = w4.kv8_read(cache, t, ints([200], dev), 200)
+    assert (k[:144] == 0).all() and (v[:144] == 0).all() and torch.isfinite(k).all()
+    for n in (1, 30):
+        q = rows(rng, n, 2, D, torch.bfloat16, dev)
+        check_attention(w4.kv8_attention(q, cache, t, ints([200], dev), dtype=torch.float32), q, codes, scales, table, [200], [n])
+
+
 def test_attention_nan_reaches_who_sees_it(dev):
     """A NaN block in places that a row does not see does not touch it; one that it sees makes it NaN."""
     rng = np.random.default_rng(7)
@@ -387,6 +410,59 @@ def test_attention_on_another_stream(dev):
     side.synchronize()
     ref = np.stack([values(codes, scales, table[b], L)[:, -1] for b, L in enumerate(lens)], axis=1)
     assert np.array_equal(k.double().cpu().numpy(), ref[0]) and np.array_equal(v.double().cpu().numpy(), ref[1])
+
+
+def test_the_largest_batch_and_the_emptiest_table(dev):
+    rng = np.random.default_rng(15)
+    B, D, page = 2048, 64, 16
+    cache, codes, scales = make_cache(rng, dev, 32, 1, page, D)
+    lens = [int(x) for x in rng.integers(0, 64, B)]
+    table = rng.integers(0, 32, (B, 4)).astype(np.int32)
+    q = rows(rng, B, 3, D, torch.bfloat16, dev)
+    t = torch.from_numpy(table).to(dev)
+    check_attention(w4.kv8_attention(q, cache, t, ints(lens, dev)), q, codes, scales, table, lens, [1] * B)
+    many = rows(rng, 2 * B, 9, D, torch.bfloat16, dev)
+    check_attention(w4.kv8_attention(many, cache, t, ints(lens, dev)), many, codes, scales, table, lens, [2] * B)
+    none = torch.empty(2, 0, dtype=torch.int32, device=dev)
+    for n in (1, 30):
+        assert (w4.kv8_attention(q[:2 * n], cache, none, ints([0, 0], dev)) == 0).all()
+    w4.w4a4_check()
+
+
+def test_attention_with_a_scale_of_zero_averages(dev):
+    rng = np.random.default_rng(16)
+    cache, codes, scales = make_cache(rng, dev, 8, 1, 32, 128)
+    table, t = make_table(rng, dev, 8, [200], 32)
+    for n in (2, 60):
+        q = rows(rng, n, 4, 128, torch.bfloat16, dev)
+        got = w4.kv8_attention(q, cache, t, ints([200], dev), scale=0.0, dtype=torch.float32)
+        check_attention(got, q, codes, scales, table, [200], [n], scale=0.0)
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    code = """
+import sys; sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch, hadamard_rotated_w4a4_gb300 as w4
+cache = w4.alloc_kv8(8, 2, 128, 64)
+x = torch.randn(40, 8, 128, device='cuda').bfloat16()
+t, lens = torch.arange(4, device='cuda', dtype=torch.int32)[None], torch.tensor([200], device='cuda', dtype=torch.int32)
+f = w4.rope_freqs(128)
+out = torch.empty(40, 4, 128, device='cuda', dtype=torch.bfloat16)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q = torch.empty_like(out)
+    w4.kv8_append(cache, x[:, 4:6], x[:, 6:], t, lens, q=x[:, :4], q_out=q, freqs=f)
+    w4.kv8_attention(q, cache, t, lens, out=out)
+    one = w4.kv8_attention(q[:1], cache, t, lens)
+g.replay(); torch.cuda.synchronize()
+a = out.clone()
+w4.kv8_attention(q, cache, t, lens, out=out); torch.cuda.synchronize()
+assert torch.equal(a, out) and torch.isfinite(out).all() and torch.equal(one, w4.kv8_attention(q[:1], cache, t, lens))
+w4.w4a4_check()
+print('captured')
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_a_batch_of_many_lengths(dev):
