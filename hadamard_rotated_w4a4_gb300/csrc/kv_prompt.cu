@@ -408,34 +408,40 @@ __device__ __forceinline__ void convert(const PromptArgs& p, int n, int first, u
   }
 }
 
-// q to shared memory by warps 0-7: rotated as the keys are, scaled by a power of two per row, in the swizzle; four
+// q to shared memory by warps 0-7: rotated as the keys are, scaled by a power of two per row, in the swizzle; eight
 // pieces' loads go out together.  Rows past the last are zeros (a NaN there would have its warp look for maxima).
 template <int D>
 __device__ __forceinline__ void load_q(const PromptArgs& p, const Work& w, int qtiles, uint8_t* smem, float* row_factor) {
   using C = Shape<D>;
   const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
-  constexpr int kOnce = 4, kTogether = D < 256 ? 256 / D : 1;  // rows of a warp's pass
-  const int pieces = (w.rows + kTogether - 1) / kTogether * kTogether * (D / 8);
+  constexpr int kOnce = 8, kTogether = D < 256 ? 256 / D : 1;  // pieces a thread has out; rows of a warp's pass
+  constexpr int kStep = 256 / (D / 8);                         // rows of all threads' pass
+  const int rows = (w.rows + kTogether - 1) / kTogether * kTogether, cc = threadIdx.x % (D / 8), row0 = threadIdx.x / (D / 8);
   const auto place = [&](int row, int cc) {
     return reinterpret_cast<uint4*>(smem + C::kQ + (row >> 7) * 128 * D * 2 + (cc >> 3) * C::kPanel + (row & 127) * 128 + (((cc & 7) ^ (row & 7)) << 4));
   };
-  for (int ch = pieces + threadIdx.x; ch < qtiles * 128 * (D / 8); ch += 256) *place(ch / (D / 8), ch % (D / 8)) = make_uint4(0, 0, 0, 0);
-  for (int row = pieces / (D / 8) + threadIdx.x; row < qtiles * 128; row += 256) row_factor[row] = 0.0f;
-  for (int ch0 = threadIdx.x; ch0 < pieces; ch0 += 256 * kOnce) {
+  for (int ch = rows * (D / 8) + threadIdx.x; ch < qtiles * 128 * (D / 8); ch += 256) *place(ch / (D / 8), ch % (D / 8)) = make_uint4(0, 0, 0, 0);
+  for (int row = rows + threadIdx.x; row < qtiles * 128; row += 256) row_factor[row] = 0.0f;
+  // row row0 is head `h` of the group at token `t`; kStep rows on without another division
+  int t = (w.row0 + row0) / p.group, h = w.row0 + row0 - t * p.group;
+  const int dt = kStep / p.group, dh = kStep - dt * p.group;
+  for (int first = row0; first < rows; first += kStep * kOnce) {
     Chunk<float> raw[kOnce];
 #pragma unroll
     for (int i = 0; i < kOnce; ++i) {
-      const int ch = ch0 + 256 * i, row = ch / (D / 8), g = w.row0 + row;
-      if (row < w.rows) {
-        const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldq + (w.head * p.group + g % p.group) * p.a.ldqh + 8 * (ch % (D / 8));
+      if (first + kStep * i < w.rows) {
+        const int64_t at = static_cast<int64_t>(w.q.first + t) * p.a.ldq + (w.head * p.group + h) * p.a.ldqh + 8 * cc;
         if (p.a.q_bf16) reinterpret_cast<Chunk<__nv_bfloat16>&>(raw[i]).load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
         else raw[i].load(static_cast<const float*>(p.a.q) + at, false);
       }
+      t += dt;
+      h += dh;
+      if (h >= p.group) h -= p.group, ++t;
     }
 #pragma unroll
     for (int i = 0; i < kOnce; ++i) {
-      const int ch = ch0 + 256 * i, row = ch / (D / 8), cc = ch % (D / 8);
-      if (ch >= pieces) break;  // the same for a warp: its pieces fill whole rows
+      const int row = first + kStep * i;
+      if (row >= rows) break;  // the same for a warp: its pieces fill whole rows
       float v[8] = {};
       if (row < w.rows) {
         if (p.a.q_bf16) reinterpret_cast<const Chunk<__nv_bfloat16>&>(raw[i]).get(v);
@@ -669,8 +675,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
         const float4 g4 = *reinterpret_cast<const float4*>(at), e4 = *reinterpret_cast<const float4*>(at + kBlocks), b4 = *reinterpret_cast<const float4*>(at + 2 * kBlocks);
         const float kscale[4] = {g4.x, g4.y, g4.z, g4.w}, vexp[4] = {e4.x, e4.y, e4.z, e4.w}, vback[4] = {b4.x, b4.y, b4.z, b4.w};
         if (masked) mask(x, kscale, vexp, k0 + h * kHalf);
-        bool sure = false;
+        bool sure = j + h == 0;  // no reference yet
         while (true) {
+          if (sure) {
+            float top = kNegInf;
+#pragma unroll
+            for (int b = 0; b < kHB; ++b) {
+              float y = fmaxf(x[16 * b], x[16 * b + 1]);
+#pragma unroll
+              for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
+              top = fmaxf(top, masked ? y : fmaf(y, kscale[b] * f, vexp[b]));
+            }
+            const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
+            m = next;
+            l *= c;
+            if (j + h > 0) {
+              // O so far: the product before this one has to be done.  The product of the tile before that one is (this
+              // tile's S came behind it), so that a phase's parity tells which of the two is meant.
+              live = (j == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][1], (j - 1) & 1, p))) &&
+                     (h == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][0], j & 1, p)));
+              if (!live) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_at + d, o);
+                tmem_wait32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+                tmem_st32(o_at + d, o);
+              }
+            }
+          }
           const float z = m == kNegInf ? 0.0f : m;
           float sum = 0.0f, most = 0.0f;
           uint32_t w2[kHalf / 2];
@@ -695,34 +731,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
             break;
           }
           sure = true;
-          float top = kNegInf;
-#pragma unroll
-          for (int b = 0; b < kHB; ++b) {
-            float y = fmaxf(x[16 * b], x[16 * b + 1]);
-#pragma unroll
-            for (int c = 2; c < 16; c += 2) y = fmaxf(fmaxf(y, x[16 * b + c]), x[16 * b + c + 1]);
-            top = fmaxf(top, masked ? y : fmaf(y, kscale[b] * f, vexp[b]));
-          }
-          const float next = fmaxf(m, top - kShift), c = next == m ? 1.0f : ex2(m - next);
-          m = next;
-          l *= c;
-          if (j + h > 0) {
-            // O so far: the product before this one has to be done.  The product of the tile before that one is (this
-            // tile's S came behind it), so that a phase's parity tells which of the two is meant.
-            live = (j == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][1], (j - 1) & 1, p))) &&
-                   (h == 0 || __all_sync(0xFFFFFFFFu, wait_bar(S, &S.pv_done[t][0], j & 1, p)));
-            if (!live) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + d, o);
-              tmem_wait32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-              tmem_st32(o_at + d, o);
-            }
-          }
         }
         if (!live) break;
         tmem_st_wait();
@@ -737,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
       const int g = w.row0 + row;
       const int64_t at = static_cast<int64_t>(w.q.first + g / p.group) * p.a.ldo + (w.head * p.group + g % p.group) * p.a.ldoh;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint8_t* const stage = smem + C::kQ + (t * 4 + (warp & 3)) * 32 * D * 2;  // 4 KB at least
       float* const part = w.parts > 1 ? p.parts + static_cast<int64_t>(w.slot0 + w.part) * C::kPart : nullptr;
       if (part) {
         part[C::kRows * D + row] = m;
@@ -759,14 +768,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = l == 0.0f ? 0.0f : v[i] * inv;
         if (p.c.rotated) rotate32(v);
-        if (row < w.rows) {
+        // by way of shared memory, whose Q is done with: pieces of a row side by side
+        if (p.a.o_bf16) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const float (&y)[8] = *reinterpret_cast<const float(*)[8]>(v + i);
-            if (p.a.o_bf16) store8(static_cast<__nv_bfloat16*>(p.a.out) + at + d + i, y, false);
-            else store8(static_cast<float*>(p.a.out) + at + d + i, y, false);
+          for (int i = 0; i < 4; ++i) {
+            __nv_bfloat162 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+            memcpy(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), y, 16);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int from = 8 * i + (lane >> 2), cc = lane & 3;
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, at, from);
+            if (row - lane + from < w.rows)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + to + d + 8 * cc) =
+                  *reinterpret_cast<const uint4*>(stage + from * 64 + ((cc ^ ((from >> 1) & 3)) << 4));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int from = 4 * i + (lane >> 3), cc = lane & 7;
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, at, from);
+            if (row - lane + from < w.rows)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + to + d + 4 * cc) =
+                  *reinterpret_cast<const float4*>(stage + from * 128 + ((cc ^ (from & 7)) << 4));
           }
         }
+        __syncwarp();
       }
     }
   } else {
