@@ -578,29 +578,37 @@ cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t st) {
 
 }  // namespace
 
-// Few query rows (tokens x query heads per head of K and V), up to a tile of this kernel, are its work; more
-// go to the tensor cores.  A call with offsets may hold both kinds: each kernel takes its own.
 size_t kv8_attention_workspace_bytes(int dim) {
   const size_t mine = kWsCounters + static_cast<size_t>(2 * num_sms()) * 2 * kRows * (dim + 2) * sizeof(float);
   const size_t other = kv8_prompt_workspace_bytes(dim);
   return mine > other ? mine : other;
 }
 
+// Few query rows (tokens x query heads per head of K and V) are this kernel's work, more the other's (kv_prompt.cu).  Up
+// to 32, two tiles that read the keys twice: 24 rows over 4000 keys of 64 sequences, heads of 128, 111 us here and 149
+// there (of 64: 76 and 138); 64 rows 208 and 146.  Heads of 256 have 16 rows at most here (24 rows over 6000 keys of 8
+// sequences 71 and 56).  And all rows of a call whose tiles have few keys, by the tables' width, each as many as 512
+// keys for itself: 64 tokens of a prompt, 32 heads of 128 over 4: 7.3 and 14.7 us; 512 tokens 28 and 28.
+// A call with offsets may hold both kinds: each kernel takes its own.
 cudaError_t launch_kv8_attention(const KvCache& c, const KvSeqs& s, const KvAttn& a, void* ws, cudaStream_t st) {
   DecodeArgs p{};
   p.c = c;
   p.s = s;
   p.a = a;
   p.group = a.q_heads / c.heads;
-  p.most_rows = kRows;
+  const int64_t tiles = c.heads * (s.cu ? static_cast<int64_t>(s.tokens) * p.group / kRows + s.batch
+                                        : s.batch * ((static_cast<int64_t>(s.each) * p.group + kRows - 1) / kRows));
+  const bool small = c.dim <= 128 && tiles * (static_cast<int64_t>(s.width) * c.page + 512) <= (int64_t(1) << 18);
+  const int most = small ? 0x7FFFFFFF : c.dim <= 128 ? 2 * kRows : kRows;
+  p.most_rows = most;
   p.tickets = static_cast<uint32_t*>(ws);
   p.parts = ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounters) : nullptr;
   p.err = device_error_word();
-  const bool few = s.cu ? p.group <= kRows : static_cast<int64_t>(s.each) * p.group <= kRows;
-  const bool many = static_cast<int64_t>(s.cu ? s.tokens : s.each) * p.group > kRows;
+  const bool few = s.cu ? p.group <= most : static_cast<int64_t>(s.each) * p.group <= most;
+  const bool many = static_cast<int64_t>(s.cu ? s.tokens : s.each) * p.group > most;
   cudaError_t e = cudaSuccess;
   if (few) e = c.dim == 64 ? launch_decode<64>(p, st) : c.dim == 128 ? launch_decode<128>(p, st) : launch_decode<256>(p, st);
-  if (e == cudaSuccess && many) e = launch_kv8_prompt(c, s, a, kRows + 1, ws, st);
+  if (e == cudaSuccess && many) e = launch_kv8_prompt(c, s, a, most + 1, ws, st);
   return e;
 }
 

@@ -209,13 +209,16 @@ CASES = [
 ]
 
 
+WIDE = 1 << 19  # keys a table has places for: which kernel takes many rows of few keys goes by this
+
+
 @pytest.mark.parametrize("dim,heads,group,page,lens,counts", CASES)
-@pytest.mark.parametrize("rotated", [True, False])
-def test_attention(dev, dim, heads, group, page, lens, counts, rotated):
+@pytest.mark.parametrize("rotated,wide", [(True, False), (False, False), (True, True)])
+def test_attention(dev, dim, heads, group, page, lens, counts, rotated, wide):
     rng = np.random.default_rng(dim + sum(lens))
     pages = sum((L + page - 1) // page for L in lens) + 2
     cache, codes, scales = make_cache(rng, dev, pages, heads, page, dim, rotated)
-    table, t = make_table(rng, dev, pages, lens, page)
+    table, t = make_table(rng, dev, pages, lens, page, WIDE // page if wide else None)
     T, Hq = sum(counts), heads * group
     q = rows(rng, T, Hq, dim, torch.bfloat16, dev) * 0.2
     cu = None if len(set(counts)) == 1 else ints(offsets(counts), dev)
@@ -270,7 +273,7 @@ def test_attention_gives_up_on_a_bounded_wait(dev):
     rng = np.random.default_rng(13)
     for dim in (128, 256):
         cache, codes, scales = make_cache(rng, dev, 8, 1, 64, dim)
-        table, t = make_table(rng, dev, 8, [400], 64)
+        table, t = make_table(rng, dev, 8, [400], 64, WIDE // 64)
         q = rows(rng, 50, 2, dim, torch.bfloat16, dev)
         w4.w4a4_debug_set_wait_limit(2_000_000, 20_000_000)
         try:
@@ -289,16 +292,18 @@ def test_attention_types_strides_scale(dev):
     rng = np.random.default_rng(5)
     lens, counts, page, H, g, D = [90, 40], [30, 2], 32, 2, 3, 128
     cache, codes, scales = make_cache(rng, dev, 8, H, page, D)
-    table, t = make_table(rng, dev, 8, lens, page, 9)
-    x = rows(rng, 40, H * g + 2, D, torch.float32, dev) * 0.3
-    q = x[:, 1:1 + H * g]
-    out = torch.full((40, H * g + 2, D), 3.0, device=dev)
-    w4.kv8_attention(q, cache, t, ints(lens, dev), cu=ints([0, 30, 32], dev), scale=-0.05, out=out[:, 2:])
-    assert (out[:, :2] == 3).all() and (out[32:] == 3).all()
-    check_attention(out[:32, 2:], q[:32], codes, scales, table, lens, counts, scale=-0.05)
-    y = q.clone()  # in place
-    w4.kv8_attention(y, cache, t, ints(lens, dev), cu=ints([0, 30, 32], dev), scale=-0.05, out=y)
-    assert torch.equal(y[:32], out[:32, 2:]) and torch.equal(y[32:], q[32:])
+    for width in (9, WIDE // page):
+        table, t = make_table(rng, dev, 8, lens, page, width)
+        for o_type in (torch.float32, torch.bfloat16):
+            x = rows(rng, 40, H * g + 2, D, o_type, dev) * 0.3
+            q = x[:, 1:1 + H * g]
+            out = torch.full((40, H * g + 2, D), 3.0, device=dev, dtype=o_type)
+            w4.kv8_attention(q, cache, t, ints(lens, dev), cu=ints([0, 30, 32], dev), scale=-0.05, out=out[:, 2:])
+            assert (out[:, :2] == 3).all() and (out[32:] == 3).all()
+            check_attention(out[:32, 2:], q[:32], codes, scales, table, lens, counts, scale=-0.05)
+            y = q.clone()  # in place
+            w4.kv8_attention(y, cache, t, ints(lens, dev), cu=ints([0, 30, 32], dev), scale=-0.05, out=y)
+            assert torch.equal(y[:32], out[:32, 2:]) and torch.equal(y[32:], q[32:])
     assert w4.kv8_attention(q[:0], cache, t, ints(lens, dev), cu=ints([0, 0, 0], dev)).shape == (0, H * g, D)
 
 
@@ -321,7 +326,8 @@ def test_pages_that_were_only_zeroed_hold_zeros(dev):
     """Blocks that no append wrote, in the middle of a sequence: keys and values of zero, in every kernel alike."""
     D = 128
     cache = w4.alloc_kv8(8, 1, D, 32, dev)
-    t = ints(range(8), dev)[None]
+    t = torch.full((1, WIDE // 32), -1, dtype=torch.int32, device=dev)
+    t[0, :8] = ints(range(8), dev)
     rng = np.random.default_rng(17)
     x = rows(rng, 40, 2, D, torch.bfloat16, dev)
     w4.kv8_append(cache, x[:, :1], x[:, 1:], t, ints([200], dev))
@@ -329,16 +335,16 @@ def test_pages_that_were_only_zeroed_hold_zeros(dev):
     table = t.cpu().numpy()
     k, v = w4.kv8_read(cache, t, ints([200], dev), 200)
     assert (k[:144] == 0).all() and (v[:144] == 0).all() and torch.isfinite(k).all()
-    for n in (1, 30):
+    for n, width in ((1, 8), (30, 8), (30, WIDE // 32)):
         q = rows(rng, n, 2, D, torch.bfloat16, dev)
-        check_attention(w4.kv8_attention(q, cache, t, ints([200], dev), dtype=torch.float32), q, codes, scales, table, [200], [n])
+        check_attention(w4.kv8_attention(q, cache, t[:, :width], ints([200], dev), dtype=torch.float32), q, codes, scales, table, [200], [n])
 
 
 def test_attention_nan_reaches_who_sees_it(dev):
     """A NaN block in places that a row does not see does not touch it; one that it sees makes it NaN."""
     rng = np.random.default_rng(7)
     page, H, g, D, L, n = 16, 1, 2, 64, 100, 70
-    table, t = make_table(rng, dev, 8, [L], page)
+    table, t = make_table(rng, dev, 8, [L], page, WIDE // page)
     for kind in (0, 1):
         for n, window in ((70, 0), (70, 20), (4, 0), (4, 20)):
             cache, codes, scales = make_cache(rng, dev, 8, H, page, D)
@@ -432,8 +438,8 @@ def test_the_largest_batch_and_the_emptiest_table(dev):
 def test_attention_with_a_scale_of_zero_averages(dev):
     rng = np.random.default_rng(16)
     cache, codes, scales = make_cache(rng, dev, 8, 1, 32, 128)
-    table, t = make_table(rng, dev, 8, [200], 32)
-    for n in (2, 60):
+    for n, width in ((2, None), (60, None), (60, WIDE // 32)):
+        table, t = make_table(rng, dev, 8, [200], 32, width)
         q = rows(rng, n, 4, 128, torch.bfloat16, dev)
         got = w4.kv8_attention(q, cache, t, ints([200], dev), scale=0.0, dtype=torch.float32)
         check_attention(got, q, codes, scales, table, [200], [n], scale=0.0)
