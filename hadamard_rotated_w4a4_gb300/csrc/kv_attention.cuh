@@ -17,9 +17,10 @@
 
 namespace w4a4 {
 
-// Weights are 2^(t + Ev - m) with m kShift below a maximum that may lag the true one by
-// kLag: 2^(kShift + kLag) at most, well below fp16's 65504, and what lies 2^-28 below the
-// largest still has a bit in fp16's subnormals.
+// Weights are 2^(t + Ev - m) with m kShift below the maximum that was last looked for, which may
+// lag the true one: by kLag at most with few rows (2^(kShift + kLag), well below fp16's 65504), by
+// as much as the weights' sums allow with many.  What lies 2^-28 below the largest still has a bit
+// in fp16's subnormals.
 constexpr float kShift = 4.0f, kLag = 10.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 

@@ -16,6 +16,15 @@
 // and the next tile's S runs beside the softmax.
 //
 // The running maximum is looked for, and O rescaled, only where a weight might not fit fp16.
+//
+// Measured: 4096 tokens behind 12288, 40 heads of 128 over 8: 1266 us, 950 TFLOP/s (0.50 of a
+// bf16 product's burst).  A row tile's S and O products take 1900 cycles a key tile there, 1040 by
+// themselves: shared memory, which Q K^T alone reads at 128 bytes a cycle, is shared with the
+// conversion's writes; without those 1100 us, without the exponentials 1090.  Kept out: products of
+// 64 keys with two S a row tile (1399 us: Q read twice as often), two threads a row (1277), codes
+// by plain loads into registers (1484 at best).  8 drafted tokens of 8 sequences of up to 6000 keys,
+// heads of 256: 37 us; prompts of 7 sequences, heads of 64, window 500: 34 us; both are set-up,
+// one tile's chain and the join more than products.
 #include <cuda_bf16.h>
 
 #include "kv_attention.cuh"
@@ -85,8 +94,8 @@ struct Bars {
   volatile int abort;
 };
 
-// Bounded wait; on giving up, every other wait of the CTA gives up too.  The clock is read every 64 tries: sixteen
-// warps wait about half of the time, and what they do meanwhile takes issue slots from the others.
+// Bounded wait; on giving up, every other wait of the CTA gives up too.  The clock is read every 64 tries: the CTA's
+// sixteen warps wait about half of the time, and what they do meanwhile takes issue slots from the others.
 __device__ __forceinline__ bool wait_bar(Bars& S, uint64_t* b, uint32_t parity, const PromptArgs& p) {
   if (mbar_try(b, parity)) return true;
   const int64_t t0 = clock64();

@@ -157,7 +157,7 @@ size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 // Test hook, as grp_set_wait_limit, of the MXFP4 product's waits.
 void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
 
-// ---- the 8-bit paged key/value cache (kv_cache.cu, kv_attention.cu)
+// ---- the 8-bit paged key/value cache (kv_cache.cu, kv_decode.cu, kv_prompt.cu)
 struct KvCache {
   int8_t* codes;    // [pages][heads][2][page][dim]
   uint8_t* scales;  // [pages][heads][2][page / 16]

@@ -110,6 +110,26 @@ def test_positions(dev, dim, nf, interleaved, dtype):
     w4.w4a4_check()
 
 
+def test_positions_of_any_frequency(dev):
+    """Negative, zero and tiny ones, several turns a position, and NaN and infinities, which reach their pairs alone.  An
+    angle's own roundings, in 64 bits here and in 2^-64 turns there, are 2^-51 of it at most: 3e-10 at 1000 x 700."""
+    rng = np.random.default_rng(18)
+    D, L = 64, 1000
+    f = np.concatenate([[-1.0, 0.0, -0.0, 700.0, -700.0, 1e-9, -1e-300, 2 * np.pi, np.nan, np.inf, -np.inf, 3.0], rng.standard_normal(20)])
+    freqs = torch.from_numpy(f).to(dev)
+    x = rows(rng, L, 3, D, torch.float32, dev)
+    cache, t = w4.alloc_kv8(63, 1, D, 16, dev), ints(range(63), dev)[None]
+    q = w4.kv8_append(cache, x[:, 1:2], x[:, 2:], t, ints([L], dev), q=x[:, :1], q_out=torch.empty_like(x[:, :1]), freqs=freqs)
+    q, xs = q.double().cpu().numpy(), x.double().cpu().numpy()[:, :1]
+    bad = np.tile(~np.isfinite(f), 2)
+    assert np.isnan(q[..., bad]).all() and np.isfinite(q[..., ~bad]).all()
+    want = oracle.rope(xs, np.arange(L), np.where(np.isfinite(f), f, 0), False)
+    B = np.abs(xs).max(axis=-1, keepdims=True)
+    assert (np.abs(q - want) <= (14 * U + 1e-9) * B)[..., ~bad].all()
+    assert (cache.scales[:, 0, 0] == 255).all() and (cache.scales[:, 0, 1] != 255).all()
+    w4.w4a4_check()
+
+
 def test_append_strides_and_rows_behind(dev):
     """Views of one product's output, padded rows, and tokens past the last offset: nothing but the named rows is written."""
     rng = np.random.default_rng(1)
