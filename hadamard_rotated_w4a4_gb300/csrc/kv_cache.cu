@@ -15,7 +15,7 @@
 //
 // Bound: memory and the issue of instructions for long prompts, else latency.  8192 tokens of
 // 40 + 16 heads of 128 in bf16: 47.5 us, 5.3 TB/s of q, k, v and codes (first form 98 us; 55 with
-// angles reduced in fp64); 64 sequences' next token, 20 + 8 heads of 256 in fp32, 6.8 us; one token
+// angles reduced in fp64); 64 sequences' next token, 20 + 8 heads of 256 in fp32, 5.7 us; one token
 // 3.7 us.  Reading 8192
 // tokens back to bf16, from L2: 12.6 us.
 #include <cuda_bf16.h>
@@ -388,9 +388,10 @@ cudaError_t launch_kv8_append(const KvCache& c, const KvSeqs& s, const KvNew& a,
   const int64_t few = s.batch < s.tokens ? s.batch : s.tokens;
   const int64_t blocks = s.cu ? s.tokens / kKvTokens + 2 * few : static_cast<int64_t>(s.batch) * ((s.each + kKvTokens - 2) / kKvTokens + 1);
   const int64_t shares = (2 * c.heads + a.q_heads + kWarps - 1) / kWarps;
-  // heads over several CTAs while there are fewer than two CTAs an SM
-  int64_t y = (2 * static_cast<int64_t>(num_sms()) + blocks - 1) / blocks;
-  y = y < shares ? y : shares;
+  // heads over several CTAs, each with the angles for itself, up to about a CTA an SM (64 blocks of 28 heads in fp32:
+  // 64 CTAs 7.2 us, 128 5.7, 256 6.8; 513 blocks of 56 heads: 513 CTAs 47.5 us, 1026 49.5)
+  int64_t y = (num_sms() + blocks / 2) / blocks;
+  y = y < 1 ? 1 : y < shares ? y : shares;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y));
   int* err = device_error_word();
   switch (c.dim * 2 + a.x_bf16) {
