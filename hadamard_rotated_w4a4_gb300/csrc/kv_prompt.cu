@@ -23,7 +23,7 @@
 // conversion's writes; without those 1100 us, without the exponentials 1090.  Kept out: products of
 // 64 keys with two S a row tile (1399 us: Q read twice as often), two threads a row (1277), codes
 // by plain loads into registers (1484 at best).  8 drafted tokens of 8 sequences of up to 6000 keys,
-// heads of 256: 37 us; prompts of 7 sequences, heads of 64, window 500: 34 us; both are set-up,
+// heads of 256: 36 us; prompts of 7 sequences, heads of 64, window 500: 34 us; both are set-up,
 // one tile's chain and the join more than products.
 #include <cuda_bf16.h>
 
@@ -843,10 +843,17 @@ __global__ void __launch_bounds__(kJoinGroup* kJoinMost) kv8_join_kernel(const _
   __shared__ float sm_m[kJoinMost][32], sm_l[kJoinMost][32];
   grid_dep_launch();
   grid_dep_wait();
-  Work w;
+  __shared__ Work sm_work;
   const int tid = threadIdx.x, groups = blockDim.x / kJoinGroup, group = tid / kJoinGroup;
   const int row0 = blockIdx.y / (D / 32) * 32, chunk = blockIdx.y % (D / 32);
-  if (!find_work<D>(p, prefix, carry, blockDim.x, static_cast<int>(blockIdx.x), true, w) || w.parts == 1 || row0 >= w.rows) return;
+  if (p.s.batch > 32 || tid < 32) {  // of up to 32 sequences one warp finds the tile
+    Work found;
+    if (!find_work<D>(p, prefix, carry, blockDim.x, static_cast<int>(blockIdx.x), true, found)) found.rows = 0;
+    if (tid == 0) sm_work = found;
+  }
+  __syncthreads();
+  const Work w = sm_work;
+  if (row0 >= w.rows || w.parts == 1) return;
   const int in = tid & 31, row = row0 + in, quad = tid / 32 % 8;
   float top = kNegInf, l = 0.0f;
   float4 v = make_float4(0, 0, 0, 0);
@@ -942,7 +949,9 @@ cudaError_t launch_prompt(const PromptArgs& p, int64_t least_tiles, int64_t most
   if (e != cudaSuccess || !p.parts || 2 * least_tiles > p.sms || static_cast<int64_t>(p.s.width) * p.c.page <= 2 * kBK) return e;
   const int64_t cut = most_tiles < p.sms / 2 ? most_tiles : p.sms / 2, parts = p.sms / cut;
   const int groups = parts >= 4 * kAtOnce ? 4 : parts >= 2 * kAtOnce ? 2 : 1;  // about eight parts each
-  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(cut), C::kRows / 32 * (D / 32)), groups * kJoinGroup, 0, p, st);
+  const int64_t rows = (p.s.cu ? static_cast<int64_t>(p.s.tokens) : p.s.each) * p.group;  // of a sequence at most
+  const int64_t y = ((rows < C::kRows ? rows : C::kRows) + 31) / 32 * (D / 32);
+  return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(cut), static_cast<unsigned>(y)), groups * kJoinGroup, 0, p, st);
 }
 
 int64_t g_wait = kWaitCycles, g_delay = 0;
