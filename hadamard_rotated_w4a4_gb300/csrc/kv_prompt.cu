@@ -417,13 +417,14 @@ __device__ __forceinline__ void convert(const PromptArgs& p, int n, int first, u
   }
 }
 
-// q to shared memory by warps 0-7: rotated as the keys are, scaled by a power of two per row, in the swizzle; eight
-// pieces' loads go out together.  Rows past the last are zeros (a NaN there would have its warp look for maxima).
+// q to shared memory by warps 0-7: rotated as the keys are, scaled by a power of two per row, in the swizzle; four
+// pieces' loads are out at a time, in a loop of one piece (eight unrolled: 1 us more where a CTA has few key tiles).  Rows
+// past the last are zeros (a NaN there would have its warp look for maxima).
 template <int D>
 __device__ __forceinline__ void load_q(const PromptArgs& p, const Work& w, int qtiles, uint8_t* smem, float* row_factor) {
   using C = Shape<D>;
   const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;
-  constexpr int kOnce = 8, kTogether = D < 256 ? 256 / D : 1;  // pieces a thread has out; rows of a warp's pass
+  constexpr int kOnce = 4, kTogether = D < 256 ? 256 / D : 1;  // pieces a thread has out; rows of a warp's pass
   constexpr int kStep = 256 / (D / 8);                         // rows of all threads' pass
   const int rows = (w.rows + kTogether - 1) / kTogether * kTogether, cc = threadIdx.x % (D / 8), row0 = threadIdx.x / (D / 8);
   const auto place = [&](int row, int cc) {
@@ -434,37 +435,39 @@ __device__ __forceinline__ void load_q(const PromptArgs& p, const Work& w, int q
   // row row0 is head `h` of the group at token `t`; kStep rows on without another division
   int t = (w.row0 + row0) / p.group, h = w.row0 + row0 - t * p.group;
   const int dt = kStep / p.group, dh = kStep - dt * p.group;
-  for (int first = row0; first < rows; first += kStep * kOnce) {
-    Chunk<float> raw[kOnce];
+  Chunk<float> raw[kOnce];
+  int ahead = row0;  // the next row to ask for
+  const auto ask = [&](Chunk<float>& x) {
+    if (ahead < w.rows) {
+      const int64_t at = static_cast<int64_t>(w.q.first + t) * p.a.ldq + (w.head * p.group + h) * p.a.ldqh + 8 * cc;
+      if (p.a.q_bf16) reinterpret_cast<Chunk<__nv_bfloat16>&>(x).load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
+      else x.load(static_cast<const float*>(p.a.q) + at, false);
+    }
+    ahead += kStep;
+    t += dt;
+    h += dh;
+    if (h >= p.group) h -= p.group, ++t;
+  };
 #pragma unroll
-    for (int i = 0; i < kOnce; ++i) {
-      if (first + kStep * i < w.rows) {
-        const int64_t at = static_cast<int64_t>(w.q.first + t) * p.a.ldq + (w.head * p.group + h) * p.a.ldqh + 8 * cc;
-        if (p.a.q_bf16) reinterpret_cast<Chunk<__nv_bfloat16>&>(raw[i]).load(static_cast<const __nv_bfloat16*>(p.a.q) + at, false);
-        else raw[i].load(static_cast<const float*>(p.a.q) + at, false);
-      }
-      t += dt;
-      h += dh;
-      if (h >= p.group) h -= p.group, ++t;
+  for (int i = 0; i < kOnce; ++i) ask(raw[i]);
+#pragma unroll 1
+  for (int row = row0; row < rows; row += kStep) {  // the same trips for a warp: its pieces fill whole rows
+    float v[8] = {};
+    if (row < w.rows) {
+      if (p.a.q_bf16) reinterpret_cast<const Chunk<__nv_bfloat16>&>(raw[0]).get(v);
+      else raw[0].get(v);
     }
 #pragma unroll
-    for (int i = 0; i < kOnce; ++i) {
-      const int row = first + kStep * i;
-      if (row >= rows) break;  // the same for a warp: its pieces fill whole rows
-      float v[8] = {};
-      if (row < w.rows) {
-        if (p.a.q_bf16) reinterpret_cast<const Chunk<__nv_bfloat16>&>(raw[i]).get(v);
-        else raw[i].get(v);
-      }
-      if (p.c.rotated) quad_rotate(v, threadIdx.x & 3);
-      float amax = lane_amax(v);
+    for (int i = 0; i + 1 < kOnce; ++i) raw[i] = raw[i + 1];
+    ask(raw[kOnce - 1]);
+    if (p.c.rotated) quad_rotate(v, threadIdx.x & 3);
+    float amax = lane_amax(v);
 #pragma unroll
-      for (int d = 1; d < D / 8; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
-      const int e = row_exponent(amax);
-      const float f = sign * pow2i(-e);  // the scale's sign goes to q: the scores' factors are positive
-      *place(row, cc) = make_uint4(pack_half(v[0] * f, v[1] * f), pack_half(v[2] * f, v[3] * f), pack_half(v[4] * f, v[5] * f), pack_half(v[6] * f, v[7] * f));
-      if (cc == 0) row_factor[row] = fabsf(p.a.scale) * 1.4426950408889634f * pow2i(e);
-    }
+    for (int d = 1; d < D / 8; d <<= 1) amax = max3_abs(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d), 0.0f);
+    const int e = row_exponent(amax);
+    const float f = sign * pow2i(-e);  // the scale's sign goes to q: the scores' factors are positive
+    *place(row, cc) = make_uint4(pack_half(v[0] * f, v[1] * f), pack_half(v[2] * f, v[3] * f), pack_half(v[4] * f, v[5] * f), pack_half(v[6] * f, v[7] * f));
+    if (cc == 0) row_factor[row] = fabsf(p.a.scale) * 1.4426950408889634f * pow2i(e);
   }
 }
 
