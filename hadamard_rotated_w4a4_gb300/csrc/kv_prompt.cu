@@ -23,7 +23,7 @@
 // conversion's writes; without those 1100 us, without the exponentials 1090.  Kept out: products of
 // 64 keys with two S a row tile (1399 us: Q read twice as often), two threads a row (1277), codes
 // by plain loads into registers (1484 at best).  8 drafted tokens of 8 sequences of up to 6000 keys,
-// heads of 256: 36 us; prompts of 7 sequences, heads of 64, window 500: 34 us; both are set-up,
+// heads of 256: 36 us; prompts of 7 sequences, heads of 64, window 500: 33 us; both are set-up,
 // one tile's chain and the join more than products.
 #include <cuda_bf16.h>
 
