@@ -279,7 +279,7 @@ __device__ __forceinline__ float2 activate(float2 x) {
   if constexpr (ACT == kActRelu) {
     return make_float2(x.x <= 0.0f ? 0.0f : x.x, x.y <= 0.0f ? 0.0f : x.y);
   } else if constexpr (ACT == kActGelu) {
-    const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
+    const float2 a = make_float2(fminf(fabsf(x.x), 0x1p100f), fminf(fabsf(x.y), 0x1p100f));  // q is 0 there: inf stays inf
     const float2 d = __ffma2_rn(a, pair_of(0.3275911f * 0.70710678118654752f), pair_of(1.0f));
     const float2 t = make_float2(rcp(d.x), rcp(d.y));
     float2 q = __ffma2_rn(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));

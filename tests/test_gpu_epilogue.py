@@ -116,6 +116,22 @@ def test_epilogue_reads_what_the_call_before_wrote(dev):
         assert (y.double() - want).abs().max() <= 8 * U * want.abs().max()
 
 
+@pytest.mark.parametrize("M", [3, 300])
+def test_epilogue_of_infinities(dev, M):
+    """What a bias of infinity or NaN makes: its column alone, and there what the formula gives."""
+    w, a, gen = operands(5, M, 200, 96, dev)
+    bias = torch.zeros(200, device=dev)
+    bias[7], bias[8], bias[130] = float("inf"), float("nan"), -float("inf")
+    p = w4.mxfp4_gemm(w, a)
+    for act in (None, "relu", "silu", "gelu", "gelu_tanh"):
+        y = w4.mxfp4_gemm_epilogue(w, a, bias, act)
+        assert (y[:, 7] == float("inf")).all() and torch.isnan(y[:, 8]).all()
+        if act in (None, "relu"):
+            assert (y[:, 130] == (0.0 if act else -float("inf"))).all()
+        rest = bias == 0
+        check(y[:, rest], p[:, rest], None, act, None)
+
+
 def test_epilogue_refusals(dev):
     w, a, gen = operands(8, 4, 96, 64, dev)
     z = lambda *s, **k: torch.zeros(*s, device=dev, **k)  # noqa: E731
