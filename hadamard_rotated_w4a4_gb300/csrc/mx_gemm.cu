@@ -34,9 +34,9 @@
 // The epilogue, act(sum + bias) + residual, on the fp32 sums before their one rounding, as
 // instances of their own: the plain product's are as they were.  Bound: the residual's bytes and
 // the epilogue warps' instructions beside the next tile's MMAs.  Against the plain bf16 product
-// (us): M1024 N5120 K17408 34.0, bias 36.1, fp32 residual 43.9, SiLU 37.9, GELU 39.4; M4096 N17408
-// K5120 101, 102, 129 (285 MB more to read), 105, 107; M333 N4600 K1184 4.9, 5.7, 6.6, 6.4, 6.6;
-// M64 N5120 K5120 7.2, 7.9, 8.4, 7.7, 7.8.
+// (us): M1024 N5120 K17408 (fp32 out) 35.0, bias 35.3, fp32 residual 44.7, SiLU 36.4, GELU 37.5; M4096
+// N17408 K5120 102, 103, 124 (285 MB more to read), 104, 107; M333 N4600 K1184 5.0, 5.6, 6.4, 6.3, 6.5;
+// M64 N5120 K5120 6.7, 7.4, 7.8, 7.5, 7.8.
 #include <cuda_bf16.h>
 
 #include "tc_ptx.cuh"
@@ -307,32 +307,39 @@ __device__ __forceinline__ void activate_all(uint32_t (&r)[NC]) {
     r[i + 1] = __float_as_uint(y.y);
   }
 }
+// What a kernel's instance does with its sums: stores them; bias and activation alone; an fp32 or a bf16 residual as well.
+// (With both types in one instance M4096 N17408 K5120 took 129 us with fp32 and 142 with bf16, for 125 and 115.)  That
+// the residual is there is asked again in front of its loads: without the branch they were compiled among the sums'
+// arithmetic instead of together, 182 us.
+enum Epi : int { kPlain, kEpi, kEpiF32, kEpiBf16 };
 // Lines of the residual that this warp's epilogue will read, tokens m0 .. m0 + lim - 1 of weight rows n0 .. n0 + 31.
+template <int EPI>
 __device__ __forceinline__ void ask_residual(const MxEpilogue& e, int64_t n0, int64_t N, int64_t m0, int lim) {
-  if (!e.residual || n0 >= N) return;
+  if (EPI < kEpiF32 || !e.residual || n0 >= N) return;
   for (int i = threadIdx.x & 31; i < lim; i += 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(e.residual) + ((m0 + i) * e.ldr + n0) * (e.r_bf16 ? 2 : 4)));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(e.residual) + ((m0 + i) * e.ldr + n0) * (EPI == kEpiBf16 ? 2 : 4)));
 }
-// Residual of tokens m0 .. m0 + NC - 1 of weight row n; lanes and tokens past the last read the last.
-template <int NC>
-__device__ __forceinline__ void load_residual(float (&v)[NC], const MxEpilogue& e, int64_t n, int64_t N, int64_t m0, int lim) {
-  if (!e.residual || lim <= 0) return;
+// Residual of tokens m0 .. m0 + NC - 1 of weight row n, as it lies there: bf16 is widened where it is added, which waits
+// for it (here every load would be waited for by itself).  Lanes and tokens past the last read the last.
+template <int EPI, int NC>
+__device__ __forceinline__ void load_residual(uint32_t (&v)[NC], const MxEpilogue& e, int64_t n, int64_t N, int64_t m0, int lim) {
+  if (EPI < kEpiF32 || !e.residual || lim <= 0) return;
   const int64_t at = m0 * e.ldr + min(n, N - 1);
-  if (e.r_bf16) {
-    const __nv_bfloat16* const p = static_cast<const __nv_bfloat16*>(e.residual) + at;
+  if constexpr (EPI == kEpiBf16) {
+    const uint16_t* const p = static_cast<const uint16_t*>(e.residual) + at;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) v[i] = __bfloat162float(p[min(i, lim - 1) * e.ldr]);
+    for (int i = 0; i < NC; ++i) v[i] = p[min(i, lim - 1) * e.ldr];
   } else {
-    const float* const p = static_cast<const float*>(e.residual) + at;
+    const uint32_t* const p = static_cast<const uint32_t*>(e.residual) + at;
 #pragma unroll
     for (int i = 0; i < NC; ++i) v[i] = p[min(i, lim - 1) * e.ldr];
   }
 }
-template <int NC>
-__device__ __forceinline__ void add_residual(uint32_t (&r)[NC], const float (&v)[NC], const MxEpilogue& e) {
-  if (!e.residual) return;
+template <int EPI, int NC>
+__device__ __forceinline__ void add_residual(uint32_t (&r)[NC], const uint32_t (&v)[NC], const MxEpilogue& e) {
+  if (EPI < kEpiF32 || !e.residual) return;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + v[i]);
+  for (int i = 0; i < NC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(EPI == kEpiBf16 ? v[i] << 16 : v[i]));
 }
 template <int NC>
 __device__ __forceinline__ void bias_act(uint32_t (&r)[NC], const MxEpilogue& e, int64_t n, int64_t N) {
@@ -415,7 +422,7 @@ struct Small {
 constexpr int kSmallThreads = 192;  // 4 epilogue warps, a copy warp, an MMA warp
 
 // grid (S, weight tiles, token tiles), cluster (S, 1, 1).
-template <int NT, bool BF16, bool EPI>
+template <int NT, bool BF16, int EPI>
 __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                     const __grid_constant__ CUtensorMap amap,
                                                                     const __grid_constant__ CUtensorMap wsmap,
@@ -505,13 +512,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
   __syncwarp();
   if (EPI && warp < 4) {
     grid_dep_wait();  // the residual and the bias may be what the kernel in front of this one writes
-    ask_residual(p.ep, n0 + 32 * warp, p.N, m0, static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0)));
+    ask_residual<EPI>(p.ep, n0 + 32 * warp, p.N, m0, static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0)));
   }
   const int64_t n = n0 + 32 * (warp & 3) + lane;
   const int tok = static_cast<int>(min(static_cast<int64_t>(NT), p.M - m0));
   constexpr int NC = NT < 32 ? NT : 32;  // columns per pass
-  float res[NC];
-  if (EPI && warp < 4 && split == 1) load_residual(res, p.ep, n, p.N, m0, tok);
+  uint32_t res[NC];
+  if (EPI && warp < 4 && split == 1) load_residual<EPI>(res, p.ep, n, p.N, m0, tok);
   const bool whole = warp < 4 && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, 0, p) && !S.abort);
   tc_fence_after();
   const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -529,8 +536,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         for (int i = 0; i < NC; i += 16) tmem_wait(*reinterpret_cast<uint32_t(*)[16]>(r + i));
         if constexpr (EPI) {
           bias_act(r, p.ep, n, p.N);
-          add_residual(r, res, p.ep);
-          if (c + NC < NT) load_residual(res, p.ep, n, p.N, m0 + c + NC, tok - c - NC);
+          add_residual<EPI>(r, res, p.ep);
+          if (c + NC < NT) load_residual<EPI>(res, p.ep, n, p.N, m0 + c + NC, tok - c - NC);
         }
         store_cols<BF16>(r, y + c * p.ldy * kEsz, p.ldy, n, p.N, tok - c);
       }
@@ -572,10 +579,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) mx_small_kernel(const __grid
         uint32_t r[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
         const int64_t m = static_cast<int64_t>(rank) * share + i;
         if constexpr (EPI) {
-          float v4[4];
-          load_residual(v4, p.ep, n, p.N, m0 + m, static_cast<int>(tok - m));
+          uint32_t v4[4];
+          load_residual<EPI>(v4, p.ep, n, p.N, m0 + m, static_cast<int>(tok - m));
           bias_act(r, p.ep, n, p.N);
-          add_residual(r, v4, p.ep);
+          add_residual<EPI>(r, v4, p.ep);
         }
         store_cols<BF16>(r, y + m * p.ldy * kEsz, p.ldy, n, p.N, static_cast<int>(tok - m));
       }
@@ -645,7 +652,7 @@ struct Work {
 
 // Persistent.  CTA `rank` of the pair holds weight rows 128 rank .. of the tile, one
 // half of its tokens as its part of the N operand, and every token's scales.
-template <bool BF16, bool EPI>
+template <bool BF16, int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap asmap, const MxArgs p) {
@@ -752,7 +759,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     for (; more; more = work.next(p)) {
       if (EPI && work.s0 == 0) {
         const int64_t m0 = static_cast<int64_t>(tile_m(p, work.tile)) * kMaxTok + 128 * (warp >> 2);
-        ask_residual(p.ep, static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3), p.N, m0,
+        ask_residual<EPI>(p.ep, static_cast<int64_t>(tile_w(p, work.tile)) * 256 + rank * kTW + 32 * (warp & 3), p.N, m0,
                      static_cast<int>(min(static_cast<int64_t>(128), p.M - m0)));
       }
       live = live && __all_sync(0xFFFFFFFFu, wait_bar(S, &S.acc_full, seg & 1, p));
@@ -817,14 +824,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       uint8_t* const y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * (BF16 ? 2 : 4);
       if constexpr (EPI) {
         // 16 tokens at a time: beside the 128 accumulators no more fit the 168 registers that ten warps leave
-        float res[16];
-        load_residual(res, p.ep, n, p.N, m0, lim);
+        uint32_t res[16];
+        load_residual<EPI>(res, p.ep, n, p.N, m0, lim);
         bias_act(r, p.ep, n, p.N);
 #pragma unroll
         for (int c = 0; c < 128; c += 16) {
           uint32_t (&part)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + c);
-          add_residual(part, res, p.ep);
-          if (c < 112) load_residual(res, p.ep, n, p.N, m0 + c + 16, lim - c - 16);
+          add_residual<EPI>(part, res, p.ep);
+          if (c < 112) load_residual<EPI>(res, p.ep, n, p.N, m0 + c + 16, lim - c - 16);
           store_cols<BF16>(part, y + c * p.ldy * (BF16 ? 2 : 4), p.ldy, n, p.N, lim - c);
         }
       } else {
@@ -886,7 +893,7 @@ int small_split(int nt, int64_t tiles, int stages) {
   return best;
 }
 
-template <int NT, bool EPI>
+template <int NT, int EPI>
 cudaError_t launch_small(const CUtensorMap (&m)[4], const MxArgs& a, int y_bf16, cudaStream_t st) {
   using C = Small<NT>;
   static bool configured[2][64] = {};
@@ -953,7 +960,7 @@ void mx_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns) {
   g_delay = cycles(producer_delay_ns);
 }
 
-template <bool EPI>
+template <int EPI>
 static cudaError_t launch_mx(const CUtensorMap (&m)[4], const MxArgs& a, bool small, int pairs, int y_bf16, cudaStream_t stream) {
   if (!small) {
     static bool configured[2][64] = {};
@@ -1010,7 +1017,9 @@ cudaError_t launch_mx_gemm(const uint8_t* w_codes, const uint8_t* w_scales, int6
     e = encode_2d_map(&m[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, a_scales, kt, static_cast<uint64_t>((M + 127) / 128), kt * 4,
                       256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (e != cudaSuccess) return e;
-  return ep ? launch_mx<true>(m, a, small, q.pairs, y_bf16, stream) : launch_mx<false>(m, a, small, q.pairs, y_bf16, stream);
+  if (!ep) return launch_mx<kPlain>(m, a, small, q.pairs, y_bf16, stream);
+  if (!ep->residual) return launch_mx<kEpi>(m, a, small, q.pairs, y_bf16, stream);
+  return ep->r_bf16 ? launch_mx<kEpiBf16>(m, a, small, q.pairs, y_bf16, stream) : launch_mx<kEpiF32>(m, a, small, q.pairs, y_bf16, stream);
 }
 
 }  // namespace w4a4
