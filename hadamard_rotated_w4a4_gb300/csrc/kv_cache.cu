@@ -114,16 +114,17 @@ __device__ __forceinline__ void rope(float (&v)[2][8], const float* cs, const fl
       v[0][i] = a * c[i] - b * s[i];
       v[1][i] = b * c[i] + a * s[i];
     }
-  } else if (pairs == kNeighbours) {  // angles past nf are zero
+  } else if (pairs == kNeighbours) {  // what lies past the pairs as it is: an infinity times a sine of zero would be a NaN
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 c4 = *reinterpret_cast<const float4*>(cs + 4 * (k + h * kPerRow)), s4 = *reinterpret_cast<const float4*>(sn + 4 * (k + h * kPerRow));
       const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+      const int here = nf - 4 * (k + h * kPerRow);  // pairs of the chunk
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = v[h][2 * i], b = v[h][2 * i + 1];
-        v[h][2 * i] = a * c[i] - b * s[i];
-        v[h][2 * i + 1] = b * c[i] + a * s[i];
+        const float x = a * c[i] - b * s[i], y = b * c[i] + a * s[i];
+        if (i < here) v[h][2 * i] = x, v[h][2 * i + 1] = y;
       }
     }
   } else {  // nf a multiple of 8: eight pairs between two chunks, of whichever lanes
@@ -179,9 +180,9 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvCache c, c
   const Pairs pairs = a.nf == 0 ? kNoPairs : a.interleaved ? kNeighbours : 2 * a.nf == D ? kHalves : kApart;
   if (pairs != kNoPairs) {
     // angle j of every row by the same threads, so that its share of a turn is taken once
-    for (int j = threadIdx.x % (D / 2); j < (pairs == kNeighbours ? D / 2 : a.nf); j += D / 2) {
+    for (int j = threadIdx.x % (D / 2); j < a.nf; j += D / 2) {
       // a position's share of a turn in units of 2^-64, so that a position times it is exact but for whole turns
-      const double turns = j < a.nf ? a.freqs[j] * 0.15915494309189533577 : 0.0;  // 1 / (2 pi)
+      const double turns = a.freqs[j] * 0.15915494309189533577;  // 1 / (2 pi)
       const uint64_t share = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
       const float bad = static_cast<float>(turns - turns);  // 0, or NaN
       for (int r = lo + threadIdx.x / (D / 2); r < hi; r += kThreads / (D / 2)) {
