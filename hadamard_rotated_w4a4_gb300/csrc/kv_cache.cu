@@ -32,8 +32,10 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Blocks of 16 tokens that the last n of len tokens touch, and the first of them.
-__device__ __forceinline__ int touched(const Seq& q, int& first) {
+// Blocks of 16 tokens that the last n of len tokens touch, and the first of them.  More new tokens than there are: the
+// first of them have no place.
+__device__ __forceinline__ int touched(const Seq& q, int& first, int* err) {
+  if (q.n > q.len) kv_flag(err);
   const int start = max(q.len - q.n, 0);
   first = start / kKvTokens;
   return q.n == 0 || q.len == 0 ? 0 : (q.len + kKvTokens - 1) / kKvTokens - first;
@@ -53,7 +55,7 @@ __device__ __forceinline__ Found find_block(const KvSeqs& s, int page, int x, in
     if (b >= s.batch) return f;
     f.q = kv_seq(s, b, page, err);
     int first;
-    const int n = touched(f.q, first);
+    const int n = touched(f.q, first, err);
     if (x % most < n) f.b = b, f.block = first + x % most;
     return f;
   }
@@ -62,7 +64,7 @@ __device__ __forceinline__ Found find_block(const KvSeqs& s, int page, int x, in
     Seq q{};
     int first = 0;
     if (b < s.batch) q = kv_seq(s, b, page, err);
-    const int n = b < s.batch ? touched(q, first) : 0;
+    const int n = b < s.batch ? touched(q, first, err) : 0;
     int at = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -164,8 +166,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const KvCache c, c
     if (lane == 0) {
       at[0] = f.b;
       if (f.b >= 0) {
-        const int p0 = f.block * kKvTokens, start = f.q.len - f.q.n;  // start < 0: its first tokens have no place
-        if (start < 0) kv_flag(err);
+        const int p0 = f.block * kKvTokens, start = f.q.len - f.q.n;  // start < 0: its first tokens are skipped
         at[1] = max(max(start, 0) - p0, 0);             // the block's new rows: first, end
         at[2] = min(f.q.len - p0, kKvTokens);
         at[3] = p0;

@@ -610,10 +610,12 @@ typedef struct {
  *          (0 <= cu[0], never falling, cu[batch] <= tokens; what lies outside is left as it
  *          was); NULL: tokens / batch each.
  * These are read on the device, so that a captured call follows them.  A table entry
- * outside 0 .. pages - 1 counts as a page without tokens (append skips its tokens, read gives
+ * outside 0 .. pages - 1 counts as a page without tokens (append skips their k and v, read gives
  * zeros, attention does not see them); a length past the table is cut, offsets are clamped;
- * so are tokens before a sequence's start (cu longer than lens) skipped.  Each of these sets
- * the flag that w4a4_check reports as W4A4_ERR_DEVICE_FLAG.
+ * so are tokens before a sequence's start (more new tokens than lens) skipped: append leaves
+ * their rows of q_out as they were, read gives zeros.  Each of these sets the flag that
+ * w4a4_check reports as W4A4_ERR_DEVICE_FLAG.  But not in kv8_attention, where a query before
+ * its sequence's start is one that sees no key.
  */
 typedef struct {
   const int32_t* table;

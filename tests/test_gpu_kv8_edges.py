@@ -1,9 +1,10 @@
-"""Appending at the edges: elements that the positions leave alone."""
+"""Appending at the edges: elements that the positions leave alone, tokens before a sequence's start."""
+import numpy as np
 import pytest
 import torch
 
 import hadamard_rotated_w4a4_gb300 as w4
-from kv8_testutil import ints
+from kv8_testutil import ints, make_cache, make_table
 from w4a4_testutil import device
 
 pytestmark = pytest.mark.gpu
@@ -12,6 +13,12 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module")
 def dev():
     return device()
+
+
+def flagged():
+    with pytest.raises(w4.W4A4Error) as e:
+        w4.w4a4_check()
+    return e.value.status_name
 
 
 @pytest.mark.parametrize("dim,nf,interleaved", [(64, 5, True), (64, 8, False), (128, 1, True), (128, 30, True), (256, 127, True), (256, 120, False)])
@@ -42,4 +49,34 @@ def test_elements_past_the_pairs_pass_as_they_are(dev, dim, nf, interleaved, dty
     mine = q.clone()  # in place
     call(mine, None)
     assert torch.equal(mine.isnan(), got.isnan()) and torch.equal(mine.nan_to_num(nan=5), got.nan_to_num(nan=5))
+    w4.w4a4_check()
+
+
+@pytest.mark.parametrize("lens,counts", [([0], [8]), ([5], [8]), ([0, 30], [4, 4]), ([30, 0], [4, 4]), ([0] * 40 + [30], [0] * 39 + [1, 4]),
+                                         ([30] + [0] * 40, [4] + [1] + [0] * 39)])
+def test_tokens_before_a_sequences_start_are_reported(dev, lens, counts):
+    """... also where there is not one token of the sequence; the other sequences' tokens are written."""
+    rng = np.random.default_rng(4)
+    page, D, T = 16, 64, sum(counts)
+    cache, codes, scales = make_cache(rng, dev, 8, 1, page, D)
+    table, t = make_table(rng, dev, 8, lens, page)
+    x = torch.randn(T, 3, D, device=dev)
+    q_out = torch.full((T, 1, D), 7.0, device=dev)
+    for cu in ([0, *np.cumsum(counts)], None):
+        if cu is None and len(set(counts)) > 1:
+            continue
+        w4.w4a4_check()
+        w4.kv8_append(cache, x[:, 1:2], x[:, 2:], t, ints(lens, dev), cu=None if cu is None else ints(cu, dev), q=x[:, :1], q_out=q_out)
+        assert flagged() == "W4A4_ERR_DEVICE_FLAG"
+        w4.w4a4_check()
+        at = 0
+        for L, n in zip(lens, counts):
+            skip = max(n - L, 0)
+            assert (q_out[at:at + skip] == 7).all() and torch.equal(q_out[at + skip:at + n], x[at + skip:at + n, :1])
+            at += n
+    # as many new tokens as there are: nothing to report
+    n = min(16, max(lens))
+    if n:
+        b = lens.index(max(lens))
+        w4.kv8_append(cache, x[:1, 1:2].expand(n, 1, D).contiguous(), x[:1, 2:].expand(n, 1, D).contiguous(), t[b:b + 1], ints([n], dev))
     w4.w4a4_check()
