@@ -645,7 +645,8 @@ def w4a4_gemm_id_static(experts: Q4_0Weights, E: int, a: Act4, ids: torch.Tensor
 
 def w4a4_check(stream=None) -> None:
     """Synchronise and raise W4A4Error: W4A4_ERR_TIMEOUT if a GEMM or attention kernel gave up on a bounded wait, else
-    W4A4_ERR_DEVICE_FLAG if a kv8 call met a page, length or offset out of range.
+    W4A4_ERR_DEVICE_FLAG if a kv8 call met a page, length or offset out of range.  What it raises is cleared: behind a
+    timeout the next check tells of such a call.
 
     A kernel that gave up may leave stream-K arrival tickets standing in its
     workspace, and a later call on that workspace would then finish its cut

@@ -1357,8 +1357,8 @@ cudaError_t read_and_clear_device_error(int* value) {
   if (e != cudaSuccess) return e;
   *value = v;
   if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_w4a4_device_error, &zero, sizeof(int));
+    const int left = (v & ~kErrPage) != 0 ? v & kErrPage : 0;  // a wait that gave up is reported first
+    e = cudaMemcpyToSymbol(g_w4a4_device_error, &left, sizeof(int));
   }
   return e;
 }

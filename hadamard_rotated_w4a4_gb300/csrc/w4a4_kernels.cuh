@@ -104,7 +104,7 @@ cudaError_t launch_gemm_grp_routed(const uint8_t* w_codes, const uint16_t* w_sca
 // Test hook: the bound of the super-tile GEMM's pipeline waits (0 = the default
 // second) and a delay before its producer's first copy.
 void grp_set_wait_limit(uint64_t wait_ns, uint64_t producer_delay_ns);
-// Reads the GEMM kernels' device error word (bounded waits that gave up) and clears it.
+// Reads the kernels' device error word and clears it, but for kErrPage beside a bounded wait that gave up.
 cudaError_t read_and_clear_device_error(int* value);
 // Device address of the error word the GEMM and activation kernels set when a
 // bounded wait gives up (nullptr on failure).

@@ -699,8 +699,9 @@ size_t kv8_attention_workspace_bytes(int dim);
  * since the last check gave up on one of its bounded internal waits (a pipeline
  * that stopped making progress for a second).  Such a kernel stops early, so
  * its output is incomplete: W4A4_ERR_TIMEOUT.  Without one, W4A4_ERR_DEVICE_FLAG if a kv8
- * call met a page, length or offset outside its range.  Clears both conditions.  Returns
- * W4A4_ERR_CUDA for an error already pending on the stream.
+ * call met a page, length or offset outside its range.  Clears the condition that it reports:
+ * behind a timeout the next check tells of such a call.  Returns W4A4_ERR_CUDA for an error
+ * already pending on the stream.
  *
  * The library caches, per device, the addresses of its device-side state (this
  * error word, the static routing scratch of w4a4_gemm_id_static) and each

@@ -1,4 +1,5 @@
-"""Appending at the edges: elements that the positions leave alone, tokens before a sequence's start."""
+"""Appending at the edges: elements that the positions leave alone, tokens before a sequence's start, and what
+w4a4_check says of several faults at once."""
 import numpy as np
 import pytest
 import torch
@@ -79,4 +80,22 @@ def test_tokens_before_a_sequences_start_are_reported(dev, lens, counts):
     if n:
         b = lens.index(max(lens))
         w4.kv8_append(cache, x[:1, 1:2].expand(n, 1, D).contiguous(), x[:1, 2:].expand(n, 1, D).contiguous(), t[b:b + 1], ints([n], dev))
+    w4.w4a4_check()
+
+
+def test_a_fault_is_reported_behind_a_wait_that_gave_up(dev):
+    rng = np.random.default_rng(5)
+    cache, codes, scales = make_cache(rng, dev, 8, 1, 64, 128)
+    wide = torch.full((1, (1 << 19) // 64), -1, dtype=torch.int32, device=dev)
+    wide[0, :7] = ints(range(7), dev)
+    q = torch.randn(50, 2, 128, device=dev).to(torch.bfloat16)
+    w4.w4a4_debug_set_wait_limit(2_000_000, 20_000_000)
+    try:
+        w4.kv8_attention(q, cache, wide, ints([400], dev))
+        torch.cuda.synchronize()
+    finally:
+        w4.w4a4_debug_set_wait_limit()
+    w4.kv8_read(cache, wide, ints([500], dev), 100)  # its last page is not one
+    assert flagged() == "W4A4_ERR_TIMEOUT"
+    assert flagged() == "W4A4_ERR_DEVICE_FLAG"
     w4.w4a4_check()
