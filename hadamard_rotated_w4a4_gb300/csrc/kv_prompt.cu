@@ -828,24 +828,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const __grid_co
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The parts of cut tiles together, in a fixed order.  grid (cut tiles at most, pieces of 32 rows x 32 elements of a tile,
-// or fewer that take several): a thread takes four elements of a row, a warp 32 rows side by side as the parts hold them,
-// and the warps of a group every groups-th part; the groups meet in shared memory, where a row's 32 elements meet for H32.
-// (One group, its warps over rows 8 KB apart: 24 parts 20 us, 76 parts 49.)
+// The parts of cut tiles together, in a fixed order.  grid (cut tiles at most, 32 rows x 32 elements of a tile): a
+// thread takes four elements of a row, a warp 32 rows side by side as the parts hold them, and the warps of a group
+// every groups-th part; the groups meet in shared memory, where a row's 32 elements meet for H32.  (One group, its
+// warps over rows 8 KB apart: 24 parts 20 us, 76 parts 49.)
 constexpr int kJoinGroup = 256, kJoinMost = 4, kAtOnce = 8;
 // What sums of weights 2^(. - m), l of them together, count for against `top`: nothing without a key seen, unless NaN.
 __device__ __forceinline__ float join_factor(float m, float l, float top) {
   return m == kNegInf ? (l == l ? 0.0f : 1.0f) : ex2(m - top);
 }
-struct JoinShared {
-  float v[kJoinMost][32][36];
-  float m[kJoinMost][32], l[kJoinMost][32];
-};
-// 32 rows from row0 on, 32 elements from 32 * chunk on, of a cut tile, by the CTA.
 template <int D>
-__device__ __forceinline__ void join_piece(const PromptArgs& p, const Work& w, int row0, int chunk, JoinShared& sm) {
+__global__ void __launch_bounds__(kJoinGroup* kJoinMost) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
   using C = Shape<D>;
+  __shared__ int prefix[2 * kKvMaxBatch];
+  __shared__ int64_t carry[32];
+  __shared__ __align__(16) float sm_v[kJoinMost][32][36];
+  __shared__ float sm_m[kJoinMost][32], sm_l[kJoinMost][32];
+  grid_dep_launch();
+  grid_dep_wait();
+  __shared__ Work sm_work;
   const int tid = threadIdx.x, groups = blockDim.x / kJoinGroup, group = tid / kJoinGroup;
+  const int row0 = blockIdx.y / (D / 32) * 32, chunk = blockIdx.y % (D / 32);
+  if (p.s.batch > 32 || tid < 32) {  // of up to 32 sequences one warp finds the tile
+    Work found;
+    if (!find_work<D>(p, prefix, carry, blockDim.x, static_cast<int>(blockIdx.x), true, found)) found.rows = 0;
+    if (tid == 0) sm_work = found;
+  }
+  __syncthreads();
+  const Work w = sm_work;
+  if (row0 >= w.rows || w.parts == 1) return;
   const int in = tid & 31, row = row0 + in, quad = tid / 32 % 8;
   float top = kNegInf, l = 0.0f;
   float4 v = make_float4(0, 0, 0, 0);
@@ -879,21 +890,21 @@ __device__ __forceinline__ void join_piece(const PromptArgs& p, const Work& w, i
       v.x += y[i].x * f; v.y += y[i].y * f; v.z += y[i].z * f; v.w += y[i].w * f;
     }
   }
-  *reinterpret_cast<float4*>(&sm.v[group][in][4 * quad]) = v;
+  *reinterpret_cast<float4*>(&sm_v[group][in][4 * quad]) = v;
   if (quad == 0) {
-    sm.m[group][in] = top;
-    sm.l[group][in] = l;
+    sm_m[group][in] = top;
+    sm_l[group][in] = l;
   }
   __syncthreads();
   if (tid < 128) {
     const int r = tid >> 2, e = 8 * (tid & 3);
     float m = kNegInf, sum = 0.0f, o[8] = {};
-    for (int g = 0; g < groups; ++g) m = fmaxf(m, sm.m[g][r]);
+    for (int g = 0; g < groups; ++g) m = fmaxf(m, sm_m[g][r]);
     for (int g = 0; g < groups; ++g) {
-      const float f = join_factor(sm.m[g][r], sm.l[g][r], m);
-      sum += sm.l[g][r] * f;
+      const float f = join_factor(sm_m[g][r], sm_l[g][r], m);
+      sum += sm_l[g][r] * f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += sm.v[g][r][e + i] * f;
+      for (int i = 0; i < 8; ++i) o[i] += sm_v[g][r][e + i] * f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] / sum;
@@ -905,27 +916,6 @@ __device__ __forceinline__ void join_piece(const PromptArgs& p, const Work& w, i
       else store8(static_cast<float*>(p.a.out) + at, o, false);
     }
   }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kJoinGroup* kJoinMost) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
-  __shared__ int prefix[2 * kKvMaxBatch];
-  __shared__ int64_t carry[32];
-  __shared__ __align__(16) JoinShared sm;
-  grid_dep_launch();
-  grid_dep_wait();
-  __shared__ Work sm_work;
-  const int tid = threadIdx.x;
-  if (p.s.batch > 32 || tid < 32) {  // of up to 32 sequences one warp finds the tile
-    Work found;
-    if (!find_work<D>(p, prefix, carry, blockDim.x, static_cast<int>(blockIdx.x), true, found)) found.rows = 0;
-    if (tid == 0) sm_work = found;
-  }
-  __syncthreads();
-  const Work w = sm_work;
-  if (w.rows == 0 || w.parts == 1) return;
-  for (int y = blockIdx.y; y < (w.rows + 31) / 32 * (D / 32); y += gridDim.y, __syncthreads())
-    join_piece<D>(p, w, y / (D / 32) * 32, y % (D / 32), sm);
 }
 
 template <typename K>
@@ -943,12 +933,12 @@ cudaError_t launch(K kernel, dim3 grid, int threads, int smem, const PromptArgs&
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Row tiles: most_tiles at most; all_tiles at least if every token belongs to a sequence.  Offsets are only seen on the
-// device, and may name a few rows of a large buffer: so with them the join follows whatever the buffer's size, and the
-// kernel has the parts to cut into only where it follows.  Where all_tiles are too many to be cut it most often finds
-// nothing, with four CTAs an SM at most.  4096 tokens of 8 sequences of 4000 keys, 40 heads of 128 over 8: 382 us, 379
-// without the join, 385 with a CTA a piece; a buffer of 512 rows with 100 behind 15900: 66 us, 58 with a CTA a piece, 269
-// uncut.
+// Row tiles: most_tiles at most; all_tiles at least if every token belongs to a sequence, which only the device knows: a
+// buffer's offsets may name a few of its rows.  Whether tiles may be cut is decided here alone, by the call's sizes: the
+// kernel gets parts to cut into only where the join follows.  So a short batch is not cut in a buffer whose rows would not
+// be if all were named: 100 rows of 512 behind 15900 keys, 40 heads of 128 over 8, take 269 us.  A join behind every call
+// with offsets would make that 58 us and cost all others its launch: ragged prompts of heads of 64 33.1 -> 36.1 us, 4096
+// tokens of 8 sequences of 4000 keys 379 -> 382.
 template <int D>
 cudaError_t launch_prompt(PromptArgs p, int64_t all_tiles, int64_t most_tiles, cudaStream_t st) {
   using C = Shape<D>;
@@ -963,15 +953,14 @@ cudaError_t launch_prompt(PromptArgs p, int64_t all_tiles, int64_t most_tiles, c
     configured[dev] = true;
   }
   // tiles are cut while there are two SMs each and three key tiles
-  if ((!p.s.cu && 2 * all_tiles > p.sms) || static_cast<int64_t>(p.s.width) * p.c.page <= 2 * kBK) p.parts = nullptr;
+  if (2 * all_tiles > p.sms || static_cast<int64_t>(p.s.width) * p.c.page <= 2 * kBK) p.parts = nullptr;
   const int64_t grid = most_tiles > p.sms ? most_tiles : p.sms;
   e = launch(kv8_prompt_kernel<D>, dim3(static_cast<unsigned>(p.parts ? grid : most_tiles)), kThreads, C::kSmem, p, st);
   if (e != cudaSuccess || !p.parts) return e;
   const int64_t cut = most_tiles < p.sms / 2 ? most_tiles : p.sms / 2, parts = p.sms / cut;
   const int groups = parts >= 4 * kAtOnce ? 4 : parts >= 2 * kAtOnce ? 2 : 1;  // about eight parts each
   const int64_t rows = (p.s.cu ? static_cast<int64_t>(p.s.tokens) : p.s.each) * p.group;  // of a sequence at most
-  int64_t y = ((rows < C::kRows ? rows : C::kRows) + 31) / 32 * (D / 32);
-  if (2 * all_tiles > p.sms && y * cut > 4 * p.sms) y = 4 * p.sms / cut;
+  const int64_t y = ((rows < C::kRows ? rows : C::kRows) + 31) / 32 * (D / 32);
   return launch(kv8_join_kernel<D>, dim3(static_cast<unsigned>(cut), static_cast<unsigned>(y)), groups * kJoinGroup, 0, p, st);
 }
 

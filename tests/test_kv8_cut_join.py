@@ -21,7 +21,12 @@ class Call:
 
     def joined(self):
         """The host's decision: the keys may be cut, and the join follows."""
-        return self.width * self.page > 2 * KEYS and (self.offsets or 2 * self.most <= SMS)
+        return self.width * self.page > 2 * KEYS and 2 * self.all() <= SMS
+
+    def all(self):
+        """Row tiles at least if every token of the buffer belongs to a sequence."""
+        mine = self.tokens * self.group - (self.least - 1) * len(self.counts)
+        return self.heads * max(0, ceil(mine, self.rows)) if self.offsets else self.most
 
     def key_tiles(self, b, row0, rows):
         L, start = self.lens[b], self.lens[b] - self.counts[b]
@@ -78,7 +83,8 @@ def unwritten(call, cut, join):
     for tile, p in parts.items():
         assert len(p) == tile[4] and all(a[1] == b[0] for a, b in zip(p, p[1:])) and p[0][0] == 0
         assert p[-1][1] == call.key_tiles(tile[0], tile[2], tile[3])
-        if join and most and joins.index(tile) < min(call.most, SMS // 2):  # its CTAs take all pieces of a tile between them
+        lines = min((call.tokens if call.offsets else max(call.counts)) * call.group, call.rows)  # that the join has CTAs for
+        if join and most and joins.index(tile) < min(call.most, SMS // 2) and tile[3] <= ceil(lines, 32) * 32:
             written.add(tile)
     return [t for t in joins if t not in written]
 
@@ -114,8 +120,7 @@ def test_every_row_tile_is_written():
 
 @pytest.mark.parametrize("tokens,counts,lens", [(512, [100], [16000]), (4096, [64], [5000])])
 def test_the_model_sees_a_join_left_out_for_the_buffers_size(tokens, counts, lens):
-    """A lower bound on the tiles taken from the buffer's tokens, all of them taken for named: keys cut and never joined."""
+    """A kernel that may cut behind a host that takes all of the buffer's tokens for named: keys cut and never joined."""
     call = Call(128, 8, 5, tokens, counts, lens, ceil(lens[0], 64), 64, True)
-    least = call.heads * ceil(tokens * call.group - (call.least - 1) * len(counts), call.rows)
-    assert 2 * least > SMS and len(unwritten(call, True, False)) == 8 * ceil(counts[0] * 5, 256)
+    assert not call.joined() and len(unwritten(call, True, False)) == 8 * ceil(counts[0] * 5, 256)
     assert not unwritten(call, call.joined(), call.joined())
