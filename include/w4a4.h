@@ -515,7 +515,8 @@ size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *             be y itself (same type and stride), no other overlap with y.
  *   act     : W4A4_ACT_NONE, _RELU (max(x, 0); a NaN stays one), _SILU (x / (1 + exp(-x))),
  *             _GELU (x (1 + erf(x / sqrt 2)) / 2) or _GELU_TANH (x (1 + tanh(sqrt(2 / pi)
- *             (x + 0.044715 x^3))) / 2).
+ *             (x + 0.044715 x^3))) / 2).  erf is off by 1.5e-7 at most, the exponential by 2^-22
+ *             of itself.
  */
 #define W4A4_ACT_NONE 0
 #define W4A4_ACT_RELU 1
@@ -713,11 +714,13 @@ w4a4_status w4a4_check(w4a4_stream_t stream);
 /*
  * w4a4_debug_set_wait_limit -- a test hook for the bounded waits.  Later launches
  * of the super-tile GEMM kernel (w4a4_gemm with the expanded activation operand,
- * and w4a4_gemm_id), of mxfp4_gemm and of kv8_attention with more than 16 query rows a head
- * give up on a pipeline wait after wait_ns nanoseconds instead
- * of one second, and their producer holds its first copy back for
- * producer_delay_ns (mxfp4_gemm and kv8_attention count both in SM cycles of the top clock, 2.07
- * GHz: at a lower one they last longer).  With a delay longer than the limit every CTA gives up: the
+ * and w4a4_gemm_id), of mxfp4_gemm and of kv8_attention's kernel of many query rows give up on
+ * a pipeline wait after wait_ns nanoseconds instead of one second, and their producer holds its
+ * first copy back for producer_delay_ns (mxfp4_gemm and kv8_attention count both in SM cycles of
+ * the top clock, 2.07 GHz: at a lower one they last longer).  That kernel takes sequences of more
+ * than 32 query rows (tokens x query heads of a K/V head; 16 with heads of 256), but none of a
+ * call of heads of 64 or 128 whose tiles have few keys by the tables' width; the other has no
+ * such wait.  With a delay longer than the limit every CTA gives up: the
  * kernel returns by itself, with its output incomplete, and w4a4_check reports
  * W4A4_ERR_TIMEOUT.  (0, 0) restores the defaults.  Not synchronised with other
  * host threads; for tests only.  The wind-down waits (copies in flight, MMAs in
