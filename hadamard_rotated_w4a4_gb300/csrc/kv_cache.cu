@@ -13,11 +13,17 @@
 // numbers of 2^-64 turns, reduced by themselves, for 16 tokens once per CTA, and the CTA's heads
 // share them.
 //
-// Bound: memory and the issue of instructions for long prompts, else latency.  8192 tokens of
-// 40 + 16 heads of 128 in bf16: 47.5 us, 5.3 TB/s of q, k, v and codes (first form 98 us; 55 with
-// angles reduced in fp64); 64 sequences' next token, 20 + 8 heads of 256 in fp32, 5.7 us; one token
-// 3.7 us.  Reading 8192
-// tokens back to bf16, from L2: 12.6 us.
+// Bound: waves of CTAs and the latency of their loads for long prompts, latency else.  8192 tokens of
+// 40 + 16 heads of 128 in bf16: 47.6 us, 4.6 TB/s of q, k, v and codes (0.68 of a plain copy's; first
+// form 98 us; 55 with angles reduced in fp64).  Its 513 CTAs have 304 places, two an SM: 303 CTAs
+// take 27.8 us (4.65 TB/s), 455 take 45.9, 607 take 51.3 (5.0 TB/s); issue is active 39% of the time.
+// 64 sequences' next token, 20 + 8 heads of 256 in fp32, 5.4 us; one token 3.6 us.  Reading 8192 tokens back
+// to bf16, codes from L2: 13.0 us, 3.9 TB/s, latency: loads of 8 bytes behind the look-up of a page and a
+// scale, in 1.1 waves of CTAs.
+//
+// Sine and cosine are fp32's, 1.3 units of 2^-24 off at most (0.31 root mean square; 0.26 of 64 bits rounded).
+// 64 bits for 8192 tokens would cost more than that gives: of 8.4 million codes of k 11 and 10 differ from
+// those of 64 bits (two inputs), 11 and 9 with cosines of 64 bits.
 #include <cuda_bf16.h>
 
 #include "kv_cache.cuh"
@@ -391,7 +397,7 @@ cudaError_t launch_kv8_append(const KvCache& c, const KvSeqs& s, const KvNew& a,
   const int64_t blocks = s.cu ? s.tokens / kKvTokens + 2 * few : static_cast<int64_t>(s.batch) * ((s.each + kKvTokens - 2) / kKvTokens + 1);
   const int64_t shares = (2 * c.heads + a.q_heads + kWarps - 1) / kWarps;
   // heads over several CTAs, each with the angles for itself, up to about a CTA an SM (64 blocks of 28 heads in fp32:
-  // 64 CTAs 7.2 us, 128 5.7, 256 6.8; 513 blocks of 56 heads: 513 CTAs 47.5 us, 1026 49.5)
+  // 64 CTAs 7.0 us, 128 5.4, 256 6.4; 513 blocks of 56 heads: 513 CTAs 47.8 us, 1026 49.4)
   int64_t y = (num_sms() + blocks / 2) / blocks;
   y = y < 1 ? 1 : y < shares ? y : shares;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y));

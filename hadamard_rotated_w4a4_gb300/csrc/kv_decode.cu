@@ -2,7 +2,7 @@
 // batches, the stream of the cache's codes.
 //
 // A tile is a sequence's head of K and V with up to 16 query rows (tokens x the heads that
-// share it).  Its keys are cut in units of 128 and the units of all tiles dealt evenly to two
+// share it).  Its keys are cut in units of 64 and the units of all tiles dealt evenly to two
 // CTAs per SM, so that sequences of any lengths fill the GPU; a tile cut between CTAs is
 // joined by the last of them to arrive, its parts added in the order of their CTAs: equal
 // inputs give equal bits.
@@ -17,7 +17,7 @@
 // places by its number so that the reads meet no bank twice.
 //
 // Bound: the codes' stream, 2 D + 1/8 bytes a key and head.  8 heads of 128: 131072 keys of 4
-// sequences 189-193 us, 5.6 TB/s (0.83 of a plain copy's); 64 sequences of 5 to 8192 keys 89 us,
+// sequences 189-193 us, 5.6 TB/s (0.83 of a plain copy's); 64 sequences of 515 to 8192 keys 90 us,
 // 4.5 TB/s, the rest what a tile costs beside its keys; one token over 1000 keys 9.8 us, one
 // latency behind another (lengths, pages, codes, the join).
 #include <cuda_bf16.h>

@@ -17,10 +17,12 @@
 //
 // The running maximum is looked for, and O rescaled, only where a weight might not fit fp16.
 //
-// Measured: 4096 tokens behind 12288, 40 heads of 128 over 8: 1266 us, 950 TFLOP/s (0.50 of a
-// bf16 product's burst).  A row tile's S and O products take 1900 cycles a key tile there, 1040 by
-// themselves: shared memory, which Q K^T alone reads at 128 bytes a cycle, is shared with the
-// conversion's writes; without those 1100 us, without the exponentials 1090.  Kept out: products of
+// Measured: 4096 tokens behind 12288, 40 heads of 128 over 8: 1277 us, 940 TFLOP/s (0.50 of a
+// bf16 product's burst).  A key tile takes 3800 cycles, two row tiles of 1900.  By themselves their products
+// would take 2080, and shared memory 2500 at 128 bytes a cycle (Q K^T reads 128 KB, P V 64, the conversion
+// reads and writes 128).  Neither fills it: a row tile's softmax, P V and next Q K^T stand behind one another,
+// with one S each.  Without the conversion's writes 1100 us, without the exponentials 1090, without both
+// 1002.  Kept out: products of
 // 64 keys with two S a row tile (1399 us: Q read twice as often), two threads a row (1277), codes
 // by plain loads into registers (1484 at best).  8 drafted tokens of 8 sequences of up to 6000 keys,
 // heads of 256: 36 us; prompts of 7 sequences, heads of 64, window 500: 33 us; both are set-up,
