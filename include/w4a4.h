@@ -678,8 +678,9 @@ w4a4_status kv8_read(const w4a4_kv8* cache, const w4a4_kv8_seqs* seqs, void* k, 
  *   ws: optional device workspace (kv8_attention_workspace_bytes or more, 16-byte aligned,
  *       its first MiB zero before its first use; a smaller one is W4A4_ERR_WORKSPACE; it may
  *       be one that a product uses as well).  With it long sequences are cut over the SMs
- *       and joined; without it few sequences leave SMs idle.  Every call leaves it as it
- *       needs to find it.  Calls that share one must not overlap on the GPU.
+ *       and joined; without it few sequences leave SMs idle.  (More than a few query rows: as
+ *       far as `tokens` says that they are few, whatever cu names of them.)  Every call leaves
+ *       it as it needs to find it.  Calls that share one must not overlap on the GPU.
  * batch <= 2048 (W4A4_ERR_UNSUPPORTED above).  The order of every sum is fixed by the call's
  * numbers (tokens, heads, the table's width, lengths) on a given device: equal inputs give equal
  * bits.
